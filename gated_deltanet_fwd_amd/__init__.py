@@ -14,6 +14,13 @@ allocates are allocated on its launch stream. The functions carry the C names:
     gdn_status(problem, op, workspace)            -> int (synchronises the stream)
     gdn_conv_fwd(conv_problem, x, weight, bias, cu, ...)      -> list of outputs (one per group)
     gdn_conv_bwd(conv_problem, x, weight, bias, cu, dys, ...) -> dict dx, dweight, dbias
+    gdn_recurrent(recurrent_problem, q, k, v, g, beta, states, slot_in, slot_out, ...) -> o
+    gdn_conv_step(conv_step_problem, x, weight, bias, windows, slot_in, slot_out, ...) -> list of outputs
+    gdn_rope_frequencies(rotary_dim, ...)         -> (int64 tensor on the CPU, magnitude)
+    gdn_qk_rope_fwd(rope_problem, q, k, positions, freqs, ...) -> (q_out, k_out)
+    gdn_qk_rope_bwd(rope_problem, q, k, positions, freqs, dq_out, dk_out, ...) -> dict of gradients
+
+The last five check their tensors (shape, type, layout, device) before the call and raise GdnError.
 
 A missing or unloadable library raises ImportError-like errors at first use; there is no other
 code path.
@@ -38,7 +45,10 @@ ABI_VERSION = 2
 
 EXPORTS = ("gdn_saved_bytes", "gdn_workspace_bytes", "gdn_fwd", "gdn_fwd_recompute", "gdn_bwd", "gdn_status",
            "gdn_fwd_noalloc", "gdn_conv_workspace_bytes", "gdn_conv_fwd", "gdn_conv_bwd", "gdn_last_error",
-           "gdn_abi_version")
+           "gdn_abi_version", "gdn_recurrent", "gdn_conv_step", "gdn_rope_frequencies", "gdn_qk_rope_workspace_bytes",
+           "gdn_qk_rope_fwd", "gdn_qk_rope_bwd")
+NORMS = {"none": 0, "l2": 1, "rms": 2}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
 
 
 class GdnError(RuntimeError):
@@ -81,6 +91,75 @@ class _ConvProblem(ctypes.Structure):
     ]
 
 
+class _RecurrentProblem(ctypes.Structure):
+    _fields_ = [
+        ("n_seqs", ctypes.c_int32),
+        ("h_qk", ctypes.c_int32),
+        ("h_v", ctypes.c_int32),
+        ("d", ctypes.c_int32),
+        ("n_tokens", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("l2norm_qk", ctypes.c_int32),
+        ("n_slots", ctypes.c_int32),
+        ("reserved0", ctypes.c_int32),
+        ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+        ("cu_seqlens_host", ctypes.POINTER(ctypes.c_int32)),
+    ]
+
+
+class _ConvStepProblem(ctypes.Structure):
+    _fields_ = [
+        ("n_seqs", ctypes.c_int32),
+        ("channels", ctypes.c_int32),
+        ("n_tokens", ctypes.c_int64),
+        ("width", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("silu", ctypes.c_int32),
+        ("n_groups", ctypes.c_int32),
+        ("group_channels", ctypes.c_int32 * 4),
+        ("n_slots", ctypes.c_int32),
+        ("reserved0", ctypes.c_int32),
+        ("x_stride", ctypes.c_int64),
+        ("cu_seqlens_host", ctypes.POINTER(ctypes.c_int32)),
+    ]
+
+
+class _QkRopeProblem(ctypes.Structure):
+    _fields_ = [
+        ("n_tokens", ctypes.c_int64),
+        ("h_q", ctypes.c_int32),
+        ("h_k", ctypes.c_int32),
+        ("d", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("norm", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("magnitude", ctypes.c_float),
+        ("reserved0", ctypes.c_int32),
+        ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("qo_stride", ctypes.c_int64),
+        ("ko_stride", ctypes.c_int64),
+        ("dq_stride", ctypes.c_int64),
+        ("dk_stride", ctypes.c_int64),
+    ]
+
+
+class _RopeScaling(ctypes.Structure):
+    _fields_ = [
+        ("kind", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32),
+        ("base", ctypes.c_double),
+        ("factor", ctypes.c_double),
+        ("original_length", ctypes.c_double),
+        ("fast", ctypes.c_double),
+        ("slow", ctypes.c_double),
+    ]
+
+
 _lib = None
 
 
@@ -115,6 +194,19 @@ def load_library(path: str = LIB_PATH):
     lib.gdn_conv_fwd.restype = I
     lib.gdn_conv_bwd.argtypes = [cp, P, P, P, P, P, P, P, P, P, Z, P]
     lib.gdn_conv_bwd.restype = I
+    lib.gdn_recurrent.argtypes = [ctypes.POINTER(_RecurrentProblem)] + [P] * 12
+    lib.gdn_recurrent.restype = I
+    lib.gdn_conv_step.argtypes = [ctypes.POINTER(_ConvStepProblem)] + [P] * 10
+    lib.gdn_conv_step.restype = I
+    lib.gdn_rope_frequencies.argtypes = [ctypes.POINTER(_RopeScaling), P, ctypes.POINTER(ctypes.c_float)]
+    lib.gdn_rope_frequencies.restype = I
+    rp = ctypes.POINTER(_QkRopeProblem)
+    lib.gdn_qk_rope_workspace_bytes.argtypes = [rp]
+    lib.gdn_qk_rope_workspace_bytes.restype = Z
+    lib.gdn_qk_rope_fwd.argtypes = [rp] + [P] * 9
+    lib.gdn_qk_rope_fwd.restype = I
+    lib.gdn_qk_rope_bwd.argtypes = [rp] + [P] * 13 + [Z, P]
+    lib.gdn_qk_rope_bwd.restype = I
     lib.gdn_last_error.argtypes = []
     lib.gdn_last_error.restype = ctypes.c_char_p
     lib.gdn_abi_version.argtypes = []
@@ -387,3 +479,250 @@ def gdn_conv_bwd(p: ConvProblem, x, weight, bias, cu_seqlens, dys, dx=None, dwei
                             _ptr(dweight), _ptr(dbias), _ptr(workspace), workspace.numel(),
                             ctypes.c_void_p(s.cuda_stream)))
     return dict(dx=dx, dweight=dweight, dbias=dbias)
+
+
+# ------------------------------------------------------------------- serving steps, q/k rotation
+
+
+def _io_dtype(dtype) -> int:
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise GdnError(GDN_EUNSUPPORTED, "unsupported dtype %s" % (dtype,))
+    return DTYPE_BF16 if dtype == torch.bfloat16 else DTYPE_F32
+
+
+def _expect(t, name: str, shape, dtype, device, strided: bool = False):
+    """The tensor's address. Raises unless `t` has this shape, type and device and is contiguous
+    (`strided`: but for the distance between its first dimension's entries)."""
+    if t.shape != shape:
+        raise GdnError(GDN_EINVAL, "%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if t.dtype != dtype:
+        raise GdnError(GDN_EINVAL, "%s has type %s, expected %s" % (name, t.dtype, dtype))
+    if t.device != device:
+        raise GdnError(GDN_EINVAL, "%s is on %s, expected %s" % (name, t.device, device))
+    if not t.is_contiguous() and not (strided and t.numel() and t[0].is_contiguous() and t.stride(0) >= t[0].numel()):
+        raise GdnError(GDN_EINVAL, "%s is not contiguous%s" % (name, " within a token" if strided else ""))
+    return t.data_ptr()
+
+
+def _token_stride(t) -> int:
+    """Elements between the tokens of a tensor that _expect let pass (0: contiguous)."""
+    return 0 if t.is_contiguous() else t.stride(0)
+
+
+def _given(t, name: str, shape, dtype, device):
+    return None if t is None else _expect(t, name, shape, dtype, device)
+
+
+class _On:
+    """The launch stream's handle; as a context, the stream that buffers are allocated on."""
+
+    def __init__(self, stream, device):
+        self.stream = None if stream is None else _torch_stream(stream, device)
+        self.handle = (self.stream or torch.cuda.current_stream(device)).cuda_stream
+
+    def empty(self, shape, dtype, device):
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=device)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _step_lengths(cu_seqlens_host, n_seqs):
+    """(host copy of cu_seqlens or None, its pointer or None, token count)."""
+    if cu_seqlens_host is None:
+        return None, None, int(n_seqs)
+    cu = np.ascontiguousarray(np.asarray(cu_seqlens_host, dtype=np.int32))
+    if cu.shape != (n_seqs + 1,):
+        raise GdnError(GDN_EINVAL, "cu_seqlens_host has shape %s, expected (%d,)" % (cu.shape, n_seqs + 1))
+    return cu, cu.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)), int(cu[-1])
+
+
+class RecurrentProblem:
+    """A gdn_recurrent_problem descriptor: `n_seqs` sequences on a cache of `n_slots` states, one
+    token each, or as many as the host copy of cu_seqlens says."""
+
+    def __init__(self, n_seqs: int, h_qk: int, h_v: int, d: int, n_slots: int, cu_seqlens_host=None,
+                 dtype=torch.bfloat16, l2norm: bool = True):
+        self.cu, ptr, tokens = _step_lengths(cu_seqlens_host, n_seqs)
+        self.dtype = dtype
+        self.st = _RecurrentProblem(n_seqs=int(n_seqs), h_qk=int(h_qk), h_v=int(h_v), d=int(d), n_tokens=tokens,
+                                    dtype=_io_dtype(dtype),
+                                    l2norm_qk=int(bool(l2norm)), n_slots=int(n_slots), cu_seqlens_host=ptr)
+        self.shapes = dict(q=(tokens, int(h_qk), int(d)), v=(tokens, int(h_v), int(d)), g=(tokens, int(h_v)),
+                           states=(int(n_slots), int(h_v), int(d), int(d)), seqs=(int(n_seqs),), tok=(tokens,),
+                           cu=(int(n_seqs) + 1,))
+
+    def ref(self):
+        return ctypes.byref(self.st)
+
+
+def gdn_recurrent(p: RecurrentProblem, q, k, v, g, beta, states, slot_in, slot_out, slot_tok=None, cu_seqlens=None,
+                  o=None, stream=None):
+    """One serving step of the recurrent rule: runs every sequence's tokens from states[slot_in] (-1:
+    zero), leaves its state in states[slot_out] (-1: nowhere) and, with slot_tok, the state after each
+    token in states[slot_tok]. q, k and v may be parts of one row (a token's heads contiguous).
+    Returns o; `states` is updated in place."""
+    lib, st, sh, dev, f32, i32 = load_library(), p.st, p.shapes, v.device, torch.float32, torch.int32
+    on = _On(stream, dev)
+    if o is None:
+        o = on.empty(sh["v"], p.dtype, dev)
+    args = (_expect(q, "q", sh["q"], p.dtype, dev, True), _expect(k, "k", sh["q"], p.dtype, dev, True),
+            _expect(v, "v", sh["v"], p.dtype, dev, True), _expect(g, "g", sh["g"], f32, dev),
+            _expect(beta, "beta", sh["g"], f32, dev), _given(cu_seqlens, "cu_seqlens", sh["cu"], i32, dev),
+            _expect(slot_in, "slot_in", sh["seqs"], i32, dev), _expect(slot_out, "slot_out", sh["seqs"], i32, dev),
+            _given(slot_tok, "slot_tok", sh["tok"], i32, dev), _expect(states, "states", sh["states"], f32, dev),
+            _expect(o, "o", sh["v"], p.dtype, dev))
+    st.q_stride, st.k_stride, st.v_stride = _token_stride(q), _token_stride(k), _token_stride(v)
+    _check(lib.gdn_recurrent(p.ref(), *args, on.handle))
+    return o
+
+
+class ConvStepProblem:
+    """A gdn_conv_step_problem descriptor: the conv1d + SiLU front-end on `n_seqs` sequences with a
+    cache of `n_slots` windows, one token each, or as many as the host copy of cu_seqlens says."""
+
+    def __init__(self, n_seqs: int, group_channels, n_slots: int, cu_seqlens_host=None, width: int = 4,
+                 dtype=torch.bfloat16, silu: bool = True):
+        self.cu, ptr, tokens = _step_lengths(cu_seqlens_host, n_seqs)
+        self.dtype = dtype
+        self.groups = [int(c) for c in group_channels]
+        if not 1 <= len(self.groups) <= 4:
+            raise GdnError(GDN_EINVAL, "n_groups must be 1..4 (got %d)" % len(self.groups))
+        channels, width = sum(self.groups), int(width)
+        self.st = _ConvStepProblem(n_seqs=int(n_seqs), channels=channels, n_tokens=tokens, width=width,
+                                   dtype=_io_dtype(dtype), silu=int(bool(silu)),
+                                   n_groups=len(self.groups),
+                                   group_channels=(ctypes.c_int32 * 4)(*self.groups),
+                                   n_slots=int(n_slots), cu_seqlens_host=ptr)
+        self.shapes = dict(x=(tokens, channels), weight=(channels, width), bias=(channels,),
+                           windows=(int(n_slots), width - 1, channels), seqs=(int(n_seqs),), tok=(tokens,),
+                           cu=(int(n_seqs) + 1,), outs=[(tokens, c) for c in self.groups])
+
+    def ref(self):
+        return ctypes.byref(self.st)
+
+
+def gdn_conv_step(p: ConvStepProblem, x, weight, bias, windows, slot_in, slot_out, slot_tok=None, cu_seqlens=None,
+                  outs=None, stream=None):
+    """One serving step of the conv front-end on cached windows (slots as in gdn_recurrent). Returns
+    the list of outputs, [T, group_channels[g]]; `windows` is updated in place (None at width 1)."""
+    lib, st, sh, dev, f32, i32 = load_library(), p.st, p.shapes, x.device, torch.float32, torch.int32
+    on = _On(stream, dev)
+    if outs is None:
+        outs = [on.empty(s, p.dtype, dev) for s in sh["outs"]]
+    elif len(outs) != len(sh["outs"]):
+        raise GdnError(GDN_EINVAL, "outs has %d tensors, expected %d" % (len(outs), len(sh["outs"])))
+    ys = (ctypes.c_void_p * 4)(*[_expect(t, "outs", s, p.dtype, dev) for t, s in zip(outs, sh["outs"])])
+    args = (_expect(x, "x", sh["x"], p.dtype, dev, True), _expect(weight, "weight", sh["weight"], f32, dev),
+            _given(bias, "bias", sh["bias"], f32, dev), _given(cu_seqlens, "cu_seqlens", sh["cu"], i32, dev),
+            _expect(slot_in, "slot_in", sh["seqs"], i32, dev), _expect(slot_out, "slot_out", sh["seqs"], i32, dev),
+            _given(slot_tok, "slot_tok", sh["tok"], i32, dev),
+            _given(windows, "windows", sh["windows"], p.dtype, dev))
+    st.x_stride = _token_stride(x)
+    _check(lib.gdn_conv_step(p.ref(), *args, ys, on.handle))
+    return outs
+
+
+def gdn_rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                         original_length: float = 0.0, fast: float = 32.0, slow: float = 1.0):
+    """Frequencies of the rotation as 64-bit fractions of a turn (an int64 tensor of rotary_dim / 2 on
+    the CPU: move it to the GPU once) and the magnitude. `scaling`: "none", "linear", "ntk", "yarn" or
+    "bands" (see gdn.h)."""
+    if scaling not in ROPE_SCALINGS:
+        raise GdnError(GDN_EINVAL, "unknown scaling %r" % (scaling,))
+    s = _RopeScaling(kind=ROPE_SCALINGS[scaling], rotary_dim=int(rotary_dim), base=float(base), factor=float(factor),
+                     original_length=float(original_length), fast=float(fast), slow=float(slow))
+    out = torch.zeros(max(int(rotary_dim) // 2, 1), dtype=torch.int64)
+    m = ctypes.c_float()
+    _check(load_library().gdn_rope_frequencies(ctypes.byref(s), out.data_ptr(), ctypes.byref(m)))
+    return out, float(m.value)
+
+
+class QkRopeProblem:
+    """A gdn_qk_rope_problem descriptor: norms ("rms", "l2" or "none") of h_q q heads and h_k k heads
+    of n_tokens tokens and the rotation of each head's first rotary_dim values (None: all)."""
+
+    def __init__(self, n_tokens: int, h_q: int, h_k: int, d: int, dtype=torch.bfloat16, norm: str = "rms",
+                 rotary_dim: Optional[int] = None, interleaved: bool = False, eps: float = 1e-6,
+                 magnitude: float = 1.0):
+        if norm not in NORMS:
+            raise GdnError(GDN_EINVAL, "unknown norm %r" % (norm,))
+        rotary = int(d if rotary_dim is None else rotary_dim)
+        self.dtype = dtype
+        self.st = _QkRopeProblem(n_tokens=int(n_tokens), h_q=int(h_q), h_k=int(h_k), d=int(d),
+                                 dtype=_io_dtype(dtype), norm=NORMS[norm],
+                                 rotary_dim=rotary, interleaved=int(bool(interleaved)), eps=float(eps),
+                                 magnitude=float(magnitude))
+        self.shapes = dict(q=(int(n_tokens), int(h_q), int(d)), k=(int(n_tokens), int(h_k), int(d)),
+                           tok=(int(n_tokens),), freqs=(rotary // 2,), w=(int(d),))
+        self.workspace_bytes = None  # of the backward, asked for once
+
+    def ref(self):
+        return ctypes.byref(self.st)
+
+
+def gdn_qk_rope_workspace_bytes(p: QkRopeProblem) -> int:
+    if p.workspace_bytes is None:
+        n = load_library().gdn_qk_rope_workspace_bytes(p.ref())
+        if n == 0:
+            raise GdnError(GDN_EINVAL, load_library().gdn_last_error().decode())
+        p.workspace_bytes = int(n)
+    return p.workspace_bytes
+
+
+def _rope_common(p, positions, freqs, q_weight, k_weight, dev):
+    sh = p.shapes
+    return (_given(positions, "positions", sh["tok"], torch.int32, dev),
+            _given(freqs, "freqs", sh["freqs"], torch.int64, dev),
+            _given(q_weight, "q_weight", sh["w"], torch.float32, dev),
+            _given(k_weight, "k_weight", sh["w"], torch.float32, dev))
+
+
+def gdn_qk_rope_fwd(p: QkRopeProblem, q, k, positions, freqs, q_weight=None, k_weight=None, q_out=None, k_out=None,
+                    stream=None):
+    """Norms and rotation of q [T, h_q, d] and k [T, h_k, d] (None when h_k = 0), which may be parts of
+    one row, with positions int32 [T] and the frequencies of gdn_rope_frequencies on the device.
+    Returns (q_out, k_out); they may be given, also as q and k themselves."""
+    lib, st, sh, dev = load_library(), p.st, p.shapes, q.device
+    on = _On(stream, dev)
+    if q_out is None:
+        q_out = on.empty(sh["q"], p.dtype, dev)
+    if k_out is None and k is not None:
+        k_out = on.empty(sh["k"], p.dtype, dev)
+    args = [None if t is None else _expect(t, name, sh[name[0]], p.dtype, dev, True)
+            for t, name in ((q, "q"), (k, "k"), (q_out, "q_out"), (k_out, "k_out"))]
+    st.q_stride, st.qo_stride = _token_stride(q), _token_stride(q_out)
+    st.k_stride, st.ko_stride = (0, 0) if k is None else (_token_stride(k), _token_stride(k_out))
+    _check(lib.gdn_qk_rope_fwd(p.ref(), *args[:2], *_rope_common(p, positions, freqs, q_weight, k_weight, dev),
+                               *args[2:], on.handle))
+    return q_out, k_out
+
+
+def gdn_qk_rope_bwd(p: QkRopeProblem, q, k, positions, freqs, dq_out, dk_out, q_weight=None, k_weight=None, grads=None,
+                    workspace=None, stream=None) -> Dict[str, torch.Tensor]:
+    """Backward of gdn_qk_rope_fwd (q and k may be None with norm "none"): returns dict dq, dk,
+    dq_weight, dk_weight (None without the weight). `grads` may name any of the buffers."""
+    lib, st, sh, dev, f32 = load_library(), p.st, p.shapes, dq_out.device, torch.float32
+    on = _On(stream, dev)
+    grads = dict(grads or {})
+    for name, like, shape in (("dq", dq_out, sh["q"]), ("dk", dk_out, sh["k"])):
+        if grads.get(name) is None:
+            grads[name] = None if like is None else on.empty(shape, p.dtype, dev)
+    for name, w in (("dq_weight", q_weight), ("dk_weight", k_weight)):
+        if w is None:
+            grads[name] = None
+        elif grads.get(name) is None:
+            grads[name] = on.empty(sh["w"], f32, dev)
+    if workspace is None and (q_weight is not None or k_weight is not None):
+        workspace = on.empty((gdn_qk_rope_workspace_bytes(p),), torch.uint8, dev)
+    ts = dict(q=q, k=k, dq_out=dq_out, dk_out=dk_out, dq=grads["dq"], dk=grads["dk"])
+    ptr = {n: None if t is None else _expect(t, n, sh["q" if "q" in n else "k"], p.dtype, dev, True)
+           for n, t in ts.items()}
+    st.q_stride, st.k_stride, st.qo_stride, st.ko_stride, st.dq_stride, st.dk_stride = (
+        0 if t is None else _token_stride(t) for t in ts.values())
+    _check(lib.gdn_qk_rope_bwd(p.ref(), ptr["q"], ptr["k"], *_rope_common(p, positions, freqs, q_weight, k_weight, dev),
+                               ptr["dq_out"], ptr["dk_out"], ptr["dq"], ptr["dk"],
+                               _given(grads["dq_weight"], "dq_weight", sh["w"], f32, dev),
+                               _given(grads["dk_weight"], "dk_weight", sh["w"], f32, dev), _ptr(workspace),
+                               0 if workspace is None else workspace.numel(), on.handle))
+    return grads

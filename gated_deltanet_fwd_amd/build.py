@@ -14,7 +14,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libgdn.so")
 BUILD = os.path.join(HERE, "_build")
-SOURCES = ["gdn_fwd.hip", "gdn_bwd.hip", "gdn_api.cpp", "gdn_static.hip", "gdn_conv.hip"]
+SOURCES = ["gdn_fwd.hip", "gdn_bwd.hip", "gdn_api.cpp", "gdn_static.hip", "gdn_conv.hip", "gdn_conv_step.hip",
+           "gdn_recurrent.hip", "gdn_rope.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950",

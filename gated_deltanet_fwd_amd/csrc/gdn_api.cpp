@@ -8,6 +8,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -1010,6 +1011,335 @@ int gdn_conv_bwd(const gdn_conv_problem* p, const void* x, const float* weight, 
   a.db = dbias;
   a.part = (float*)workspace;
   LAUNCH("gdn_conv_bwd", gdn::launch_conv_bwd(a, p->dtype, stream));
+  g_err.clear();
+  return GDN_OK;
+}
+
+} // extern "C"
+
+// ---------------------------------------------------------------------------------------------
+// Serving steps on cached states and windows; norms of the q and k heads with the rotation
+
+namespace {
+
+// Sequences of a serving step: host cu_seqlens, or one token a sequence.
+int check_steps(int n_seqs, int64_t n_tokens, int n_slots, int reserved, const int32_t* cu) {
+  if (n_seqs < 1) return fail(GDN_EINVAL, "n_seqs must be >= 1 (got %d)", n_seqs);
+  if (n_slots < 1) return fail(GDN_EINVAL, "n_slots must be >= 1 (got %d)", n_slots);
+  if (reserved != 0) return fail(GDN_EINVAL, "reserved0 must be 0");
+  if (!cu) {
+    if (n_tokens != n_seqs)
+      return fail(GDN_EINVAL, "without cu_seqlens n_tokens (%lld) must equal n_seqs (%d)", (long long)n_tokens, n_seqs);
+    return GDN_OK;
+  }
+  if (cu[0] != 0) return fail(GDN_EINVAL, "cu_seqlens[0] must be 0");
+  for (int n = 0; n < n_seqs; ++n)
+    if (cu[n + 1] < cu[n]) return fail(GDN_EINVAL, "cu_seqlens decreases at %d", n);
+  if ((int64_t)cu[n_seqs] != n_tokens)
+    return fail(GDN_EINVAL, "cu_seqlens[N] = %d but n_tokens = %lld", cu[n_seqs], (long long)n_tokens);
+  return GDN_OK;
+}
+
+int check_step_arrays(const int32_t* cu_host, const int32_t* cu, const int32_t* slot_in, const int32_t* slot_out,
+                      const int32_t* slot_tok) {
+  if ((cu != nullptr) != (cu_host != nullptr))
+    return fail(GDN_EINVAL, "cu_seqlens and cu_seqlens_host must be given together");
+  if (cu) CHECK(check_ptr(cu, "cu_seqlens"));
+  CHECK(check_ptr(slot_in, "slot_in"));
+  CHECK(check_ptr(slot_out, "slot_out"));
+  if (slot_tok && !aligned16(slot_tok)) return fail(GDN_EINVAL, "slot_tok is not 16-byte aligned");
+  return GDN_OK;
+}
+
+// Elements between tokens: `given`, or the contiguous `row` for 0; rows stay 16-byte aligned and
+// do not overlap.
+int token_stride(int64_t given, int64_t row, int dtype, const char* name, int64_t* out) {
+  *out = given == 0 ? row : given;
+  if (*out < row) return fail(GDN_EINVAL, "%s (%lld) is below a token's %lld elements", name, (long long)given, (long long)row);
+  if (*out % (dtype == GDN_DTYPE_BF16 ? 8 : 4) != 0)
+    return fail(GDN_EINVAL, "%s (%lld) does not keep rows 16-byte aligned", name, (long long)*out);
+  return GDN_OK;
+}
+
+} // namespace
+
+extern "C" {
+
+int gdn_recurrent(const gdn_recurrent_problem* p, const void* q, const void* k, const void* v, const float* g,
+                  const float* beta, const int32_t* cu_seqlens, const int32_t* slot_in, const int32_t* slot_out,
+                  const int32_t* slot_tok, float* states, void* o, void* stream) {
+  if (!p) return fail(GDN_EINVAL, "recurrent problem descriptor is NULL");
+  if (p->h_qk < 1 || p->h_v < 1) return fail(GDN_EINVAL, "head counts must be >= 1");
+  if (p->h_v % p->h_qk != 0) return fail(GDN_EINVAL, "h_v (%d) must be a multiple of h_qk (%d)", p->h_v, p->h_qk);
+  if (p->d != 64 && p->d != 128) return fail(GDN_EUNSUPPORTED, "d must be 64 or 128 (got %d)", p->d);
+  if (p->dtype != GDN_DTYPE_BF16 && p->dtype != GDN_DTYPE_F32)
+    return fail(GDN_EUNSUPPORTED, "unsupported dtype %d", p->dtype);
+  CHECK(check_steps(p->n_seqs, p->n_tokens, p->n_slots, p->reserved0, p->cu_seqlens_host));
+  if ((int64_t)p->n_seqs * p->h_v > (int64_t)0x0fffffff) return fail(GDN_EINVAL, "too many sequences x heads");
+  gdn::RecurrentArgs a;
+  std::memset(&a, 0, sizeof a);
+  CHECK(token_stride(p->q_stride, (int64_t)p->h_qk * p->d, p->dtype, "q_stride", &a.qs));
+  CHECK(token_stride(p->k_stride, (int64_t)p->h_qk * p->d, p->dtype, "k_stride", &a.ks));
+  CHECK(token_stride(p->v_stride, (int64_t)p->h_v * p->d, p->dtype, "v_stride", &a.vs));
+  const int64_t T = p->n_tokens;
+  CHECK(check_tok(q, "q", T));
+  CHECK(check_tok(k, "k", T));
+  CHECK(check_tok(v, "v", T));
+  CHECK(check_tok(g, "g", T));
+  CHECK(check_tok(beta, "beta", T));
+  CHECK(check_tok(o, "o", T));
+  CHECK(check_ptr(states, "states"));
+  CHECK(check_step_arrays(p->cu_seqlens_host, cu_seqlens, slot_in, slot_out, slot_tok));
+  a.T = T;
+  a.N = p->n_seqs;
+  a.H = p->h_qk;
+  a.HV = p->h_v;
+  a.G = p->h_v / p->h_qk;
+  a.D = p->d;
+  a.l2norm = p->l2norm_qk ? 1 : 0;
+  a.n_slots = p->n_slots;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.g = g;
+  a.beta = beta;
+  a.cu = cu_seqlens;
+  a.slot_in = slot_in;
+  a.slot_out = slot_out;
+  a.slot_tok = slot_tok;
+  a.states = states;
+  a.o = o;
+  LAUNCH("gdn_recurrent", gdn::launch_recurrent(a, p->dtype, stream));
+  g_err.clear();
+  return GDN_OK;
+}
+
+int gdn_conv_step(const gdn_conv_step_problem* p, const void* x, const float* weight, const float* bias,
+                  const int32_t* cu_seqlens, const int32_t* slot_in, const int32_t* slot_out,
+                  const int32_t* slot_tok, void* windows, void* const* y, void* stream) {
+  if (!p) return fail(GDN_EINVAL, "conv step problem descriptor is NULL");
+  CHECK(check_steps(p->n_seqs, p->n_tokens, p->n_slots, p->reserved0, p->cu_seqlens_host));
+  // the front-end's own checks, on one document of the same channels
+  gdn_conv_problem c;
+  std::memset(&c, 0, sizeof c);
+  const int32_t none[2] = {0, 0};
+  c.n_seqs = 1;
+  c.channels = p->channels;
+  c.width = p->width;
+  c.dtype = p->dtype;
+  c.silu = p->silu;
+  c.n_groups = p->n_groups;
+  std::memcpy(c.group_channels, p->group_channels, sizeof c.group_channels);
+  c.cu_seqlens_host = none;
+  CHECK(check_conv(&c));
+  gdn::ConvArgs base;
+  conv_args(base, &c, x, weight, bias, nullptr);
+  gdn::ConvStepArgs a;
+  std::memset(&a, 0, sizeof a);
+  CHECK(token_stride(p->x_stride, p->channels, p->dtype, "x_stride", &a.xs));
+  const int64_t T = p->n_tokens;
+  CHECK(check_tok(x, "x", T));
+  CHECK(check_ptr(weight, "weight"));
+  if (bias && !aligned16(bias)) return fail(GDN_EINVAL, "bias is not 16-byte aligned");
+  if (p->width > 1) CHECK(check_ptr(windows, "windows"));
+  CHECK(check_step_arrays(p->cu_seqlens_host, cu_seqlens, slot_in, slot_out, slot_tok));
+  if (!y) return fail(GDN_EINVAL, "y (the array of output pointers) is NULL");
+  for (int g = 0; g < p->n_groups; ++g) {
+    CHECK(check_tok(y[g], "y[g]", T));
+    a.y[g] = y[g];
+  }
+  a.T = T;
+  a.C = base.C;
+  a.W = base.W;
+  a.N = p->n_seqs;
+  a.silu = base.silu;
+  a.n_groups = base.n_groups;
+  a.n_slots = p->n_slots;
+  std::memcpy(a.goff, base.goff, sizeof a.goff);
+  a.x = x;
+  a.w = weight;
+  a.b = bias;
+  a.cu = cu_seqlens;
+  a.slot_in = slot_in;
+  a.slot_out = slot_out;
+  a.slot_tok = slot_tok;
+  a.win = windows;
+  LAUNCH("gdn_conv_step", gdn::launch_conv_step(a, p->dtype, stream));
+  g_err.clear();
+  return GDN_OK;
+}
+
+int gdn_rope_frequencies(const gdn_rope_scaling* s, uint64_t* freqs_host, float* magnitude) {
+  if (!s) return fail(GDN_EINVAL, "scaling descriptor is NULL");
+  if (!freqs_host) return fail(GDN_EINVAL, "freqs_host is NULL");
+  if (!magnitude) return fail(GDN_EINVAL, "magnitude is NULL");
+  if (s->kind < GDN_ROPE_PLAIN || s->kind > GDN_ROPE_BANDS) return fail(GDN_EINVAL, "unknown scaling kind %d", s->kind);
+  const int r = s->rotary_dim;
+  if (r < 2 || r % 2 != 0) return fail(GDN_EINVAL, "rotary_dim must be even and >= 2 (got %d)", r);
+  if (!(s->base > 1.0) || !std::isfinite(s->base)) return fail(GDN_EINVAL, "base must be above 1 (got %g)", s->base);
+  if (s->kind != GDN_ROPE_PLAIN && (!(s->factor > 0.0) || !std::isfinite(s->factor)))
+    return fail(GDN_EINVAL, "factor must be above 0 (got %g)", s->factor);
+  if (s->kind == GDN_ROPE_NTK && r == 2) return fail(GDN_EINVAL, "this scaling needs a rotary_dim above 2");
+  const bool blend = s->kind == GDN_ROPE_YARN || s->kind == GDN_ROPE_BANDS;
+  if (blend && (!(s->original_length > 0.0) || !std::isfinite(s->original_length)))
+    return fail(GDN_EINVAL, "original_length must be above 0 (got %g)", s->original_length);
+  if (blend && (!(s->slow > 0.0) || !(s->fast > s->slow) || !std::isfinite(s->fast)))
+    return fail(GDN_EINVAL, "fast (%g) must be above slow (%g), and slow above 0", s->fast, s->slow);
+  const double two_pi = 6.283185307179586476925286766559;
+  const double base = s->kind == GDN_ROPE_NTK ? s->base * std::pow(s->factor, (double)r / (r - 2)) : s->base;
+  double lo = 0.0, hi = 0.0;
+  if (s->kind == GDN_ROPE_YARN) { // indices that make `fast` and `slow` turns, rounded outwards
+    const auto index = [&](double turns) {
+      return r * std::log(s->original_length / (turns * two_pi)) / (2.0 * std::log(base));
+    };
+    lo = std::max(std::floor(index(s->fast)), 0.0);
+    hi = std::min(std::ceil(index(s->slow)), (double)(r - 1));
+    if (hi - lo < 0.001) hi = lo + 0.001;
+  }
+  for (int i = 0; i < r / 2; ++i) {
+    long double f = std::pow((long double)base, -2.0L * i / r);
+    if (s->kind == GDN_ROPE_LINEAR) f /= s->factor;
+    if (blend) {
+      long double ramp = s->kind == GDN_ROPE_YARN
+                             ? (i - (long double)lo) / (hi - lo)
+                             : 1.0L - (s->original_length * f / two_pi - s->slow) / (s->fast - s->slow);
+      ramp = std::min(std::max(ramp, 0.0L), 1.0L);
+      f = f * (1.0L - ramp) + f / s->factor * ramp;
+    }
+    f /= 6.283185307179586476925286766559L; // turns per position; whole turns do not matter
+    f -= std::floor(f);
+    const long double scaled = std::round(f * 18446744073709551616.0L);
+    freqs_host[i] = scaled >= 18446744073709551616.0L ? 0 : (uint64_t)scaled;
+  }
+  *magnitude = s->kind == GDN_ROPE_YARN && s->factor > 1.0 ? (float)(0.1 * std::log(s->factor) + 1.0) : 1.0f;
+  g_err.clear();
+  return GDN_OK;
+}
+
+} // extern "C"
+
+namespace {
+
+int check_rope(const gdn_qk_rope_problem* p) {
+  if (!p) return fail(GDN_EINVAL, "q/k rope problem descriptor is NULL");
+  if (p->n_tokens < 0) return fail(GDN_EINVAL, "n_tokens must be >= 0");
+  if (p->h_q < 1 || p->h_k < 0 || p->h_q > 16384 || p->h_k > 16384)
+    return fail(GDN_EINVAL, "h_q must be 1..16384 and h_k 0..16384 (got %d, %d)", p->h_q, p->h_k);
+  if (p->d < 8 || p->d > 256 || p->d % 8 != 0)
+    return fail(GDN_EUNSUPPORTED, "d must be a multiple of 8, 8..256 (got %d)", p->d);
+  if (p->dtype != GDN_DTYPE_BF16 && p->dtype != GDN_DTYPE_F32)
+    return fail(GDN_EUNSUPPORTED, "unsupported dtype %d", p->dtype);
+  if (p->norm != GDN_NORM_NONE && p->norm != GDN_NORM_L2 && p->norm != GDN_NORM_RMS)
+    return fail(GDN_EINVAL, "norm must be none (0), l2 (1) or rms (2)");
+  if (p->rotary_dim < 0 || p->rotary_dim > p->d || p->rotary_dim % 8 != 0)
+    return fail(GDN_EINVAL, "rotary_dim must be a multiple of 8, 0..d (got %d)", p->rotary_dim);
+  if (!(p->eps >= 0.f) || !std::isfinite(p->eps)) return fail(GDN_EINVAL, "eps must be >= 0");
+  if (!std::isfinite(p->magnitude)) return fail(GDN_EINVAL, "magnitude must be finite");
+  if (p->reserved0 != 0) return fail(GDN_EINVAL, "reserved0 must be 0");
+  if (p->n_tokens > (int64_t)0x7fffffff) return fail(GDN_EINVAL, "too many tokens for one call");
+  return GDN_OK;
+}
+
+// Sizes, strides and the arrays both directions read.
+int rope_args(gdn::RopeArgs& a, const gdn_qk_rope_problem* p, const int32_t* positions, const uint64_t* freqs,
+              const float* q_weight, const float* k_weight) {
+  std::memset(&a, 0, sizeof a);
+  CHECK(check_rope(p));
+  const int64_t nq = (int64_t)p->h_q * p->d, nk = (int64_t)p->h_k * p->d;
+  CHECK(token_stride(p->q_stride, nq, p->dtype, "q_stride", &a.qs));
+  CHECK(token_stride(p->k_stride, nk, p->dtype, "k_stride", &a.ks));
+  CHECK(token_stride(p->qo_stride, nq, p->dtype, "qo_stride", &a.qos));
+  CHECK(token_stride(p->ko_stride, nk, p->dtype, "ko_stride", &a.kos));
+  CHECK(token_stride(p->dq_stride, nq, p->dtype, "dq_stride", &a.dqs));
+  CHECK(token_stride(p->dk_stride, nk, p->dtype, "dk_stride", &a.dks));
+  if (p->rotary_dim > 0) {
+    CHECK(check_tok(positions, "positions", p->n_tokens));
+    CHECK(check_ptr(freqs, "freqs"));
+  }
+  if ((q_weight || k_weight) && p->norm == GDN_NORM_NONE) return fail(GDN_EINVAL, "a weight needs a norm");
+  if (q_weight) CHECK(check_ptr(q_weight, "q_weight"));
+  if (k_weight) CHECK(check_ptr(k_weight, "k_weight"));
+  if (k_weight && p->h_k == 0) return fail(GDN_EINVAL, "k_weight is given but h_k = 0");
+  a.T = p->n_tokens;
+  a.hq = p->h_q;
+  a.hk = p->h_k;
+  a.D = p->d;
+  a.RD = p->rotary_dim;
+  a.norm = p->norm;
+  a.interleaved = p->interleaved ? 1 : 0;
+  a.eps = p->eps;
+  a.mag = p->magnitude;
+  a.pos = positions;
+  a.freq = freqs;
+  a.wq = q_weight;
+  a.wk = k_weight;
+  return GDN_OK;
+}
+
+} // namespace
+
+extern "C" {
+
+size_t gdn_qk_rope_workspace_bytes(const gdn_qk_rope_problem* p) {
+  if (check_rope(p) != GDN_OK) return 0;
+  const int blocks = p->n_tokens ? gdn::rope_bwd_blocks(p->n_tokens, p->h_q + p->h_k, p->d) : 1;
+  return align_up((size_t)blocks * 2 * p->d * 4);
+}
+
+int gdn_qk_rope_fwd(const gdn_qk_rope_problem* p, const void* q, const void* k, const int32_t* positions,
+                    const uint64_t* freqs, const float* q_weight, const float* k_weight, void* q_out, void* k_out,
+                    void* stream) {
+  gdn::RopeArgs a;
+  CHECK(rope_args(a, p, positions, freqs, q_weight, k_weight));
+  const int64_t T = p->n_tokens, Tk = p->h_k ? T : 0;
+  CHECK(check_tok(q, "q", T));
+  CHECK(check_tok(k, "k", Tk));
+  CHECK(check_tok(q_out, "q_out", T));
+  CHECK(check_tok(k_out, "k_out", Tk));
+  a.q = q;
+  a.k = k;
+  a.qo = q_out;
+  a.ko = k_out;
+  LAUNCH("gdn_qk_rope_fwd", gdn::launch_rope_fwd(a, p->dtype, stream));
+  g_err.clear();
+  return GDN_OK;
+}
+
+int gdn_qk_rope_bwd(const gdn_qk_rope_problem* p, const void* q, const void* k, const int32_t* positions,
+                    const uint64_t* freqs, const float* q_weight, const float* k_weight, const void* dq_out,
+                    const void* dk_out, void* dq, void* dk, float* dq_weight, float* dk_weight, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  gdn::RopeArgs a;
+  CHECK(rope_args(a, p, positions, freqs, q_weight, k_weight));
+  const int64_t T = p->n_tokens, Tk = p->h_k ? T : 0;
+  if (p->norm != GDN_NORM_NONE) {
+    CHECK(check_tok(q, "q", T));
+    CHECK(check_tok(k, "k", Tk));
+  }
+  CHECK(check_tok(dq_out, "dq_out", T));
+  CHECK(check_tok(dk_out, "dk_out", Tk));
+  CHECK(check_tok(dq, "dq", T));
+  CHECK(check_tok(dk, "dk", Tk));
+  if ((dq_weight != nullptr) != (q_weight != nullptr) || (dk_weight != nullptr) != (k_weight != nullptr))
+    return fail(GDN_EINVAL, "a weight and its gradient must be given together");
+  if (dq_weight) CHECK(check_ptr(dq_weight, "dq_weight"));
+  if (dk_weight) CHECK(check_ptr(dk_weight, "dk_weight"));
+  if (q_weight || k_weight) {
+    CHECK(check_ptr(workspace, "workspace"));
+    if (workspace_bytes < gdn_qk_rope_workspace_bytes(p))
+      return fail(GDN_EWORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes,
+                  gdn_qk_rope_workspace_bytes(p));
+  }
+  a.q = q;
+  a.k = k;
+  a.dqo = dq_out;
+  a.dko = dk_out;
+  a.dq = dq;
+  a.dk = dk;
+  a.dwq = dq_weight;
+  a.dwk = dk_weight;
+  a.part = (float*)workspace;
+  LAUNCH("gdn_qk_rope_bwd", gdn::launch_rope_bwd(a, p->dtype, stream));
   g_err.clear();
   return GDN_OK;
 }

@@ -339,4 +339,25 @@ __device__ __forceinline__ int launch_chunk(const Args& a, int x) {
   return a.c_base + x + (x >= a.c_skip_at ? a.c_skip : 0);
 }
 
+// One sequence of a serving step: its token range and slots, checked against the call's sizes. ok
+// is false when the device arrays hold a range outside [0, T] or a slot outside [-1, n_slots); the
+// range is then cut to [0, T], for the NaN that its rows get.
+struct SeqSpan {
+  int64_t t0, t1;
+  int in, out;
+  bool ok;
+};
+__device__ __forceinline__ SeqSpan seq_span(const int32_t* cu, const int32_t* slot_in, const int32_t* slot_out, int n,
+                                            int64_t T, int n_slots) {
+  SeqSpan s;
+  s.t0 = cu ? cu[n] : n;
+  s.t1 = cu ? cu[n + 1] : n + 1;
+  s.in = slot_in[n];
+  s.out = slot_out[n];
+  s.ok = s.t0 >= 0 && s.t1 >= s.t0 && s.t1 <= T && s.in >= -1 && s.in < n_slots && s.out >= -1 && s.out < n_slots;
+  s.t0 = s.t0 < 0 ? 0 : s.t0;
+  s.t1 = s.t1 > T ? T : s.t1;
+  return s;
+}
+
 } // namespace gdn

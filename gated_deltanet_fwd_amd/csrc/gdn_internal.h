@@ -166,4 +166,67 @@ int conv_blocks(int64_t T);
 int launch_conv_fwd(const ConvArgs& a, int dtype, void* stream);
 int launch_conv_bwd(const ConvArgs& a, int dtype, void* stream);
 
+// Conv front-end's serving step (gdn_conv_step.hip).
+struct ConvStepArgs {
+  int64_t T, xs; // tokens; elements between the tokens of x
+  int C, W, N, silu, n_groups, n_slots;
+  int goff[5];
+  const void* x;
+  const float* w;
+  const float* b;
+  const int32_t* cu; // NULL: one token a sequence
+  const int32_t* slot_in;
+  const int32_t* slot_out;
+  const int32_t* slot_tok; // NULL: no state kept inside a sequence
+  void* win;
+  void* y[4];
+};
+int launch_conv_step(const ConvStepArgs& a, int dtype, void* stream);
+
+// Recurrent gated delta rule (gdn_recurrent.hip).
+struct RecurrentArgs {
+  int64_t T, qs, ks, vs; // tokens; elements between the tokens of q, k, v
+  int N, H, HV, G, D, l2norm, n_slots;
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* g;
+  const float* beta;
+  const int32_t* cu; // NULL: one token a sequence
+  const int32_t* slot_in;
+  const int32_t* slot_out;
+  const int32_t* slot_tok;
+  float* states;
+  void* o;
+};
+int launch_recurrent(const RecurrentArgs& a, int dtype, void* stream);
+
+// Norms of the q and k heads with the position rotation (gdn_rope.hip).
+struct RopeArgs {
+  int64_t T;                           // tokens
+  int64_t qs, ks, qos, kos, dqs, dks; // elements between the tokens of q, k, q_out/dq_out, k_out/dk_out, dq, dk
+  int hq, hk, D, RD, norm, interleaved;
+  int hc; // heads per unit of work (one token's heads are cut into units)
+  float eps, mag;
+  const void* q;
+  const void* k;
+  const int32_t* pos;
+  const uint64_t* freq;
+  const float* wq;
+  const float* wk;
+  void* qo;
+  void* ko;
+  const void* dqo;
+  const void* dko;
+  void* dq;
+  void* dk;
+  float* dwq;
+  float* dwk;
+  float* part; // [blocks][2][D] partial sums of the weight gradients
+};
+// Workgroups of the backward (the rows of `part`), and the launches.
+int rope_bwd_blocks(int64_t T, int heads, int D);
+int launch_rope_fwd(const RopeArgs& a, int dtype, void* stream);
+int launch_rope_bwd(const RopeArgs& a, int dtype, void* stream);
+
 } // namespace gdn

@@ -225,6 +225,165 @@ int gdn_conv_bwd(const gdn_conv_problem* p, const void* x, const float* weight, 
                  const int32_t* cu_seqlens, const void* const* dy, void* dx, float* dweight, float* dbias,
                  void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- The gated delta rule, recurrent: one serving step on cached states --------------------
+ * The operation at the top of this file, token by token, on states that live in a cache between
+ * calls: one token a sequence when decoding, a few when drafted tokens are checked or a prompt is
+ * extended (whole prompts go through gdn_fwd, whose ht has the layout of one cached state).
+ * Sequence n starts from states[slot_in[n]] (from zero if slot_in[n] = -1), runs its tokens in
+ * order and leaves its last state in states[slot_out[n]] (nowhere if -1; a sequence of no tokens
+ * leaves its start state). slot_in[n] = slot_out[n] updates a state in place. slot_tok, if given,
+ * names for each token the slot that keeps the state after it (-1: none), so that a run of drafted
+ * tokens can be rolled back to any of them.
+ *
+ *   q, k      [T, H, d], v [T, HV, d]  io dtype; a token's heads are contiguous, tokens are
+ *                                      q_stride, k_stride, v_stride elements apart
+ *   g, beta   [T, HV] f32;  o [T, HV, d] io dtype (contiguous)
+ *   states    [n_slots, HV, d, d] f32 (key index, value index)
+ *   slot_in, slot_out  [N] int32;  slot_tok [T] int32 or NULL
+ *   cu_seqlens [N + 1] int32, or NULL (with cu_seqlens_host NULL): one token a sequence, T = N
+ *
+ * A state is read whole before any state of its sequence is written, and sequences run side by
+ * side: a slot that one sequence writes must not be read or written by another in the same call.
+ * The call may be captured into a graph; the device arrays are read at each replay. They are
+ * checked on the device: a sequence with a token range outside [0, T] or a slot outside
+ * [-1, n_slots) writes no state and fills its o rows (those inside [0, T]) with NaN, as does a
+ * token with such a slot_tok for its own state and row. */
+typedef struct gdn_recurrent_problem {
+  int32_t n_seqs;                 /* N >= 1 sequences (of zero tokens or more) */
+  int32_t h_qk;                   /* H q/k heads */
+  int32_t h_v;                    /* HV value heads, a multiple of H */
+  int32_t d;                      /* head dim, 64 or 128 */
+  int64_t n_tokens;               /* T */
+  int32_t dtype;                  /* GDN_DTYPE_* of q, k, v, o */
+  int32_t l2norm_qk;              /* 1: L2-normalise q and k rows inside the kernel */
+  int32_t n_slots;                /* states in the cache, >= 1 */
+  int32_t reserved0;              /* must be 0 */
+  int64_t q_stride;               /* elements from one token's q to the next (0: H * d); the same */
+  int64_t k_stride;               /* for k (0: H * d) and v (0: HV * d). Rows are 16-byte aligned */
+  int64_t v_stride;
+  const int32_t* cu_seqlens_host; /* host copy of cu_seqlens, read during each call only; NULL: one
+                                     token a sequence */
+} gdn_recurrent_problem;
+
+int gdn_recurrent(const gdn_recurrent_problem* p, const void* q, const void* k, const void* v, const float* g,
+                  const float* beta, const int32_t* cu_seqlens, const int32_t* slot_in, const int32_t* slot_out,
+                  const int32_t* slot_tok, float* states, void* o, void* stream);
+
+/* ---- Norms of the q and k heads with the position rotation ---------------------------------
+ * What stands between a layer's q/k projections (or the conv front-end) and the rule or an
+ * attention over the same heads, in one pass over q and k. For each head row x of a token at
+ * position p (d values, weight w or all ones):
+ *
+ *   n = x / sqrt(mean(x^2) + eps)      (GDN_NORM_RMS)
+ *       x / sqrt(sum(x^2) + eps)       (GDN_NORM_L2)
+ *       x                              (GDN_NORM_NONE: the rotation alone)
+ *   z = n w
+ *   y = z with the pairs (z_a, z_b) of its first rotary_dim values turned by the angle p f_i:
+ *       y_a = m (z_a cos - z_b sin),  y_b = m (z_b cos + z_a sin),  i = 0 .. rotary_dim / 2 - 1
+ *       pairs (i, i + rotary_dim / 2), or with interleaved = 1 (2 i, 2 i + 1)
+ *
+ * freqs holds f_i as an unsigned 64-bit fraction of a turn per position, f_i / (2 pi) 2^64, so that
+ * the angle modulo a turn is exact at every position: gdn_rope_frequencies makes it. m is the
+ * magnitude. The backward takes the gradients of y and the forward's inputs and gives those of
+ * x and of the weights (summed over tokens and heads in a fixed order: bitwise reproducible).
+ * Outputs may be the inputs' own buffers (q_out = q, k_out = k; dq = dq_out, dk = dk_out): each
+ * row is read before it is written, by the same lanes. */
+#define GDN_NORM_NONE 0
+#define GDN_NORM_L2 1
+#define GDN_NORM_RMS 2
+
+typedef struct gdn_qk_rope_problem {
+  int64_t n_tokens;    /* T >= 0 */
+  int32_t h_q;         /* q heads, 1 .. 16384 */
+  int32_t h_k;         /* k heads, 0 .. 16384 (0: no k tensors) */
+  int32_t d;           /* head dim, a multiple of 8, 8 .. 256 */
+  int32_t dtype;       /* GDN_DTYPE_* of q, k and their outputs and gradients */
+  int32_t norm;        /* GDN_NORM_* */
+  int32_t rotary_dim;  /* values of each head that are rotated: a multiple of 8, 0 .. d */
+  int32_t interleaved; /* 0: pairs half the rotary dim apart; 1: neighbours */
+  float eps;           /* added under the norm's root */
+  float magnitude;     /* m */
+  int32_t reserved0;   /* must be 0 */
+  int64_t q_stride;    /* elements between the tokens of q (0: contiguous), */
+  int64_t k_stride;    /* of k, */
+  int64_t qo_stride;   /* of q_out and dq_out, */
+  int64_t ko_stride;   /* of k_out and dk_out, */
+  int64_t dq_stride;   /* of dq */
+  int64_t dk_stride;   /* and of dk (the backward's). Rows are 16-byte aligned */
+} gdn_qk_rope_problem;
+
+/* Frequencies of the rotation, on the host: freqs[i] (rotary_dim / 2 of them) and the magnitude,
+ * from the base b and one of
+ *   GDN_ROPE_PLAIN  f_i = b^(-2 i / rotary_dim)
+ *   GDN_ROPE_LINEAR f_i / factor (every position divided by factor)
+ *   GDN_ROPE_NTK    the base raised to b factor^(rotary_dim / (rotary_dim - 2))
+ *   GDN_ROPE_YARN   f_i (1 - r_i) + f_i / factor r_i, r_i rising from 0 to 1 over the indices i between
+ *                   those that make `fast` and `slow` turns in original_length positions (rounded
+ *                   outwards); magnitude 0.1 ln(factor) + 1 for factor > 1
+ *   GDN_ROPE_BANDS  the same blend with r_i = 1 - (turns_i - slow) / (fast - slow), cut to [0, 1], where
+ *                   turns_i = original_length f_i / (2 pi); magnitude 1
+ * (YaRN: Peng et al. 2023, the blend by index and the blend by turns of its section 3.2.) */
+#define GDN_ROPE_PLAIN 0
+#define GDN_ROPE_LINEAR 1
+#define GDN_ROPE_NTK 2
+#define GDN_ROPE_YARN 3
+#define GDN_ROPE_BANDS 4
+
+typedef struct gdn_rope_scaling {
+  int32_t kind;           /* GDN_ROPE_* */
+  int32_t rotary_dim;     /* even, >= 2 */
+  double base;            /* > 1 */
+  double factor;          /* > 0 (not read by GDN_ROPE_PLAIN) */
+  double original_length; /* > 0 (GDN_ROPE_YARN and GDN_ROPE_BANDS) */
+  double fast;            /* turns: fast > slow > 0 (GDN_ROPE_YARN and GDN_ROPE_BANDS) */
+  double slow;
+} gdn_rope_scaling;
+
+int gdn_rope_frequencies(const gdn_rope_scaling* s, uint64_t* freqs_host, float* magnitude);
+
+/* Bytes of device workspace gdn_qk_rope_bwd needs (the workgroups' partial sums of the weight
+ * gradients). 0 if the problem is invalid. */
+size_t gdn_qk_rope_workspace_bytes(const gdn_qk_rope_problem* p);
+
+/* Forward: q_out, k_out. positions [T] int32 (any sign) and freqs [rotary_dim / 2] uint64 on the
+ * device, NULL iff rotary_dim = 0; q_weight, k_weight f32 [d] or NULL (NULL with GDN_NORM_NONE). */
+int gdn_qk_rope_fwd(const gdn_qk_rope_problem* p, const void* q, const void* k, const int32_t* positions,
+                    const uint64_t* freqs, const float* q_weight, const float* k_weight, void* q_out, void* k_out,
+                    void* stream);
+
+/* Backward: dq, dk from q, k (not read, may be NULL, with GDN_NORM_NONE) and the upstream
+ * gradients dq_out, dk_out; dq_weight, dk_weight f32 [d] iff the weight is given. */
+int gdn_qk_rope_bwd(const gdn_qk_rope_problem* p, const void* q, const void* k, const int32_t* positions,
+                    const uint64_t* freqs, const float* q_weight, const float* k_weight, const void* dq_out,
+                    const void* dk_out, void* dq, void* dk, float* dq_weight, float* dk_weight, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/* ---- The conv front-end's serving step ------------------------------------------------------
+ * gdn_conv_fwd's operation on sequences whose last W - 1 inputs live in a cache between calls:
+ * windows [n_slots, W - 1, C] in the io dtype, oldest row first (the last W - 1 rows of a prompt's
+ * x, zeros before its first token, are its window). Slots, cu_seqlens, in-place updates and the
+ * checks on the device are those of gdn_recurrent: a sequence reads windows[slot_in[n]] (zeros if
+ * -1), writes its last window to windows[slot_out[n]], and slot_tok keeps the window after each
+ * token. Where gdn_recurrent fills o rows with NaN, the rows of every y[g] are. */
+typedef struct gdn_conv_step_problem {
+  int32_t n_seqs;                 /* N >= 1 sequences */
+  int32_t channels;               /* C = sum of group_channels, a multiple of 8 */
+  int64_t n_tokens;               /* T */
+  int32_t width;                  /* W taps, 1..4 (at 1 there is no window: windows may be NULL) */
+  int32_t dtype;                  /* GDN_DTYPE_* of x, y and windows */
+  int32_t silu;                   /* 1: y = SiLU(pre); 0: y = pre */
+  int32_t n_groups;               /* 1..4 output tensors */
+  int32_t group_channels[4];      /* channels of each output tensor, multiples of 8 */
+  int32_t n_slots;                /* windows in the cache, >= 1 */
+  int32_t reserved0;              /* must be 0 */
+  int64_t x_stride;               /* elements from one token's x to the next (0: C); 16-byte rows */
+  const int32_t* cu_seqlens_host; /* host copy of cu_seqlens; NULL: one token a sequence */
+} gdn_conv_step_problem;
+
+int gdn_conv_step(const gdn_conv_step_problem* p, const void* x, const float* weight, const float* bias,
+                  const int32_t* cu_seqlens, const int32_t* slot_in, const int32_t* slot_out,
+                  const int32_t* slot_tok, void* windows, void* const* y, void* stream);
+
 /* Message of the calling thread's last error ("" if none). */
 const char* gdn_last_error(void);
 

@@ -1,0 +1,269 @@
+"""GPU tests of the recurrent gated delta rule on cached states against the FP64 token recurrence:
+every output row and every state, at the sizes and slots where it can go wrong."""
+import numpy as np
+import pytest
+import torch
+
+import gated_deltanet_fwd_amd as G
+import oracle
+from step_util import check, f64
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+# sums of 128 products, and a state's roundings over the tokens it remembers
+K = 400
+
+
+def make(lengths, H, HV, d, dtype=torch.bfloat16, keep=False, fresh=(), spare=3, packed=False, seed=3, **kw):
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(seed)
+    normal = lambda *s: torch.randn(*s, generator=gen, device=DEV)
+    N, T = len(lengths), sum(lengths)
+    cu = np.concatenate([[0], np.cumsum(lengths)]).astype(np.int32)
+    slots = N + (T if keep else 0) + spare
+    order = torch.randperm(slots, generator=gen, device=DEV).to(torch.int32)
+    s = dict(cu_host=cu, cu=torch.from_numpy(cu).to(DEV), slots=slots)
+    if packed:
+        x = normal(T, (2 * H + HV) * d + 8).to(dtype)
+        s["q"] = x[:, :H * d].view(T, H, d)
+        s["k"] = x[:, H * d:2 * H * d].view(T, H, d)
+        s["v"] = x[:, 2 * H * d:(2 * H + HV) * d].view(T, HV, d)
+    else:
+        s["q"], s["k"], s["v"] = normal(T, H, d).to(dtype), normal(T, H, d).to(dtype), normal(T, HV, d).to(dtype)
+    s["beta"] = torch.sigmoid(normal(T, HV))
+    s["g"] = torch.nn.functional.logsigmoid(normal(T, HV) + 3)
+    s["states"] = 0.1 * normal(slots, HV, d, d)
+    s["slot_in"] = order[:N].clone()
+    for n in fresh:
+        s["slot_in"][n] = -1
+    s["slot_out"] = order[:N].clone()
+    s["slot_tok"] = order[N:N + T].clone() if keep else None
+    s.update(kw)
+    return s
+
+
+def reference(s, l2norm=True):
+    """(o, states) by the token recurrence, a call per sequence, or per token where states are kept."""
+    q, k, v = (x.float().cpu().numpy() for x in (s["q"], s["k"], s["v"]))
+    g, beta = s["g"].cpu().numpy(), s["beta"].cpu().numpy()
+    start = s["states"].cpu().numpy()
+    o, states = np.zeros(v.shape), start.astype(np.float64)
+    si, so = s["slot_in"].tolist(), s["slot_out"].tolist()
+    st = s["slot_tok"].tolist() if s["slot_tok"] is not None else None
+    for n in range(len(si)):
+        a, e = int(s["cu_host"][n]), int(s["cu_host"][n + 1])
+        h0 = start[si[n]][None] if si[n] >= 0 else np.zeros_like(start[:1])
+        part = lambda x, b: np.ascontiguousarray(x[a:b])
+        for b in ([e] if st is None else range(a + 1, e + 1)) if e > a else []:
+            oo, ht = oracle.fwd(np.array([0, b - a], np.int32), part(q, b), part(k, b), part(v, b), part(g, b),
+                                part(beta, b), np.ascontiguousarray(h0), l2norm=l2norm)
+            o[a:b] = oo
+            if st is not None and st[b - 1] >= 0:
+                states[st[b - 1]] = ht[0]
+        if so[n] >= 0:
+            states[so[n]] = ht[0] if e > a else h0[0]
+    return o, states
+
+
+def run(s, l2norm=True, one=None, **kw):
+    H, d, HV = s["q"].shape[1], s["q"].shape[2], s["v"].shape[1]
+    one = bool(np.all(np.diff(s["cu_host"]) == 1)) if one is None else one
+    p = G.RecurrentProblem(len(s["cu_host"]) - 1, H, HV, d, s["slots"], cu_seqlens_host=None if one else s["cu_host"],
+                           dtype=s["v"].dtype, l2norm=l2norm)
+    print("recurrent N=%d T=%d (H,HV)=(%d,%d) d=%d" % (len(s["cu_host"]) - 1, s["v"].shape[0], H, HV, d), flush=True)
+    states = s["states"].clone()
+    o = G.gdn_recurrent(p, s["q"], s["k"], s["v"], s["g"], s["beta"], states, s["slot_in"], s["slot_out"],
+                        slot_tok=s["slot_tok"], cu_seqlens=None if one else s["cu"], **kw)
+    torch.cuda.synchronize()
+    return o, states
+
+
+CASES = {
+    "one_sequence": dict(lengths=[1], H=16, HV=48, d=128),
+    "decode_33": dict(lengths=[1] * 33, H=2, HV=6, d=128, fresh=(4, 32)),
+    "decode_300_d64": dict(lengths=[1] * 300, H=1, HV=3, d=64),
+    "decode_f32": dict(lengths=[1] * 7, H=3, HV=3, d=128, dtype=torch.float32),
+    "decode_packed": dict(lengths=[1] * 9, H=2, HV=4, d=64, packed=True),
+    "ragged": dict(lengths=[3, 0, 1, 17, 64, 2, 0], H=2, HV=6, d=128, fresh=(1, 3)),
+    "ragged_f32_d64": dict(lengths=[5, 130, 0, 63], H=4, HV=8, d=64, dtype=torch.float32, fresh=(0,)),
+    "drafts": dict(lengths=[8, 1, 5, 0, 3], H=2, HV=4, d=128, keep=True),
+    "drafts_packed_f32": dict(lengths=[2, 4, 7], H=1, HV=2, d=64, keep=True, packed=True, dtype=torch.float32),
+    "long": dict(lengths=[1000, 37], H=1, HV=2, d=128, fresh=(0,)),
+    "long_f32_many_heads": dict(lengths=[300], H=16, HV=48, d=128, dtype=torch.float32),
+}
+
+
+@pytest.mark.parametrize("l2norm", [True, False], ids=["l2norm", "given"])
+@pytest.mark.parametrize("name", CASES)
+def test_recurrent(name, l2norm):
+    s = make(**CASES[name])
+    if not l2norm:  # rows of about unit length
+        s["q"], s["k"] = ((x.float() * x.shape[-1] ** -0.5).to(x.dtype) for x in (s["q"], s["k"]))
+    o, states = run(s, l2norm)
+    o_ref, st_ref = reference(s, l2norm)
+    check("o", o, o_ref, K)
+    check("states", states, st_ref, K)
+
+
+def test_slots_not_named_are_untouched_and_sequences_may_share_a_start():
+    s = make([1, 2, 3], 2, 4, 64)
+    s["slot_in"][:] = s["slot_in"][0]  # one prompt's state, three continuations
+    s["slot_out"] = torch.tensor([-1, 4, 5], dtype=torch.int32, device=DEV)
+    s["slot_in"][:] = 2
+    o, states = run(s)
+    o_ref, st_ref = reference(s)
+    check("o", o, o_ref, K)
+    check("states", states, st_ref, K)
+    for slot in range(s["slots"]):
+        if slot not in (4, 5):
+            assert torch.equal(states[slot], s["states"][slot])
+
+
+def test_one_token_with_and_without_lengths_is_the_same():
+    s = make([1] * 13, 2, 6, 128)
+    a, b = run(s, one=True), run(s, one=False)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_runs_and_single_tokens_agree_to_rounding():
+    """The same tokens in one call and one by one (a new call per token), in place."""
+    s = make([6, 6, 6], 2, 4, 128, dtype=torch.float32)
+    o, states = run(s)
+    p = G.RecurrentProblem(3, 2, 4, 128, s["slots"], dtype=torch.float32)
+    st, rows = s["states"].clone(), []
+    for i in range(6):
+        at = torch.tensor([i, 6 + i, 12 + i], device=DEV)
+        rows.append(G.gdn_recurrent(p, *(s[x][at] for x in ("q", "k", "v", "g", "beta")), st, s["slot_in"], s["slot_out"]))
+    torch.cuda.synchronize()
+    o1 = torch.stack(rows, 1).flatten(0, 1)
+    check("o", o1, f64(o), K)
+    check("states", st, f64(states), K)
+
+
+def test_gates_at_their_ends():
+    """g = -inf forgets the state, g = 0 keeps it, beta = 0 writes nothing, a zero key row is harmless
+    under the norm."""
+    s = make([2, 2, 2, 2], 1, 2, 128)
+    s["g"][0:2] = float("-inf")
+    s["g"][2:4], s["beta"][2:4] = 0.0, 0.0
+    s["k"][4:6] = 0
+    s["g"][6:8], s["beta"][6:8] = -80.0, 1.0
+    o, states = run(s)
+    assert torch.equal(states[s["slot_out"][1].long()], s["states"][s["slot_in"][1].long()])
+    s["g"][0:2] = -1e30  # the oracle takes finite logs; exp is 0 either way
+    o_ref, st_ref = reference(s)
+    check("o", o, o_ref, K)
+    check("states", states, st_ref, K)
+
+
+def test_nan_in_one_state_stays_in_its_sequence_and_head():
+    s = make([1, 1, 1], 2, 4, 128)
+    s["states"][s["slot_in"][1].long(), 3] = float("nan")
+    o, states = run(s)
+    bad = torch.zeros_like(o, dtype=torch.bool)
+    bad[1, 3] = True
+    assert torch.equal(torch.isnan(o), bad)
+    bad = torch.zeros_like(states, dtype=torch.bool)
+    bad[s["slot_out"][1].long(), 3] = True
+    assert torch.equal(torch.isnan(states), bad)
+
+
+@pytest.mark.parametrize("what", ["slot_in", "slot_out", "slot_tok", "cu"])
+def test_device_arrays_out_of_range_are_refused_on_the_device(what):
+    """NaN rows for the sequence (or token) with the bad entry, no state of it written, the rest right."""
+    s = make([2, 3, 4], 2, 4, 64, keep=True)
+    s["slot_out"][:] = torch.tensor([0, 1, 2], dtype=torch.int32, device=DEV)
+    used = set(s["slot_tok"].tolist())
+    s["slot_in"][:] = -1
+    free = [x for x in range(s["slots"]) if x not in used]
+    s["slot_out"][:] = torch.tensor(free[:3], dtype=torch.int32, device=DEV)
+    o_ref, st_ref = reference(s)
+    rows = range(2, 5)
+    if what == "slot_tok":
+        lost = [s["slot_tok"][3].item()]
+        s["slot_tok"][3] = s["slots"]
+        rows = [3]
+    else:
+        lost = s["slot_tok"][2:5].tolist() + [free[1]]
+        if what == "cu":
+            s["cu"] = torch.tensor([0, 2, 5, 10], dtype=torch.int32, device=DEV)  # past the last token
+            rows, lost = range(5, 9), s["slot_tok"][5:9].tolist() + [free[2]]
+        else:
+            s[what][1] = s["slots"] if what == "slot_in" else -2
+    o, states = run(s)
+    rows = list(rows)
+    assert torch.isnan(o[rows].float()).all()
+    good = [t for t in range(9) if t not in rows]
+    check("o", o[good], o_ref[good], K)
+    st_ref[lost] = s["states"][lost].double().cpu().numpy()
+    check("states", states, st_ref, K)
+
+
+def test_states_past_32_bit_offsets():
+    """Slots whose first element lies past 2^31 and past 2^32 elements."""
+    HV, d = 48, 128
+    slots = 2 ** 32 // (HV * d * d) + 3
+    s = make([1, 1, 2], 16, HV, d, spare=0)
+    pool = torch.empty(slots, HV, d, d, device=DEV)
+    where = torch.tensor([0, 2 ** 31 // (HV * d * d) + 1, slots - 1], dtype=torch.int32, device=DEV)
+    small = s["states"][s["slot_in"].long()].clone()
+    pool[where.long()] = small
+    p = G.RecurrentProblem(3, 16, HV, d, slots, cu_seqlens_host=s["cu_host"])
+    o = G.gdn_recurrent(p, s["q"], s["k"], s["v"], s["g"], s["beta"], pool, where, where, cu_seqlens=s["cu"])
+    got = pool[where.long()].clone()
+    torch.cuda.synchronize()
+    s["states"], s["slot_in"] = small, torch.arange(3, dtype=torch.int32, device=DEV)
+    s["slot_out"] = s["slot_in"]
+    o_ref, st_ref = reference(s)
+    check("o", o, o_ref, K)
+    check("states", got, st_ref, K)
+
+
+def test_on_a_stream_of_its_own():
+    s = make([1] * 20, 2, 4, 128)
+    ref = run(s)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = run(s, stream=side)
+    assert torch.equal(ref[0], got[0]) and torch.equal(ref[1], got[1])
+
+
+def test_graph_replays_equal_eager_steps():
+    """A captured decoding step, replayed with other eager work between, against eager steps."""
+    s = make([1] * 5, 2, 4, 128)
+    p = G.RecurrentProblem(5, 2, 4, 128, s["slots"])
+    a = (s["q"], s["k"], s["v"], s["g"], s["beta"])
+    eager, graphed = s["states"].clone(), s["states"].clone()
+    o = torch.empty_like(s["v"])
+    G.gdn_recurrent(p, *a, graphed, s["slot_in"], s["slot_out"], o=o)
+    graphed.copy_(s["states"])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        G.gdn_recurrent(p, *a, graphed, s["slot_in"], s["slot_out"], o=o)
+    for i in range(4):
+        s["v"].copy_(torch.roll(s["v"], 1, 0))
+        want = G.gdn_recurrent(p, *a, eager, s["slot_in"], s["slot_out"])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want) and torch.equal(graphed, eager), i
+
+
+def test_binding_refuses_wrong_tensors():
+    s = make([1, 1], 2, 4, 64)
+    p = G.RecurrentProblem(2, 2, 4, 64, s["slots"])
+    good = dict(q=s["q"], k=s["k"], v=s["v"], g=s["g"], beta=s["beta"], states=s["states"], slot_in=s["slot_in"],
+                slot_out=s["slot_out"])
+    before = s["states"].clone()
+    for name, bad, fragment in (
+            ("q", s["q"].float(), "type"), ("k", s["k"][:1], "shape"), ("g", s["g"].double(), "type"),
+            ("v", s["v"].transpose(0, 1).contiguous().transpose(0, 1), "contiguous"),
+            ("states", s["states"][:-1], "shape"), ("slot_in", s["slot_in"].long(), "type"),
+            ("slot_out", s["slot_out"].cpu(), "is on"), ("beta", s["beta"].t().contiguous().t(), "contiguous")):
+        with pytest.raises(G.GdnError, match=fragment):
+            G.gdn_recurrent(p, **{**good, name: bad})
+    with pytest.raises(G.GdnError, match="given together"):
+        G.gdn_recurrent(p, **good, cu_seqlens=s["cu"])
+    torch.cuda.synchronize()
+    assert torch.equal(before, s["states"])
