@@ -1076,11 +1076,14 @@ int gdn_recurrent(const gdn_recurrent_problem* p, const void* q, const void* k, 
     return fail(GDN_EUNSUPPORTED, "unsupported dtype %d", p->dtype);
   CHECK(check_steps(p->n_seqs, p->n_tokens, p->n_slots, p->reserved0, p->cu_seqlens_host));
   if ((int64_t)p->n_seqs * p->h_v > (int64_t)0x0fffffff) return fail(GDN_EINVAL, "too many sequences x heads");
+  if (p->h_v > 65536) return fail(GDN_EINVAL, "h_v must be at most 65536 (got %d)", p->h_v);
   gdn::RecurrentArgs a;
   std::memset(&a, 0, sizeof a);
   CHECK(token_stride(p->q_stride, (int64_t)p->h_qk * p->d, p->dtype, "q_stride", &a.qs));
   CHECK(token_stride(p->k_stride, (int64_t)p->h_qk * p->d, p->dtype, "k_stride", &a.ks));
   CHECK(token_stride(p->v_stride, (int64_t)p->h_v * p->d, p->dtype, "v_stride", &a.vs));
+  if (std::max(std::max(a.qs, a.ks), a.vs) > (int64_t)1 << 28) // the kernels' offsets inside a few tokens are 32-bit
+    return fail(GDN_EINVAL, "token strides must be at most 2^28 elements");
   const int64_t T = p->n_tokens;
   CHECK(check_tok(q, "q", T));
   CHECK(check_tok(k, "k", T));
@@ -1090,14 +1093,25 @@ int gdn_recurrent(const gdn_recurrent_problem* p, const void* q, const void* k, 
   CHECK(check_tok(o, "o", T));
   CHECK(check_ptr(states, "states"));
   CHECK(check_step_arrays(p->cu_seqlens_host, cu_seqlens, slot_in, slot_out, slot_tok));
-  a.T = T;
+  a.T = (int)T;
   a.N = p->n_seqs;
   a.H = p->h_qk;
   a.HV = p->h_v;
   a.G = p->h_v / p->h_qk;
+  a.g_mul = ((uint64_t)1 << 32) / a.G + 1;
   a.D = p->d;
   a.l2norm = p->l2norm_qk ? 1 : 0;
   a.n_slots = p->n_slots;
+  a.longest = 1;
+  a.live = p->n_seqs;
+  if (p->cu_seqlens_host) {
+    a.live = 0;
+    for (int n = 0; n < p->n_seqs; ++n) {
+      const int len = p->cu_seqlens_host[n + 1] - p->cu_seqlens_host[n];
+      a.longest = std::max(a.longest, len);
+      a.live += len > 0;
+    }
+  }
   a.q = q;
   a.k = k;
   a.v = v;
@@ -1148,7 +1162,7 @@ int gdn_conv_step(const gdn_conv_step_problem* p, const void* x, const float* we
     CHECK(check_tok(y[g], "y[g]", T));
     a.y[g] = y[g];
   }
-  a.T = T;
+  a.T = (int)T;
   a.C = base.C;
   a.W = base.W;
   a.N = p->n_seqs;

@@ -41,7 +41,7 @@ __global__ __launch_bounds__(256) void k_conv_step(ConvStepArgs a) {
     const SeqSpan sp = seq_span(a.cu, a.slot_in, a.slot_out, n, a.T, a.n_slots);
     if (!sp.ok) {
       const vec nan4 = (vec)(TI)__builtin_nanf("");
-      for (int64_t t = sp.t0; t < sp.t1; ++t) *reinterpret_cast<vec*>(y + t * Cg) = nan4;
+      for (int t = sp.t0; t < sp.t1; ++t) *reinterpret_cast<vec*>(y + (int64_t)t * Cg) = nan4;
       continue;
     }
     vec h[W]; // the window's rows, the newest last; h[H] is the current token
@@ -51,7 +51,7 @@ __global__ __launch_bounds__(256) void k_conv_step(ConvStepArgs a) {
         h[j] = sp.in < 0 ? (vec)(TI)0.f
                          : *reinterpret_cast<const vec*>(win + ((int64_t)sp.in * H + j) * a.C);
     }
-    for (int64_t t = sp.t0; t < sp.t1; ++t) {
+    for (int t = sp.t0; t < sp.t1; ++t) {
       h[H] = *reinterpret_cast<const vec*>(x + t * a.xs);
       const int st = a.slot_tok ? a.slot_tok[t] : -1;
       vec out;
@@ -63,7 +63,7 @@ __global__ __launch_bounds__(256) void k_conv_step(ConvStepArgs a) {
         const float r = SILU ? p / (1.f + __expf(-p)) : p;
         out[e] = (TI)(st < -1 || st >= a.n_slots ? __builtin_nanf("") : r);
       }
-      *reinterpret_cast<vec*>(y + t * Cg) = out;
+      *reinterpret_cast<vec*>(y + (int64_t)t * Cg) = out;
 #pragma unroll
       for (int j = 0; j < H; ++j) h[j] = h[j + 1];
       if constexpr (H > 0) {

@@ -343,20 +343,19 @@ __device__ __forceinline__ int launch_chunk(const Args& a, int x) {
 // is false when the device arrays hold a range outside [0, T] or a slot outside [-1, n_slots); the
 // range is then cut to [0, T], for the NaN that its rows get.
 struct SeqSpan {
-  int64_t t0, t1;
-  int in, out;
+  int t0, t1, in, out;
   bool ok;
 };
 __device__ __forceinline__ SeqSpan seq_span(const int32_t* cu, const int32_t* slot_in, const int32_t* slot_out, int n,
-                                            int64_t T, int n_slots) {
+                                            int T, int n_slots) {
   SeqSpan s;
   s.t0 = cu ? cu[n] : n;
   s.t1 = cu ? cu[n + 1] : n + 1;
   s.in = slot_in[n];
   s.out = slot_out[n];
   s.ok = s.t0 >= 0 && s.t1 >= s.t0 && s.t1 <= T && s.in >= -1 && s.in < n_slots && s.out >= -1 && s.out < n_slots;
-  s.t0 = s.t0 < 0 ? 0 : s.t0;
-  s.t1 = s.t1 > T ? T : s.t1;
+  s.t0 = max(s.t0, 0);
+  s.t1 = min(s.t1, T);
   return s;
 }
 

@@ -168,8 +168,8 @@ int launch_conv_bwd(const ConvArgs& a, int dtype, void* stream);
 
 // Conv front-end's serving step (gdn_conv_step.hip).
 struct ConvStepArgs {
-  int64_t T, xs; // tokens; elements between the tokens of x
-  int C, W, N, silu, n_groups, n_slots;
+  int64_t xs; // elements between the tokens of x
+  int T, C, W, N, silu, n_groups, n_slots;
   int goff[5];
   const void* x;
   const float* w;
@@ -185,8 +185,10 @@ int launch_conv_step(const ConvStepArgs& a, int dtype, void* stream);
 
 // Recurrent gated delta rule (gdn_recurrent.hip).
 struct RecurrentArgs {
-  int64_t T, qs, ks, vs; // tokens; elements between the tokens of q, k, v
-  int N, H, HV, G, D, l2norm, n_slots;
+  int64_t qs, ks, vs; // elements between the tokens of q, k, v
+  uint64_t g_mul;     // 2^32 / G rounded up: h / G = h g_mul >> 32 for h, G <= 65536
+  int T, N, H, HV, G, D, l2norm, n_slots;
+  int longest, live; // by the host's lengths: the longest sequence, and how many have tokens
   const void* q;
   const void* k;
   const void* v;
