@@ -20,7 +20,9 @@ allocates are allocated on its launch stream. The functions carry the C names:
     gdn_qk_rope_fwd(rope_problem, q, k, positions, freqs, ...) -> (q_out, k_out)
     gdn_qk_rope_bwd(rope_problem, q, k, positions, freqs, dq_out, dk_out, ...) -> dict of gradients
 
-The last five check their tensors (shape, type, layout, device) before the call and raise GdnError.
+gdn_recurrent, gdn_conv_step, gdn_qk_rope_fwd and gdn_qk_rope_bwd check their tensors (shape, type,
+layout, device) before the call and raise GdnError; their marshalling is native (csrc/gdn_binding.cpp),
+since a decoding step is shorter than it would take in Python.
 
 A missing or unloadable library raises ImportError-like errors at first use; there is no other
 code path.
@@ -490,41 +492,34 @@ def _io_dtype(dtype) -> int:
     return DTYPE_BF16 if dtype == torch.bfloat16 else DTYPE_F32
 
 
-def _expect(t, name: str, shape, dtype, device, strided: bool = False):
-    """The tensor's address. Raises unless `t` has this shape, type and device and is contiguous
-    (`strided`: but for the distance between its first dimension's entries)."""
-    if t.shape != shape:
-        raise GdnError(GDN_EINVAL, "%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    if t.dtype != dtype:
-        raise GdnError(GDN_EINVAL, "%s has type %s, expected %s" % (name, t.dtype, dtype))
-    if t.device != device:
-        raise GdnError(GDN_EINVAL, "%s is on %s, expected %s" % (name, t.device, device))
-    if not t.is_contiguous() and not (strided and t.numel() and t[0].is_contiguous() and t.stride(0) >= t[0].numel()):
-        raise GdnError(GDN_EINVAL, "%s is not contiguous%s" % (name, " within a token" if strided else ""))
-    return t.data_ptr()
+_marshal = None
 
 
-def _token_stride(t) -> int:
-    """Elements between the tokens of a tensor that _expect let pass (0: contiguous)."""
-    return 0 if t.is_contiguous() else t.stride(0)
+def _native():
+    """The native argument marshalling of the functions below (csrc/gdn_binding.cpp), bound to the
+    loaded library. Raises OSError if it was not built."""
+    global _marshal
+    if _marshal is None:
+        lib = load_library()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise OSError("_binding.so not loadable (%s): build it with `python -m gated_deltanet_fwd_amd.build`" % e)
+        _binding.init(GdnError, *(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in
+                                  ("gdn_recurrent", "gdn_conv_step", "gdn_qk_rope_fwd", "gdn_qk_rope_bwd",
+                                   "gdn_qk_rope_workspace_bytes", "gdn_last_error")))
+        _marshal = _binding
+    return _marshal
 
 
-def _given(t, name: str, shape, dtype, device):
-    return None if t is None else _expect(t, name, shape, dtype, device)
-
-
-class _On:
-    """The launch stream's handle; as a context, the stream that buffers are allocated on."""
-
-    def __init__(self, stream, device):
-        self.stream = None if stream is None else _torch_stream(stream, device)
-        self.handle = (self.stream or torch.cuda.current_stream(device)).cuda_stream
-
-    def empty(self, shape, dtype, device):
-        if self.stream is None:
-            return torch.empty(shape, dtype=dtype, device=device)
-        with torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=dtype, device=device)
+def _call(name: str, device_of, stream, *args):
+    """A native call on torch's current stream, or with `stream` as the current one (the launch stream
+    and the one that buffers are allocated on)."""
+    f = getattr(_marshal or _native(), name)
+    if stream is None:
+        return f(*args)
+    with torch.cuda.stream(_torch_stream(stream, device_of.device)):
+        return f(*args)
 
 
 def _step_lengths(cu_seqlens_host, n_seqs):
@@ -548,9 +543,7 @@ class RecurrentProblem:
         self.st = _RecurrentProblem(n_seqs=int(n_seqs), h_qk=int(h_qk), h_v=int(h_v), d=int(d), n_tokens=tokens,
                                     dtype=_io_dtype(dtype),
                                     l2norm_qk=int(bool(l2norm)), n_slots=int(n_slots), cu_seqlens_host=ptr)
-        self.shapes = dict(q=(tokens, int(h_qk), int(d)), v=(tokens, int(h_v), int(d)), g=(tokens, int(h_v)),
-                           states=(int(n_slots), int(h_v), int(d), int(d)), seqs=(int(n_seqs),), tok=(tokens,),
-                           cu=(int(n_seqs) + 1,))
+        self.at = ctypes.addressof(self.st)
 
     def ref(self):
         return ctypes.byref(self.st)
@@ -562,19 +555,7 @@ def gdn_recurrent(p: RecurrentProblem, q, k, v, g, beta, states, slot_in, slot_o
     zero), leaves its state in states[slot_out] (-1: nowhere) and, with slot_tok, the state after each
     token in states[slot_tok]. q, k and v may be parts of one row (a token's heads contiguous).
     Returns o; `states` is updated in place."""
-    lib, st, sh, dev, f32, i32 = load_library(), p.st, p.shapes, v.device, torch.float32, torch.int32
-    on = _On(stream, dev)
-    if o is None:
-        o = on.empty(sh["v"], p.dtype, dev)
-    args = (_expect(q, "q", sh["q"], p.dtype, dev, True), _expect(k, "k", sh["q"], p.dtype, dev, True),
-            _expect(v, "v", sh["v"], p.dtype, dev, True), _expect(g, "g", sh["g"], f32, dev),
-            _expect(beta, "beta", sh["g"], f32, dev), _given(cu_seqlens, "cu_seqlens", sh["cu"], i32, dev),
-            _expect(slot_in, "slot_in", sh["seqs"], i32, dev), _expect(slot_out, "slot_out", sh["seqs"], i32, dev),
-            _given(slot_tok, "slot_tok", sh["tok"], i32, dev), _expect(states, "states", sh["states"], f32, dev),
-            _expect(o, "o", sh["v"], p.dtype, dev))
-    st.q_stride, st.k_stride, st.v_stride = _token_stride(q), _token_stride(k), _token_stride(v)
-    _check(lib.gdn_recurrent(p.ref(), *args, on.handle))
-    return o
+    return _call("recurrent", v, stream, p.at, q, k, v, g, beta, states, slot_in, slot_out, slot_tok, cu_seqlens, o)
 
 
 class ConvStepProblem:
@@ -594,9 +575,7 @@ class ConvStepProblem:
                                    n_groups=len(self.groups),
                                    group_channels=(ctypes.c_int32 * 4)(*self.groups),
                                    n_slots=int(n_slots), cu_seqlens_host=ptr)
-        self.shapes = dict(x=(tokens, channels), weight=(channels, width), bias=(channels,),
-                           windows=(int(n_slots), width - 1, channels), seqs=(int(n_seqs),), tok=(tokens,),
-                           cu=(int(n_seqs) + 1,), outs=[(tokens, c) for c in self.groups])
+        self.at = ctypes.addressof(self.st)
 
     def ref(self):
         return ctypes.byref(self.st)
@@ -606,21 +585,8 @@ def gdn_conv_step(p: ConvStepProblem, x, weight, bias, windows, slot_in, slot_ou
                   outs=None, stream=None):
     """One serving step of the conv front-end on cached windows (slots as in gdn_recurrent). Returns
     the list of outputs, [T, group_channels[g]]; `windows` is updated in place (None at width 1)."""
-    lib, st, sh, dev, f32, i32 = load_library(), p.st, p.shapes, x.device, torch.float32, torch.int32
-    on = _On(stream, dev)
-    if outs is None:
-        outs = [on.empty(s, p.dtype, dev) for s in sh["outs"]]
-    elif len(outs) != len(sh["outs"]):
-        raise GdnError(GDN_EINVAL, "outs has %d tensors, expected %d" % (len(outs), len(sh["outs"])))
-    ys = (ctypes.c_void_p * 4)(*[_expect(t, "outs", s, p.dtype, dev) for t, s in zip(outs, sh["outs"])])
-    args = (_expect(x, "x", sh["x"], p.dtype, dev, True), _expect(weight, "weight", sh["weight"], f32, dev),
-            _given(bias, "bias", sh["bias"], f32, dev), _given(cu_seqlens, "cu_seqlens", sh["cu"], i32, dev),
-            _expect(slot_in, "slot_in", sh["seqs"], i32, dev), _expect(slot_out, "slot_out", sh["seqs"], i32, dev),
-            _given(slot_tok, "slot_tok", sh["tok"], i32, dev),
-            _given(windows, "windows", sh["windows"], p.dtype, dev))
-    st.x_stride = _token_stride(x)
-    _check(lib.gdn_conv_step(p.ref(), *args, ys, on.handle))
-    return outs
+    return _call("conv_step", x, stream, p.at, x, weight, bias, windows, slot_in, slot_out, slot_tok, cu_seqlens,
+                 None if outs is None else list(outs))
 
 
 def gdn_rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -653,29 +619,17 @@ class QkRopeProblem:
                                  dtype=_io_dtype(dtype), norm=NORMS[norm],
                                  rotary_dim=rotary, interleaved=int(bool(interleaved)), eps=float(eps),
                                  magnitude=float(magnitude))
-        self.shapes = dict(q=(int(n_tokens), int(h_q), int(d)), k=(int(n_tokens), int(h_k), int(d)),
-                           tok=(int(n_tokens),), freqs=(rotary // 2,), w=(int(d),))
-        self.workspace_bytes = None  # of the backward, asked for once
+        self.at = ctypes.addressof(self.st)
 
     def ref(self):
         return ctypes.byref(self.st)
 
 
 def gdn_qk_rope_workspace_bytes(p: QkRopeProblem) -> int:
-    if p.workspace_bytes is None:
-        n = load_library().gdn_qk_rope_workspace_bytes(p.ref())
-        if n == 0:
-            raise GdnError(GDN_EINVAL, load_library().gdn_last_error().decode())
-        p.workspace_bytes = int(n)
-    return p.workspace_bytes
-
-
-def _rope_common(p, positions, freqs, q_weight, k_weight, dev):
-    sh = p.shapes
-    return (_given(positions, "positions", sh["tok"], torch.int32, dev),
-            _given(freqs, "freqs", sh["freqs"], torch.int64, dev),
-            _given(q_weight, "q_weight", sh["w"], torch.float32, dev),
-            _given(k_weight, "k_weight", sh["w"], torch.float32, dev))
+    n = load_library().gdn_qk_rope_workspace_bytes(p.ref())
+    if n == 0:
+        raise GdnError(GDN_EINVAL, load_library().gdn_last_error().decode())
+    return int(n)
 
 
 def gdn_qk_rope_fwd(p: QkRopeProblem, q, k, positions, freqs, q_weight=None, k_weight=None, q_out=None, k_out=None,
@@ -683,46 +637,14 @@ def gdn_qk_rope_fwd(p: QkRopeProblem, q, k, positions, freqs, q_weight=None, k_w
     """Norms and rotation of q [T, h_q, d] and k [T, h_k, d] (None when h_k = 0), which may be parts of
     one row, with positions int32 [T] and the frequencies of gdn_rope_frequencies on the device.
     Returns (q_out, k_out); they may be given, also as q and k themselves."""
-    lib, st, sh, dev = load_library(), p.st, p.shapes, q.device
-    on = _On(stream, dev)
-    if q_out is None:
-        q_out = on.empty(sh["q"], p.dtype, dev)
-    if k_out is None and k is not None:
-        k_out = on.empty(sh["k"], p.dtype, dev)
-    args = [None if t is None else _expect(t, name, sh[name[0]], p.dtype, dev, True)
-            for t, name in ((q, "q"), (k, "k"), (q_out, "q_out"), (k_out, "k_out"))]
-    st.q_stride, st.qo_stride = _token_stride(q), _token_stride(q_out)
-    st.k_stride, st.ko_stride = (0, 0) if k is None else (_token_stride(k), _token_stride(k_out))
-    _check(lib.gdn_qk_rope_fwd(p.ref(), *args[:2], *_rope_common(p, positions, freqs, q_weight, k_weight, dev),
-                               *args[2:], on.handle))
-    return q_out, k_out
+    return _call("rope_fwd", q, stream, p.at, q, k, positions, freqs, q_weight, k_weight, q_out, k_out)
 
 
 def gdn_qk_rope_bwd(p: QkRopeProblem, q, k, positions, freqs, dq_out, dk_out, q_weight=None, k_weight=None, grads=None,
                     workspace=None, stream=None) -> Dict[str, torch.Tensor]:
     """Backward of gdn_qk_rope_fwd (q and k may be None with norm "none"): returns dict dq, dk,
     dq_weight, dk_weight (None without the weight). `grads` may name any of the buffers."""
-    lib, st, sh, dev, f32 = load_library(), p.st, p.shapes, dq_out.device, torch.float32
-    on = _On(stream, dev)
-    grads = dict(grads or {})
-    for name, like, shape in (("dq", dq_out, sh["q"]), ("dk", dk_out, sh["k"])):
-        if grads.get(name) is None:
-            grads[name] = None if like is None else on.empty(shape, p.dtype, dev)
-    for name, w in (("dq_weight", q_weight), ("dk_weight", k_weight)):
-        if w is None:
-            grads[name] = None
-        elif grads.get(name) is None:
-            grads[name] = on.empty(sh["w"], f32, dev)
-    if workspace is None and (q_weight is not None or k_weight is not None):
-        workspace = on.empty((gdn_qk_rope_workspace_bytes(p),), torch.uint8, dev)
-    ts = dict(q=q, k=k, dq_out=dq_out, dk_out=dk_out, dq=grads["dq"], dk=grads["dk"])
-    ptr = {n: None if t is None else _expect(t, n, sh["q" if "q" in n else "k"], p.dtype, dev, True)
-           for n, t in ts.items()}
-    st.q_stride, st.k_stride, st.qo_stride, st.ko_stride, st.dq_stride, st.dk_stride = (
-        0 if t is None else _token_stride(t) for t in ts.values())
-    _check(lib.gdn_qk_rope_bwd(p.ref(), ptr["q"], ptr["k"], *_rope_common(p, positions, freqs, q_weight, k_weight, dev),
-                               ptr["dq_out"], ptr["dk_out"], ptr["dq"], ptr["dk"],
-                               _given(grads["dq_weight"], "dq_weight", sh["w"], f32, dev),
-                               _given(grads["dk_weight"], "dk_weight", sh["w"], f32, dev), _ptr(workspace),
-                               0 if workspace is None else workspace.numel(), on.handle))
-    return grads
+    g = grads or {}
+    dq, dk, dwq, dwk = _call("rope_bwd", dq_out, stream, p.at, q, k, positions, freqs, q_weight, k_weight, dq_out, dk_out,
+                             g.get("dq"), g.get("dk"), g.get("dq_weight"), g.get("dk_weight"), workspace)
+    return dict(dq=dq, dk=dk, dq_weight=dwq, dk_weight=dwk)

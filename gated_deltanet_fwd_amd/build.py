@@ -1,6 +1,7 @@
-"""Builds libgdn.so (the HIP kernels and the C ABI of include/gdn.h) for gfx950 with hipcc.
+"""Builds libgdn.so (the HIP kernels and the C ABI of include/gdn.h) for gfx950 with hipcc, and
+_binding.so (native argument marshalling of the serving steps, host code) with g++.
 
-Run as `python -m gated_deltanet_fwd_amd.build`; the library lands next to this file.
+Run as `python -m gated_deltanet_fwd_amd.build`; both land next to this file.
 """
 from __future__ import annotations
 
@@ -8,11 +9,13 @@ import concurrent.futures as cf
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libgdn.so")
+BINDING = os.path.join(HERE, "_binding.so")
 BUILD = os.path.join(HERE, "_build")
 SOURCES = ["gdn_fwd.hip", "gdn_bwd.hip", "gdn_api.cpp", "gdn_static.hip", "gdn_conv.hip", "gdn_conv_step.hip",
            "gdn_recurrent.hip", "gdn_rope.hip"]
@@ -39,15 +42,36 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_binding() -> None:
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           "-I", os.path.join(ROOT, "include"), "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(home, "include"), "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           "-I", os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "include"),
+           os.path.join(CSRC, "gdn_binding.cpp"), "-o", tmp,
+           "-L", os.path.join(home, "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("g++ failed on gdn_binding.cpp")
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        binding = ex.submit(_build_binding)
         objs = list(ex.map(_compile, SOURCES))
+        binding.result()
     tmp = OUT + ".tmp%d" % os.getpid()
     subprocess.check_call([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp])
     os.replace(tmp, OUT)
     if verbose:
-        print("built", OUT)
+        print("built", OUT, BINDING)
     return OUT
 
 

@@ -147,3 +147,14 @@ def test_problems_of_no_tokens_need_no_tensors():
 def test_other_types_are_refused(make):
     with pytest.raises(G.GdnError, match="unsupported dtype"):
         make(torch.float16)
+
+
+def test_native_binding_checks_tensors():
+    """The native marshalling is built, and refuses what is not a GPU tensor before anything else."""
+    x = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(G.GdnError, match="expected a GPU"):
+        G.gdn_recurrent(G.RecurrentProblem(3, 2, 2, 64, 8), x, x, x, x, x, x, x, x)
+    with pytest.raises(G.GdnError, match="not a tensor"):
+        G.gdn_qk_rope_fwd(G.QkRopeProblem(3, 2, 2, 64), None, x, x, x)
+    with pytest.raises(G.GdnError, match="expected a GPU"):
+        G.gdn_conv_step(G.ConvStepProblem(3, [128], 8), x, x, None, x, x, x)
