@@ -1250,22 +1250,15 @@ int check_rope(const gdn_qk_rope_problem* p) {
   if (!(p->eps >= 0.f) || !std::isfinite(p->eps)) return fail(GDN_EINVAL, "eps must be >= 0");
   if (!std::isfinite(p->magnitude)) return fail(GDN_EINVAL, "magnitude must be finite");
   if (p->reserved0 != 0) return fail(GDN_EINVAL, "reserved0 must be 0");
-  if (p->n_tokens > (int64_t)0x7fffffff) return fail(GDN_EINVAL, "too many tokens for one call");
+  if (p->n_tokens > (int64_t)0x7ff00000) return fail(GDN_EINVAL, "too many tokens for one call");
   return GDN_OK;
 }
 
-// Sizes, strides and the arrays both directions read.
+// Sizes and the arrays both directions read.
 int rope_args(gdn::RopeArgs& a, const gdn_qk_rope_problem* p, const int32_t* positions, const uint64_t* freqs,
-              const float* q_weight, const float* k_weight) {
+              const float* q_weight, const float* k_weight, bool bwd) {
   std::memset(&a, 0, sizeof a);
   CHECK(check_rope(p));
-  const int64_t nq = (int64_t)p->h_q * p->d, nk = (int64_t)p->h_k * p->d;
-  CHECK(token_stride(p->q_stride, nq, p->dtype, "q_stride", &a.qs));
-  CHECK(token_stride(p->k_stride, nk, p->dtype, "k_stride", &a.ks));
-  CHECK(token_stride(p->qo_stride, nq, p->dtype, "qo_stride", &a.qos));
-  CHECK(token_stride(p->ko_stride, nk, p->dtype, "ko_stride", &a.kos));
-  CHECK(token_stride(p->dq_stride, nq, p->dtype, "dq_stride", &a.dqs));
-  CHECK(token_stride(p->dk_stride, nk, p->dtype, "dk_stride", &a.dks));
   if (p->rotary_dim > 0) {
     CHECK(check_tok(positions, "positions", p->n_tokens));
     CHECK(check_ptr(freqs, "freqs"));
@@ -1274,9 +1267,7 @@ int rope_args(gdn::RopeArgs& a, const gdn_qk_rope_problem* p, const int32_t* pos
   if (q_weight) CHECK(check_ptr(q_weight, "q_weight"));
   if (k_weight) CHECK(check_ptr(k_weight, "k_weight"));
   if (k_weight && p->h_k == 0) return fail(GDN_EINVAL, "k_weight is given but h_k = 0");
-  a.T = p->n_tokens;
-  a.hq = p->h_q;
-  a.hk = p->h_k;
+  a.T = (int)p->n_tokens;
   a.D = p->d;
   a.RD = p->rotary_dim;
   a.norm = p->norm;
@@ -1285,9 +1276,29 @@ int rope_args(gdn::RopeArgs& a, const gdn_qk_rope_problem* p, const int32_t* pos
   a.mag = p->magnitude;
   a.pos = positions;
   a.freq = freqs;
-  a.wq = q_weight;
-  a.wk = k_weight;
+  gdn::RopeSide &q = a.side[0], &k = a.side[1];
+  q.heads = p->h_q;
+  k.heads = p->h_k;
+  q.w = q_weight;
+  k.w = k_weight;
+  const int64_t nq = (int64_t)p->h_q * p->d, nk = (int64_t)p->h_k * p->d;
+  CHECK(token_stride(p->q_stride, nq, p->dtype, "q_stride", &q.xs));
+  CHECK(token_stride(p->k_stride, nk, p->dtype, "k_stride", &k.xs));
+  CHECK(token_stride(p->qo_stride, nq, p->dtype, "qo_stride", bwd ? &q.dys : &q.outs));
+  CHECK(token_stride(p->ko_stride, nk, p->dtype, "ko_stride", bwd ? &k.dys : &k.outs));
+  if (bwd) {
+    CHECK(token_stride(p->dq_stride, nq, p->dtype, "dq_stride", &q.outs));
+    CHECK(token_stride(p->dk_stride, nk, p->dtype, "dk_stride", &k.outs));
+  }
+  for (const gdn::RopeSide& s : a.side) // the kernels' offsets inside a few tokens are 32-bit
+    if (std::max(std::max(s.xs, s.dys), s.outs) > (int64_t)1 << 27)
+      return fail(GDN_EINVAL, "token strides must be at most 2^27 elements");
+  gdn::rope_shape(a, bwd);
   return GDN_OK;
+}
+
+size_t rope_workspace(const gdn::RopeArgs& a) {
+  return align_up((size_t)std::max(a.side[0].blocks + a.side[1].blocks, 1) * a.D * 4);
 }
 
 } // namespace
@@ -1296,25 +1307,31 @@ extern "C" {
 
 size_t gdn_qk_rope_workspace_bytes(const gdn_qk_rope_problem* p) {
   if (check_rope(p) != GDN_OK) return 0;
-  const int blocks = p->n_tokens ? gdn::rope_bwd_blocks(p->n_tokens, p->h_q + p->h_k, p->d) : 1;
-  return align_up((size_t)blocks * 2 * p->d * 4);
+  gdn::RopeArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.T = (int)p->n_tokens;
+  a.D = p->d;
+  a.side[0].heads = p->h_q;
+  a.side[1].heads = p->h_k;
+  gdn::rope_shape(a, true);
+  return rope_workspace(a);
 }
 
 int gdn_qk_rope_fwd(const gdn_qk_rope_problem* p, const void* q, const void* k, const int32_t* positions,
                     const uint64_t* freqs, const float* q_weight, const float* k_weight, void* q_out, void* k_out,
                     void* stream) {
   gdn::RopeArgs a;
-  CHECK(rope_args(a, p, positions, freqs, q_weight, k_weight));
+  CHECK(rope_args(a, p, positions, freqs, q_weight, k_weight, false));
   const int64_t T = p->n_tokens, Tk = p->h_k ? T : 0;
   CHECK(check_tok(q, "q", T));
   CHECK(check_tok(k, "k", Tk));
   CHECK(check_tok(q_out, "q_out", T));
   CHECK(check_tok(k_out, "k_out", Tk));
-  a.q = q;
-  a.k = k;
-  a.qo = q_out;
-  a.ko = k_out;
-  LAUNCH("gdn_qk_rope_fwd", gdn::launch_rope_fwd(a, p->dtype, stream));
+  a.side[0].x = q;
+  a.side[1].x = k;
+  a.side[0].out = q_out;
+  a.side[1].out = k_out;
+  LAUNCH("gdn_qk_rope_fwd", gdn::launch_rope(a, false, p->dtype, stream));
   g_err.clear();
   return GDN_OK;
 }
@@ -1324,7 +1341,7 @@ int gdn_qk_rope_bwd(const gdn_qk_rope_problem* p, const void* q, const void* k, 
                     const void* dk_out, void* dq, void* dk, float* dq_weight, float* dk_weight, void* workspace,
                     size_t workspace_bytes, void* stream) {
   gdn::RopeArgs a;
-  CHECK(rope_args(a, p, positions, freqs, q_weight, k_weight));
+  CHECK(rope_args(a, p, positions, freqs, q_weight, k_weight, true));
   const int64_t T = p->n_tokens, Tk = p->h_k ? T : 0;
   if (p->norm != GDN_NORM_NONE) {
     CHECK(check_tok(q, "q", T));
@@ -1340,20 +1357,21 @@ int gdn_qk_rope_bwd(const gdn_qk_rope_problem* p, const void* q, const void* k, 
   if (dk_weight) CHECK(check_ptr(dk_weight, "dk_weight"));
   if (q_weight || k_weight) {
     CHECK(check_ptr(workspace, "workspace"));
-    if (workspace_bytes < gdn_qk_rope_workspace_bytes(p))
-      return fail(GDN_EWORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes,
-                  gdn_qk_rope_workspace_bytes(p));
+    if (workspace_bytes < rope_workspace(a))
+      return fail(GDN_EWORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, rope_workspace(a));
   }
-  a.q = q;
-  a.k = k;
-  a.dqo = dq_out;
-  a.dko = dk_out;
-  a.dq = dq;
-  a.dk = dk;
-  a.dwq = dq_weight;
-  a.dwk = dk_weight;
+  const void* x[2] = {q, k};
+  const void* dy[2] = {dq_out, dk_out};
+  void* dx[2] = {dq, dk};
+  float* dw[2] = {dq_weight, dk_weight};
+  for (int i = 0; i < 2; ++i) {
+    a.side[i].x = x[i];
+    a.side[i].dy = dy[i];
+    a.side[i].out = dx[i];
+    a.side[i].dw = dw[i];
+  }
   a.part = (float*)workspace;
-  LAUNCH("gdn_qk_rope_bwd", gdn::launch_rope_bwd(a, p->dtype, stream));
+  LAUNCH("gdn_qk_rope_bwd", gdn::launch_rope(a, true, p->dtype, stream));
   g_err.clear();
   return GDN_OK;
 }

@@ -203,32 +203,28 @@ struct RecurrentArgs {
 };
 int launch_recurrent(const RecurrentArgs& a, int dtype, void* stream);
 
-// Norms of the q and k heads with the position rotation (gdn_rope.hip).
+// Norms of the q and k heads with the position rotation (gdn_rope.hip). Side 0 is q, side 1 k.
+struct RopeSide {
+  const void* x;   // the forward's input
+  const void* dy;  // the backward's upstream gradient
+  void* out;       // the forward's output, the backward's gradient of x
+  const float* w;  // NULL: ones
+  float* dw;       // NULL: not wanted
+  int64_t xs, dys, outs; // elements between their tokens
+  int heads;
+  // set by rope_shape: tokens whose rows are taken together, passes over such a group's rows, how
+  // many of them a wave makes, in how many chunks that cuts a group, and the side's workgroups
+  int tpp, passes, per, chunks, blocks;
+};
 struct RopeArgs {
-  int64_t T;                           // tokens
-  int64_t qs, ks, qos, kos, dqs, dks; // elements between the tokens of q, k, q_out/dq_out, k_out/dk_out, dq, dk
-  int hq, hk, D, RD, norm, interleaved;
-  int hc; // heads per unit of work (one token's heads are cut into units)
+  int T, D, RD, norm, interleaved;
   float eps, mag;
-  const void* q;
-  const void* k;
   const int32_t* pos;
   const uint64_t* freq;
-  const float* wq;
-  const float* wk;
-  void* qo;
-  void* ko;
-  const void* dqo;
-  const void* dko;
-  void* dq;
-  void* dk;
-  float* dwq;
-  float* dwk;
-  float* part; // [blocks][2][D] partial sums of the weight gradients
+  RopeSide side[2];
+  float* part; // [blocks of both sides][D] partial sums of the weight gradients
 };
-// Workgroups of the backward (the rows of `part`), and the launches.
-int rope_bwd_blocks(int64_t T, int heads, int D);
-int launch_rope_fwd(const RopeArgs& a, int dtype, void* stream);
-int launch_rope_bwd(const RopeArgs& a, int dtype, void* stream);
+void rope_shape(RopeArgs& a, bool bwd);
+int launch_rope(const RopeArgs& a, bool bwd, int dtype, void* stream);
 
 } // namespace gdn

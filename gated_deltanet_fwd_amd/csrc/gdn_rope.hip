@@ -4,31 +4,48 @@
 //   n = x r,  z = n w,  y = m R(p f) z           (R turns the pairs of the first RD values)
 //   dz = m R(-p f) dy,  dn = dz w,  dw = sum dz n,  dx = r (dn - c n (n.dn))
 //
-// A row is held by a group of 8, 16 or 32 lanes, 8 values a lane. With pairs half the rotary dim
-// apart a lane takes 4 consecutive values of each half, so that both values of a pair and the 4
-// frequencies it needs are in the lane in both layouts. A group takes one token and `hc` of its
-// q/k heads, so the token's cosines and sines are computed once for all of them.
+// A row is held by 8, 16 or 32 lanes, 8 values a lane: 4 consecutive ones of each half of the
+// rotated part (or of the part that passes), so that both values of a pair are in one lane in both
+// layouts. A wave takes a token's q or its k heads (or some of them) and goes through their rows, 512
+// values a pass, so the lanes of an access lie next to each other (with the rows of 4 tokens in one
+// access 32,768 tokens of 16 + 16 heads moved 3.9 TB/s instead of 5.5). The next pass's rows are
+// loaded while one is computed. What bounds both directions is memory.
 //
 // The angle is exact: a frequency is a 64-bit fraction of a turn per position, and the product with
 // the position modulo 2^64 drops whole turns. Its top 32 bits give the quadrant and a remainder of
 // at most 1/8 turn, where the Taylor polynomials of sine and cosine to x^9 and x^10 are off by less
 // than 2e-9 and 2e-10.
+#include <algorithm>
+
 #include "gdn_device.h"
 
 namespace gdn {
 
+// Waves that a short call is cut into, and that a long one has at most (see rope_shape).
+constexpr int64_t FWD_FILL = 8192, FWD_MOST = 32768, BWD_FILL = 4096, BWD_MOST = 4096;
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_of(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
+}
+
+// Sum over a row's LPR lanes, in every lane.
 template <int LPR>
 __device__ __forceinline__ float group_sum(float x) {
-  const auto dpp = [](float v, auto ctrl) {
-    return __builtin_bit_cast(
-        float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), decltype(ctrl)::value, 0xf, 0xf, false));
-  };
-  x += dpp(x, std::integral_constant<int, 0xB1>{});  // lane ^ 1
-  x += dpp(x, std::integral_constant<int, 0x4E>{});  // lane ^ 2
-  x += dpp(x, std::integral_constant<int, 0x141>{}); // 7 - lane within 8: the other quad
-  if constexpr (LPR >= 16) x += dpp(x, std::integral_constant<int, 0x140>{}); // 15 - lane within 16
+  x += dpp_of<0xB1>(x);  // lane ^ 1
+  x += dpp_of<0x4E>(x);  // lane ^ 2
+  x += dpp_of<0x141>(x); // 7 - lane within 8: the other quad
+  if constexpr (LPR >= 16) x += dpp_of<0x140>(x); // 15 - lane within 16
   if constexpr (LPR >= 32) x += __shfl_xor(x, 16);
   return x;
+}
+
+// 1 / sqrt(x): the hardware's estimate (1 ulp) and one Newton step.
+__device__ __forceinline__ float inv_sqrt(float x) {
+  const float r = __builtin_amdgcn_rsqf(x);
+  const float h = 0.5f * x * r;
+  const float y = __builtin_fmaf(__builtin_fmaf(-h, r, 0.5f), r, r);
+  return __builtin_isfinite(r) && r != 0.f ? y : r; // at 0, infinity and NaN the step has nothing to add
 }
 
 // cos and sin of the angle pos * freq (freq in 2^-64 turns).
@@ -51,9 +68,10 @@ __device__ __forceinline__ void turn_cs(int pos, uint64_t freq, float& c, float&
   s = quad & 2 ? -ss : ss;       // quadrants 2 and 3
 }
 
-// Where a lane's 8 values lie in a row: values 0..3 at o1, 4..7 at o2.
+// Where a lane's 8 values lie in a row: values 0..3 at o1, 4..7 at o2, and the indices of its four
+// pairs' frequencies: f1, f1 + 1 and f2, f2 + 1.
 struct RowMap {
-  int o1, o2;
+  int o1, o2, f1, f2;
   bool on, rot;
 };
 template <bool HALF>
@@ -61,58 +79,39 @@ __device__ __forceinline__ RowMap row_map(int j, int D, int RD) {
   RowMap m;
   m.on = 8 * j < D;
   m.rot = 8 * j < RD;
-  m.o1 = HALF && m.rot ? 4 * j : 8 * j;
-  m.o2 = HALF && m.rot ? RD / 2 + 4 * j : 8 * j + 4;
+  const int k = m.rot ? j : j - RD / 8, from = m.rot ? 0 : RD, size = m.rot ? RD : D - RD;
+  m.o1 = from + 4 * k;
+  m.o2 = m.o1 + size / 2;
+  m.f1 = HALF ? 4 * j : 2 * j;
+  m.f2 = HALF ? 4 * j + 2 : RD / 4 + 2 * j;
   return m;
 }
 
+// A lane's 8 values as they are stored.
 template <typename TI>
-__device__ __forceinline__ void load4f(const TI* p, float* v) {
+struct Raw {
   typedef TI vec __attribute__((ext_vector_type(4)));
-  const vec r = *reinterpret_cast<const vec*>(p);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] = (float)r[e];
-}
-
-template <typename TI, bool HALF>
-__device__ __forceinline__ void load_row(const TI* p, const RowMap& m, float v[8]) {
-  if (!m.on) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 0.f;
-  } else if constexpr (HALF) {
-    load4f(p + m.o1, v);
-    load4f(p + m.o2, v + 4);
-  } else {
-    IO<TI>::load8f(p + m.o1, v);
+  vec a, b;
+  __device__ __forceinline__ void load(const TI* p, const RowMap& m) { // lanes past the row: its first values
+    a = *reinterpret_cast<const vec*>(p + (m.on ? m.o1 : 0));
+    b = *reinterpret_cast<const vec*>(p + (m.on ? m.o2 : 4));
   }
-}
+  __device__ __forceinline__ void unpack(float v[8], bool on) const {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = on ? (float)a[e] : 0.f;
+      v[4 + e] = on ? (float)b[e] : 0.f;
+    }
+  }
+};
 
-template <typename TI, bool HALF>
+template <typename TI>
 __device__ __forceinline__ void store_row(TI* p, const RowMap& m, const float v[8]) {
-  if (!m.on) return;
-  if constexpr (HALF) {
-    IO<TI>::store4(p + m.o1, v);
-    IO<TI>::store4(p + m.o2, v + 4);
-  } else if constexpr (sizeof(TI) == 2) {
-    bf16x8 r;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) r[e] = (bf16)v[e];
-    *reinterpret_cast<bf16x8*>(p + m.o1) = r;
-  } else {
-    IO<TI>::store4(p + m.o1, v);
-    IO<TI>::store4(p + m.o2, v + 4);
-  }
+  IO<TI>::store4(p + m.o1, v);
+  IO<TI>::store4(p + m.o2, v + 4);
 }
 
-__device__ __forceinline__ void load_weight(const float* w, const RowMap& m, float v[8]) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    v[e] = w && m.on ? w[m.o1 + e] : 1.f;
-    v[4 + e] = w && m.on ? w[m.o2 + e] : 1.f;
-  }
-}
-
-// The lane's 4 pairs turned by (c, s); sign -1: turned back.
+// The lane's 4 pairs turned by (c, s).
 template <bool HALF>
 __device__ __forceinline__ void rotate(float v[8], const float c[4], const float s[4]) {
 #pragma unroll
@@ -124,221 +123,330 @@ __device__ __forceinline__ void rotate(float v[8], const float c[4], const float
   }
 }
 
-// The 4 angles of a lane at position pos; lanes that rotate nothing get the identity.
-__device__ __forceinline__ void lane_angles(const RopeArgs& a, const RowMap& m, int j, int64_t t, float back,
-                                            float c[4], float s[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    c[i] = 1.f;
-    s[i] = 0.f;
-  }
+// x of the lanes with the same lane % 16 (rows 0..3) or lane % 32 (rows 0, 1), in every lane. The
+// lane swaps exchange x's odd 16-lane rows (or its upper half) with y's even ones; the copies keep
+// the compiler from folding a swap of one value with itself away.
+__device__ __forceinline__ void gather_rows(float x, float out[4]) {
+  unsigned a = __builtin_bit_cast(unsigned, x), b = a;
+  asm("" : "+v"(b));
+  const auto s = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  unsigned e = s[0], e2 = s[0], o = s[1], o2 = s[1];
+  asm("" : "+v"(e2), "+v"(o2));
+  const auto p = __builtin_amdgcn_permlane32_swap(e, e2, false, false), q = __builtin_amdgcn_permlane32_swap(o, o2, false, false);
+  out[0] = __builtin_bit_cast(float, (unsigned)p[0]);
+  out[1] = __builtin_bit_cast(float, (unsigned)q[0]);
+  out[2] = __builtin_bit_cast(float, (unsigned)p[1]);
+  out[3] = __builtin_bit_cast(float, (unsigned)q[1]);
+}
+__device__ __forceinline__ void gather_halves(float x, float out[2]) {
+  unsigned a = __builtin_bit_cast(unsigned, x), b = a;
+  asm("" : "+v"(b));
+  const auto s = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  out[0] = __builtin_bit_cast(float, (unsigned)s[0]);
+  out[1] = __builtin_bit_cast(float, (unsigned)s[1]);
+}
+
+// A lane's frequencies and angles. Where a pass holds one token, the lanes that share the four pairs
+// of position j divide them (one each of four lane rows, or two each of two halves) and exchange the
+// cosines and sines; where it holds several, each lane makes its four.
+template <int LPR>
+__device__ __forceinline__ void lane_freqs(const RopeArgs& a, const RowMap& m, bool one, uint64_t f[4]) {
+  f[0] = f[1] = f[2] = f[3] = 0;
   if (!m.rot) return;
-  const int pos = a.pos[t];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    turn_cs(pos, a.freq[4 * j + i], c[i], s[i]);
-    c[i] *= a.mag;
-    s[i] *= a.mag * back;
+  const int lane = threadIdx.x & 63;
+  if (!one) {
+    f[0] = a.freq[m.f1];
+    f[1] = a.freq[m.f1 + 1];
+    f[2] = a.freq[m.f2];
+    f[3] = a.freq[m.f2 + 1];
+  } else if constexpr (LPR <= 16) {
+    const int i = lane >> 4;
+    f[0] = a.freq[(i < 2 ? m.f1 : m.f2) + (i & 1)];
+  } else {
+    const int at = lane < 32 ? m.f1 : m.f2;
+    f[0] = a.freq[at];
+    f[1] = a.freq[at + 1];
   }
+}
+
+// The lane's 4 angles at position pos (lanes that rotate nothing get values that are not used).
+template <int LPR>
+__device__ __forceinline__ void lane_angles(const RopeArgs& a, const uint64_t f[4], bool one, int pos, float back,
+                                            float c[4], float s[4]) {
+  float x, y;
+  if (!one) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      turn_cs(pos, f[i], x, y);
+      c[i] = x * a.mag;
+      s[i] = y * a.mag * back;
+    }
+    return;
+  }
+  turn_cs(pos, f[0], x, y);
+  if constexpr (LPR <= 16) {
+    gather_rows(x * a.mag, c);
+    gather_rows(y * a.mag * back, s);
+  } else {
+    float t[2], u[2];
+    gather_halves(x * a.mag, t);
+    gather_halves(y * a.mag * back, u);
+    c[0] = t[0], c[2] = t[1], s[0] = u[0], s[2] = u[1];
+    turn_cs(pos, f[1], x, y);
+    gather_halves(x * a.mag, t);
+    gather_halves(y * a.mag * back, u);
+    c[1] = t[0], c[3] = t[1], s[1] = u[0], s[3] = u[1];
+  }
+}
+
+__device__ __forceinline__ void load_weight(const float* w, const RowMap& m, float v[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = 1.f;
+  if (!w || !m.on) return;
+  const f32x4 x = *reinterpret_cast<const f32x4*>(w + m.o1), y = *reinterpret_cast<const f32x4*>(w + m.o2);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = x[e], v[4 + e] = y[e];
+}
+
+// A wave's work: passes [p0, p1) over the rows of the token groups t, t + dt, ... of its side. A pass
+// takes 64 / LPR rows: of one token, or with fewer heads than that, the heads of `tpp` tokens
+// (lane group g then holds head `head` of the group's token `tok`).
+struct Share {
+  int t, dt, p0, p1, groups, head, tok;
+};
+template <int LPR>
+__device__ __forceinline__ Share share_of(const RopeArgs& a, const RopeSide& s, int block) {
+  const int wave = block * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = wave % s.chunks, g = (threadIdx.x & 63) / LPR;
+  Share sh;
+  sh.t = wave / s.chunks;
+  sh.dt = s.blocks * 4 / s.chunks;
+  sh.p0 = c * s.per;
+  sh.p1 = min(sh.p0 + s.per, s.passes);
+  sh.groups = (a.T - 1) / s.tpp + 1;
+  sh.head = g & ((64 / LPR / s.tpp) - 1);
+  sh.tok = g / (64 / LPR / s.tpp);
+  return sh;
+}
+// A lane's row in pass i over token group t, from the start of the group's first token: offsets
+// inside a group are 32-bit (the host checks the strides); rows and tokens past the end are cut.
+template <int LPR>
+__device__ __forceinline__ int row_at(const RopeArgs& a, const RopeSide& s, const Share& sh, int t, int i, int64_t stride) {
+  return min(sh.tok, a.T - 1 - t * s.tpp) * (int)stride + min(i * (64 / LPR) + sh.head, s.heads - 1) * a.D;
+}
+__device__ __forceinline__ int pos_at(const RopeArgs& a, const RopeSide& s, const Share& sh, int t) {
+  return a.RD ? a.pos[min(t * s.tpp + sh.tok, a.T - 1)] : 0;
 }
 
 template <typename TI, int LPR, bool HALF>
 __global__ __launch_bounds__(256) void k_rope_fwd(RopeArgs a) {
-  constexpr int GPB = 256 / LPR;
-  const int j = threadIdx.x % LPR;
-  const int64_t t = (int64_t)blockIdx.x * GPB + threadIdx.x / LPR;
-  if (t >= a.T) return;
-  const RowMap m = row_map<HALF>(j, a.D, a.RD);
-  float c[4], s[4];
-  lane_angles(a, m, j, t, 1.f, c, s);
-  const int heads = a.hq + a.hk, h0 = blockIdx.y * a.hc, h1 = min(h0 + a.hc, heads);
+  constexpr int RPW = 64 / LPR;
+  const int side = (int)blockIdx.x >= a.side[0].blocks;
+  const RopeSide sd = a.side[side];
+  Share sh = share_of<LPR>(a, sd, blockIdx.x - (side ? a.side[0].blocks : 0));
+  if (sh.t >= sh.groups) return;
+  const RowMap m = row_map<HALF>((threadIdx.x & 63) % LPR, a.D, a.RD);
+  const auto load = [&](Raw<TI>& r, int t, int i) {
+    r.load((const TI*)sd.x + (int64_t)t * sd.tpp * sd.xs + row_at<LPR>(a, sd, sh, t, i, sd.xs), m);
+  };
+  Raw<TI> cur, next;
+  load(cur, sh.t, sh.p0);
+  int pos = pos_at(a, sd, sh, sh.t);
+  const bool one = sd.tpp == 1;
+  uint64_t f[4];
+  lane_freqs<LPR>(a, m, one, f);
+  float w[8];
+  load_weight(sd.w, m, w);
   const float mean = a.norm == 2 ? 1.f / a.D : 1.f;
-  const auto run = [&](const TI* x, TI* y, const float* w, int lo, int hi) {
-    if (lo >= hi) return;
-    float wt[8];
-    load_weight(w, m, wt);
-    for (int h = lo; h < hi; ++h) {
+  for (; sh.t < sh.groups; sh.t += sh.dt) {
+    const int tn = min(sh.t + sh.dt, sh.groups - 1);
+    float c[4], s[4];
+    lane_angles<LPR>(a, f, one, pos, 1.f, c, s);
+    pos = pos_at(a, sd, sh, tn);
+    for (int i = sh.p0; i < sh.p1; ++i) {
+      const bool more = i + 1 < sh.p1;
+      load(next, more ? sh.t : tn, more ? i + 1 : sh.p0);
       float v[8];
-      load_row<TI, HALF>(x + (int64_t)h * a.D, m, v);
+      cur.unpack(v, m.on);
       if (a.norm) {
         float ss = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(v[e], v[e], ss);
-        const float r = 1.f / sqrtf(__builtin_fmaf(group_sum<LPR>(ss), mean, a.eps));
+        const float r = inv_sqrt(__builtin_fmaf(group_sum<LPR>(ss), mean, a.eps));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= r * wt[e];
+        for (int e = 0; e < 8; ++e) v[e] *= r * w[e];
       }
       if (m.rot) rotate<HALF>(v, c, s);
-      store_row<TI, HALF>(y + (int64_t)h * a.D, m, v);
+      if (m.on && i * RPW + sh.head < sd.heads && sh.t * sd.tpp + sh.tok < a.T)
+        store_row((TI*)sd.out + (int64_t)sh.t * sd.tpp * sd.outs + row_at<LPR>(a, sd, sh, sh.t, i, sd.outs), m, v);
+      cur = next;
     }
-  };
-  run((const TI*)a.q + t * a.qs, (TI*)a.qo + t * a.qos, a.wq, h0, min(h1, a.hq));
-  run((const TI*)a.k + t * a.ks, (TI*)a.ko + t * a.kos, a.wk, max(h0 - a.hq, 0), h1 - a.hq);
+  }
 }
 
+// The weight's gradient is summed in the lane over all its rows, then over the workgroup's lanes in
+// LDS, and over the side's workgroups by k_rope_reduce. (A row that is loaded ahead and not this
+// wave's to compute may be written in place meanwhile: nothing made of it is kept.)
 template <typename TI, int LPR, bool HALF>
 __global__ __launch_bounds__(256) void k_rope_bwd(RopeArgs a) {
-  constexpr int GPB = 256 / LPR;
-  __shared__ float red[256][17];
-  const int j = threadIdx.x % LPR;
-  const RowMap m = row_map<HALF>(j, a.D, a.RD);
-  const int heads = a.hq + a.hk, h0 = blockIdx.y * a.hc, h1 = min(h0 + a.hc, heads);
-  const float mean = a.norm == 2 ? 1.f / a.D : 1.f;
-  float acc[2][8];
+  constexpr int RPW = 64 / LPR, GPB = 256 / LPR;
+  __shared__ float red[256][9];
+  const int side = (int)blockIdx.x >= a.side[0].blocks;
+  const RopeSide sd = a.side[side];
+  Share sh = share_of<LPR>(a, sd, blockIdx.x - (side ? a.side[0].blocks : 0));
+  const RowMap m = row_map<HALF>((threadIdx.x & 63) % LPR, a.D, a.RD);
+  const auto load = [&](Raw<TI>& x, Raw<TI>& d, int t, int i) {
+    d.load((const TI*)sd.dy + (int64_t)t * sd.tpp * sd.dys + row_at<LPR>(a, sd, sh, t, i, sd.dys), m);
+    if (a.norm) x.load((const TI*)sd.x + (int64_t)t * sd.tpp * sd.xs + row_at<LPR>(a, sd, sh, t, i, sd.xs), m);
+  };
+  float sum[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) acc[0][e] = acc[1][e] = 0.f;
-  for (int64_t t = (int64_t)blockIdx.x * GPB + threadIdx.x / LPR; t < a.T; t += (int64_t)gridDim.x * GPB) {
-    float c[4], s[4];
-    lane_angles(a, m, j, t, -1.f, c, s);
-    const auto run = [&](const TI* x, const TI* dy, TI* dx, const float* w, float sum[8], int lo, int hi) {
-      if (lo >= hi) return;
-      float wt[8];
-      load_weight(w, m, wt);
-      for (int h = lo; h < hi; ++h) {
-        float g[8];
-        load_row<TI, HALF>(dy + (int64_t)h * a.D, m, g);
-        if (m.rot) rotate<HALF>(g, c, s);
+  for (int e = 0; e < 8; ++e) sum[e] = 0.f;
+  if (sh.t < sh.groups) {
+    Raw<TI> cx, cd, nx, nd;
+    load(cx, cd, sh.t, sh.p0);
+    int pos = pos_at(a, sd, sh, sh.t);
+    const bool one = sd.tpp == 1;
+    uint64_t f[4];
+    lane_freqs<LPR>(a, m, one, f);
+    float w[8];
+    load_weight(sd.w, m, w);
+    const float mean = a.norm == 2 ? 1.f / a.D : 1.f;
+    for (; sh.t < sh.groups; sh.t += sh.dt) {
+      const int tn = min(sh.t + sh.dt, sh.groups - 1);
+      float c[4], s[4];
+      lane_angles<LPR>(a, f, one, pos, -1.f, c, s);
+      pos = pos_at(a, sd, sh, tn);
+      for (int i = sh.p0; i < sh.p1; ++i) {
+        const bool more = i + 1 < sh.p1;
+        load(nx, nd, more ? sh.t : tn, more ? i + 1 : sh.p0);
+        const bool mine = i * RPW + sh.head < sd.heads && sh.t * sd.tpp + sh.tok < a.T;
+        float d[8];
+        cd.unpack(d, m.on);
+        if (m.rot) rotate<HALF>(d, c, s);
         if (a.norm) {
-          float v[8];
-          load_row<TI, HALF>(x + (int64_t)h * a.D, m, v);
-          float ss = 0.f, vg = 0.f;
+          float v[8], dn[8], ss = 0.f, vd = 0.f;
+          cx.unpack(v, m.on);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
+            dn[e] = d[e] * w[e];
             ss = __builtin_fmaf(v[e], v[e], ss);
-            vg = __builtin_fmaf(v[e], g[e] * wt[e], vg);
+            vd = __builtin_fmaf(v[e], dn[e], vd);
           }
-          const float r = 1.f / sqrtf(__builtin_fmaf(group_sum<LPR>(ss), mean, a.eps));
-          const float k = group_sum<LPR>(vg) * r * r * mean; // c (n . dn) / |x's scale|
+          const float r = inv_sqrt(__builtin_fmaf(group_sum<LPR>(ss), mean, a.eps));
+          const float k = group_sum<LPR>(vd) * r * r * r * mean;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            sum[e] = __builtin_fmaf(g[e], v[e] * r, sum[e]);
-            g[e] = r * (g[e] * wt[e] - k * v[e]);
+            sum[e] = mine ? __builtin_fmaf(d[e], v[e] * r, sum[e]) : sum[e];
+            d[e] = __builtin_fmaf(r, dn[e], -k * v[e]);
           }
         }
-        store_row<TI, HALF>(dx + (int64_t)h * a.D, m, g);
+        if (m.on && mine)
+          store_row((TI*)sd.out + (int64_t)sh.t * sd.tpp * sd.outs + row_at<LPR>(a, sd, sh, sh.t, i, sd.outs), m, d);
+        cx = nx;
+        cd = nd;
       }
-    };
-    run((const TI*)a.q + t * a.qs, (const TI*)a.dqo + t * a.qos, (TI*)a.dq + t * a.dqs, a.wq, acc[0], h0,
-        min(h1, a.hq));
-    run((const TI*)a.k + t * a.ks, (const TI*)a.dko + t * a.kos, (TI*)a.dk + t * a.dks, a.wk, acc[1],
-        max(h0 - a.hq, 0), h1 - a.hq);
+    }
   }
-  if (!a.dwq && !a.dwk) return;
+  if (!sd.dw) return;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    red[threadIdx.x][e] = acc[0][e];
-    red[threadIdx.x][8 + e] = acc[1][e];
-  }
+  for (int e = 0; e < 8; ++e) red[threadIdx.x][e] = sum[e];
   __syncthreads();
-  float* part = a.part + ((size_t)blockIdx.y * gridDim.x + blockIdx.x) * 2 * a.D;
-  for (int i = threadIdx.x; i < LPR * 16; i += 256) {
-    const int jj = i / 16, e = i % 16;
+  if (threadIdx.x < LPR * 8) {
+    const int jj = threadIdx.x / 8, e = threadIdx.x % 8;
     const RowMap mm = row_map<HALF>(jj, a.D, a.RD);
-    if (!mm.on) continue;
     float x = 0.f;
 #pragma unroll
-    for (int g = 0; g < GPB; ++g) x += red[g * LPR + jj][e];
-    const int ee = e & 7;
-    part[(e >> 3) * a.D + (ee < 4 ? mm.o1 + ee : mm.o2 + ee - 4)] = x;
+    for (int k = 0; k < GPB; ++k) x += red[k * LPR + jj][e];
+    if (mm.on) a.part[(size_t)blockIdx.x * a.D + (e < 4 ? mm.o1 + e : mm.o2 + e - 4)] = x;
   }
 }
 
-// dq_weight and dk_weight: the workgroups' partial sums, added in a fixed order: 16 columns a
-// workgroup, 16 slices of the rows each, then the slices.
-__global__ __launch_bounds__(256) void k_rope_reduce(RopeArgs a, int blocks) {
-  __shared__ float red[16][17];
-  const int c = threadIdx.x & 15, s = threadIdx.x >> 4;
-  const int col = blockIdx.x * 16 + c;
+// dq_weight and dk_weight: the workgroups' partial sums, added in a fixed order: 8 columns a
+// workgroup, 128 slices of the rows each, then the slices.
+__global__ __launch_bounds__(1024) void k_rope_reduce(RopeArgs a) {
+  __shared__ float red[128][9];
+  const int c = threadIdx.x & 7, s = threadIdx.x >> 3, side = blockIdx.x * 8 >= a.D;
+  const int col = blockIdx.x * 8 + c - (side ? a.D : 0);
+  const int b0 = side ? a.side[0].blocks : 0, b1 = b0 + a.side[side].blocks;
+  float* dw = a.side[side].dw;
+  if (!dw) return;
   float x = 0.f;
-  if (col < 2 * a.D)
-    for (int b = s; b < blocks; b += 16) x += a.part[(size_t)b * 2 * a.D + col];
+#pragma unroll 8
+  for (int b = b0 + s; b < b1; b += 128) x += a.part[(size_t)b * a.D + col];
   red[s][c] = x;
   __syncthreads();
-  if (s == 0 && col < 2 * a.D) {
-    x = 0.f;
+  if (s != 0) return;
+  x = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x += red[i][c];
-    if (col < a.D) {
-      if (a.dwq) a.dwq[col] = x;
-    } else if (a.dwk) {
-      a.dwk[col - a.D] = x;
-    }
-  }
+  for (int i = 0; i < 128; ++i) x += red[i][c];
+  dw[col] = x;
 }
 
 static int lanes_of(int D) { return D <= 64 ? 8 : D <= 128 ? 16 : 32; }
 
-// Heads per unit of work: all of a token's heads share one set of cosines and sines, but a short
-// call is cut further, down to one head, to keep 2048 waves.
-static int heads_per_unit(int64_t T, int heads, int D) {
-  const int64_t want = 2048 * (64 / lanes_of(D));
-  int64_t hc = (T * heads + want - 1) / want;
-  return (int)(hc < 1 ? 1 : hc > heads ? heads : hc);
+// The grid of a side. A wave takes a token group's passes in turn, loading one ahead. Short calls are
+// cut to `fill` waves over both sides, down to one pass a wave: 4096 tokens of 16 + 16 heads, 128
+// wide, forward, take 12.8 us in 8192 waves, 17 us in 32768, each with its own cosines and sines.
+// Long ones go over the groups with up to `most`, each wave the same number of groups: 32,768 such
+// tokens take 97 us in 32768 waves, 101 us in 8192; backward, where each workgroup leaves a row of
+// partial sums, 154 us in 4096 and 159 us in 8192 or more.
+static void shape_side(RopeSide& s, int64_t T, int D, int all_heads, int64_t fill, int64_t most) {
+  const int rpw = 64 / lanes_of(D);
+  s.tpp = 1;
+  while (s.heads > 0 && s.heads * s.tpp * 2 <= rpw) s.tpp *= 2;
+  s.passes = (s.heads * s.tpp + rpw - 1) / rpw;
+  s.per = s.passes;
+  s.chunks = 1;
+  s.blocks = 0;
+  if (T == 0 || s.heads == 0) return;
+  const int64_t groups = (T + s.tpp - 1) / s.tpp;
+  fill = fill * s.heads / all_heads;
+  most = std::max<int64_t>(most * s.heads / all_heads, 1);
+  if (groups < fill) {
+    const int64_t c = (fill + groups - 1) / groups;
+    s.per = (int)(c >= s.passes ? 1 : (s.passes + c - 1) / c);
+    s.chunks = (s.passes + s.per - 1) / s.per;
+  }
+  const int64_t each = std::max<int64_t>((groups + most / 2) / most, 1); // groups a wave
+  const int64_t waves = (groups + each - 1) / each * s.chunks;
+  // a whole number of token groups a step, so that a wave keeps its place in them
+  s.blocks = (int)((waves + 4 * s.chunks - 1) / (4 * s.chunks)) * s.chunks;
 }
-
-static dim3 bwd_grid(int64_t T, int heads, int D) {
-  const int gpb = 256 / lanes_of(D), hc = heads_per_unit(T, heads, D);
-  int64_t x = (T + gpb - 1) / gpb;
-  if (x > 1024) x = 1024;
-  return dim3((unsigned)(x < 1 ? 1 : x), (heads + hc - 1) / hc);
-}
-
-int rope_bwd_blocks(int64_t T, int heads, int D) {
-  const dim3 g = bwd_grid(T, heads, D);
-  return (int)(g.x * g.y);
+void rope_shape(RopeArgs& a, bool bwd) {
+  for (RopeSide& s : a.side)
+    shape_side(s, a.T, a.D, a.side[0].heads + a.side[1].heads, bwd ? BWD_FILL : FWD_FILL, bwd ? BWD_MOST : FWD_MOST);
 }
 
 template <typename TI, int LPR>
-static int rope_fwd_t(RopeArgs a, hipStream_t s) {
-  const int heads = a.hq + a.hk;
-  a.hc = heads_per_unit(a.T, heads, a.D);
-  const dim3 grid((unsigned)((a.T + 256 / LPR - 1) / (256 / LPR)), (heads + a.hc - 1) / a.hc);
-  if (a.interleaved) hipLaunchKernelGGL((k_rope_fwd<TI, LPR, false>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_rope_fwd<TI, LPR, true>), grid, dim3(256), 0, s, a);
+static int rope_t(const RopeArgs& a, bool bwd, hipStream_t s) {
+  const dim3 grid((unsigned)(a.side[0].blocks + a.side[1].blocks)), blk(256);
+  if (bwd) {
+    if (a.interleaved) hipLaunchKernelGGL((k_rope_bwd<TI, LPR, false>), grid, blk, 0, s, a);
+    else hipLaunchKernelGGL((k_rope_bwd<TI, LPR, true>), grid, blk, 0, s, a);
+  } else {
+    if (a.interleaved) hipLaunchKernelGGL((k_rope_fwd<TI, LPR, false>), grid, blk, 0, s, a);
+    else hipLaunchKernelGGL((k_rope_fwd<TI, LPR, true>), grid, blk, 0, s, a);
+  }
   return (int)hipGetLastError();
 }
 
-template <typename TI, int LPR>
-static int rope_bwd_t(RopeArgs a, hipStream_t s) {
-  const int heads = a.hq + a.hk;
-  a.hc = heads_per_unit(a.T, heads, a.D);
-  const dim3 grid = bwd_grid(a.T, heads, a.D);
-  if (a.interleaved) hipLaunchKernelGGL((k_rope_bwd<TI, LPR, false>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_rope_bwd<TI, LPR, true>), grid, dim3(256), 0, s, a);
-  const int e = (int)hipGetLastError();
-  if (e || (!a.dwq && !a.dwk)) return e;
-  hipLaunchKernelGGL(k_rope_reduce, dim3((2 * a.D + 15) / 16), dim3(256), 0, s, a, (int)(grid.x * grid.y));
+int launch_rope(const RopeArgs& a, bool bwd, int dtype, void* stream) {
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  int e = 0;
+  if (a.T > 0) {
+    switch (lanes_of(a.D) + (dtype == 0 ? 0 : 1)) {
+      case 8: e = rope_t<bf16, 8>(a, bwd, s); break;
+      case 9: e = rope_t<float, 8>(a, bwd, s); break;
+      case 16: e = rope_t<bf16, 16>(a, bwd, s); break;
+      case 17: e = rope_t<float, 16>(a, bwd, s); break;
+      case 32: e = rope_t<bf16, 32>(a, bwd, s); break;
+      default: e = rope_t<float, 32>(a, bwd, s); break;
+    }
+  }
+  if (e || (!a.side[0].dw && !a.side[1].dw)) return e;
+  hipLaunchKernelGGL(k_rope_reduce, dim3(2 * a.D / 8), dim3(1024), 0, s, a); // no tokens: zeros
   return (int)hipGetLastError();
-}
-
-int launch_rope_fwd(const RopeArgs& a, int dtype, void* stream) {
-  if (a.T == 0) return 0;
-  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  switch (lanes_of(a.D) + (dtype == 0 ? 0 : 1)) {
-    case 8: return rope_fwd_t<bf16, 8>(a, s);
-    case 9: return rope_fwd_t<float, 8>(a, s);
-    case 16: return rope_fwd_t<bf16, 16>(a, s);
-    case 17: return rope_fwd_t<float, 16>(a, s);
-    case 32: return rope_fwd_t<bf16, 32>(a, s);
-    default: return rope_fwd_t<float, 32>(a, s);
-  }
-}
-
-int launch_rope_bwd(const RopeArgs& a, int dtype, void* stream) {
-  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  if (a.T == 0) { // no tokens: the weight gradients are zero
-    if (!a.dwq && !a.dwk) return 0;
-    hipLaunchKernelGGL(k_rope_reduce, dim3((2 * a.D + 15) / 16), dim3(256), 0, s, a, 0);
-    return (int)hipGetLastError();
-  }
-  switch (lanes_of(a.D) + (dtype == 0 ? 0 : 1)) {
-    case 8: return rope_bwd_t<bf16, 8>(a, s);
-    case 9: return rope_bwd_t<float, 8>(a, s);
-    case 16: return rope_bwd_t<bf16, 16>(a, s);
-    case 17: return rope_bwd_t<float, 16>(a, s);
-    case 32: return rope_bwd_t<bf16, 32>(a, s);
-    default: return rope_bwd_t<float, 32>(a, s);
-  }
 }
 
 } // namespace gdn
