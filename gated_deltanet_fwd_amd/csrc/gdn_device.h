@@ -339,6 +339,14 @@ __device__ __forceinline__ int launch_chunk(const Args& a, int x) {
   return a.c_base + x + (x >= a.c_skip_at ? a.c_skip : 0);
 }
 
+// 1 / sqrt(x): the hardware's estimate (1 ulp) and one Newton step.
+__device__ __forceinline__ float inv_sqrt(float x) {
+  const float r = __builtin_amdgcn_rsqf(x);
+  const float h = 0.5f * x * r;
+  const float y = __builtin_fmaf(__builtin_fmaf(-h, r, 0.5f), r, r);
+  return __builtin_isfinite(r) && r != 0.f ? y : r; // at 0, infinity and NaN the step has nothing to add
+}
+
 // One sequence of a serving step: its token range and slots, checked against the call's sizes. ok
 // is false when the device arrays hold a range outside [0, T] or a slot outside [-1, n_slots); the
 // range is then cut to [0, T], for the NaN that its rows get.

@@ -160,8 +160,8 @@ __attribute__((amdgpu_waves_per_eu(KIND == ONE_TOKEN ? 3 : 1, KIND == ONE_TOKEN 
       qq = __builtin_fmaf(qf[i], qf[i], qq);
       qk = __builtin_fmaf(qf[i], kf[i], qk);
     }
-    const float rk = a.l2norm ? 1.f / sqrtf(all(kk) + 1e-6f) : 1.f;
-    const float rq = a.l2norm ? 1.f / sqrtf(all(qq) + 1e-6f) : 1.f;
+    const float rk = a.l2norm ? inv_sqrt(all(kk) + 1e-6f) : 1.f;
+    const float rq = a.l2norm ? inv_sqrt(all(qq) + 1e-6f) : 1.f;
     qk = all(qk);
     const float al = __expf(r.g);
 #pragma unroll
@@ -288,28 +288,104 @@ __global__ __launch_bounds__(256) void k_recurrent_run(RecurrentArgs a) {
   const int t0 = sp.t0, last = sp.t1 - 1;
   // row offsets inside a block of tokens are 32-bit (the host checks the strides)
   const int ks = (int)a.ks, qs = (int)a.qs, vs = (int)a.vs, ko = j * D + kk * KPL, vo = h * D + col;
-  const auto load = [&](Block& b, int t) {
-    t = min(t, last);
-    const int lim = last - t;
+  // Rows of the block of tokens t .. t + 3, cut at the last token. With one column a lane a token is
+  // about 40 instructions, and the addresses of its rows are kept and moved on by a block (141 ns a
+  // token instead of 183 in the 64-wide f32 case); with more columns they are made for each block,
+  // to leave the registers to the waves.
+  constexpr bool KEPT = CPL == 1;
+  struct Rows {
+    const TI *k[U], *q[U], *kn, *qn, *v;
+    const float *g, *beta;
+    const int32_t* st;
+  } at_rows;
+  const auto rows_of = [&](Rows& r, int t) {
+    const int lim = last - t, tc = min(c, lim);
     const TI* kp = (const TI*)a.k + (int64_t)t * a.ks;
     const TI* qp = (const TI*)a.q + (int64_t)t * a.qs;
-    const TI* vp = (const TI*)a.v + (int64_t)t * a.vs;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      b.k[u] = *reinterpret_cast<const kvec*>(kp + (ko + min(u, lim) * ks));
-      b.q[u] = *reinterpret_cast<const kvec*>(qp + (ko + min(u, lim) * qs));
+      r.k[u] = kp + (ko + min(u, lim) * ks);
+      r.q[u] = qp + (ko + min(u, lim) * qs);
     }
-    const int tc = min(c, lim);
-    b.kn = *reinterpret_cast<const kvec*>(kp + (ko + tc * ks));
-    b.qn = *reinterpret_cast<const kvec*>(qp + (ko + tc * qs));
-    b.v = *reinterpret_cast<const vvec*>(vp + (vo + min(kk & 3, lim) * vs));
-    b.g = (a.g + ((int64_t)t * a.HV + h))[tc * a.HV];
-    b.beta = (a.beta + ((int64_t)t * a.HV + h))[tc * a.HV];
-    if constexpr (TOK) b.st = (a.slot_tok + t)[tc];
+    r.kn = kp + (ko + tc * ks);
+    r.qn = qp + (ko + tc * qs);
+    r.v = (const TI*)a.v + (int64_t)t * a.vs + (vo + min(kk & 3, lim) * vs);
+    r.g = a.g + ((int64_t)t * a.HV + h) + tc * a.HV;
+    r.beta = a.beta + ((int64_t)t * a.HV + h) + tc * a.HV;
+    r.st = TOK ? a.slot_tok + t + tc : nullptr;
   };
-  const auto compute = [&](const Block& b, int t) {
+  const auto load = [&](Block& b, int t) {
+    if constexpr (!KEPT) rows_of(at_rows, min(t, last));
+    Rows& r = at_rows;
+    b.kn = *reinterpret_cast<const kvec*>(r.kn);
+    b.qn = *reinterpret_cast<const kvec*>(r.qn);
+    b.g = *r.g;
+    b.beta = *r.beta;
+    b.v = *reinterpret_cast<const vvec*>(r.v);
+    if constexpr (TOK) b.st = *r.st;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      b.k[u] = *reinterpret_cast<const kvec*>(r.k[u]);
+      b.q[u] = *reinterpret_cast<const kvec*>(r.q[u]);
+    }
+    if constexpr (KEPT) {
+      if (t + 2 * U - 1 <= last) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          r.k[u] += U * ks;
+          r.q[u] += U * qs;
+        }
+        r.kn += U * ks;
+        r.qn += U * qs;
+        r.v += U * vs;
+        r.g += U * a.HV;
+        r.beta += U * a.HV;
+        if constexpr (TOK) r.st += U;
+      } else {
+        rows_of(r, min(t + U, last));
+      }
+    }
+  };
+  // one token of a block; f is the factor of R with its decay
+  const auto token = [&](const Block& b, int u, float rq, float qk, float b1, float b2, const float vf[CPL],
+                         float held[CPL]) {
+    float kf[KPL], qf[KPL], s1[CPL], s2[CPL];
+    unpack<TI, KPL>(b.k[u], kf);
+    unpack<TI, KPL>(b.q[u], qf);
+    const float c1 = lane_value(b1, 16 * u) * __builtin_amdgcn_rcpf(f), c2 = lane_value(b2, 16 * u);
+    const float qku = lane_value(qk, 16 * u), fq = f * lane_value(rq, 16 * u);
+#pragma unroll
+    for (int e = 0; e < CPL; ++e) {
+      s1[e] = S[0][e] * kf[0];
+      s2[e] = S[0][e] * qf[0];
+#pragma unroll
+      for (int i = 1; i < KPL; ++i) {
+        s1[e] = __builtin_fmaf(S[i][e], kf[i], s1[e]);
+        s2[e] = __builtin_fmaf(S[i][e], qf[i], s2[e]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < CPL; ++e) {
+      const float v = u == 0 ? dpp<0x150>(vf[e]) : u == 1 ? dpp<0x151>(vf[e]) : u == 2 ? dpp<0x152>(vf[e]) : dpp<0x153>(vf[e]);
+      const float w = __builtin_fmaf(-c2, row_sum16(s1[e]), c1 * v); // u / f
+      const float out = fq * __builtin_fmaf(qku, w, row_sum16(s2[e]));
+      held[e] = kk == u ? out : held[e];
+#pragma unroll
+      for (int i = 0; i < KPL; ++i) S[i][e] = __builtin_fmaf(kf[i], w, S[i][e]);
+    }
+    if constexpr (TOK) {
+      const int st = __builtin_amdgcn_readlane(b.st, 16 * u);
+      if (st < -1 || st >= a.n_slots) {
+#pragma unroll
+        for (int e = 0; e < CPL; ++e) held[e] = kk == u ? nan : held[e];
+      } else if (st >= 0) {
+        store_state(st);
+      }
+    }
+  };
+  const auto compute = [&](const Block& b, int t, int count) {
     // of token c of the block, in lane row c
-    float rk = 1.f, rq = 1.f, qk = 0.f, vf[CPL], kf[KPL], qf[KPL];
+    float rk = 1.f, rq = 1.f, qk = 0.f, vf[CPL], kf[KPL], qf[KPL], held[CPL];
     unpack<TI, KPL>(b.kn, kf);
     unpack<TI, KPL>(b.qn, qf);
 #pragma unroll
@@ -322,77 +398,40 @@ __global__ __launch_bounds__(256) void k_recurrent_run(RecurrentArgs a) {
         ss = __builtin_fmaf(kf[i], kf[i], ss);
         qq = __builtin_fmaf(qf[i], qf[i], qq);
       }
-      rk = 1.f / sqrtf(row_sum16(ss) + 1e-6f);
-      rq = 1.f / sqrtf(row_sum16(qq) + 1e-6f);
+      rk = inv_sqrt(row_sum16(ss) + 1e-6f);
+      rq = inv_sqrt(row_sum16(qq) + 1e-6f);
     }
     const float b1 = b.beta * rk, b2 = b1 * rk, al = __expf(b.g);
     unpack<TI, CPL>(b.v, vf);
-    const int count = min(U, last + 1 - t);
-    float fu[U];
-    {
-      float x = f;
-      bool in = true;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        x *= lane_value(al, 16 * u);
-        fu[u] = x;
-        in = in && x >= 5.9604645e-8f && x <= 1.6777216e7f;
-      }
-      if (!in) { // every token's decay goes into the state
-#pragma unroll
-        for (int i = 0; i < KPL; ++i)
-#pragma unroll
-          for (int e = 0; e < CPL; ++e) S[i][e] *= f;
-        f = 1.f;
-        fu[0] = -1.f;
-      }
-    }
-    const bool each = fu[0] < 0.f;
-    float held[CPL];
+    float fu[U], lo = f, hi = f;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (u >= count) break;
-      if (each) {
-        const float x = lane_value(al, 16 * u);
+      fu[u] = (u ? fu[u - 1] : f) * lane_value(al, 16 * u);
+      lo = fminf(lo, fu[u]);
+      hi = fmaxf(hi, fu[u]);
+    }
+    const bool in = lo >= 5.9604645e-8f && hi <= 1.6777216e7f; // a NaN passes, and its state is NaN either way
+    if (KEPT && count == U && in) {
 #pragma unroll
-        for (int i = 0; i < KPL; ++i)
-#pragma unroll
-          for (int e = 0; e < CPL; ++e) S[i][e] *= x;
-      } else {
+      for (int u = 0; u < U; ++u) {
         f = fu[u];
+        token(b, u, rq, qk, b1, b2, vf, held);
       }
-      unpack<TI, KPL>(b.k[u], kf);
-      unpack<TI, KPL>(b.q[u], qf);
-      const float c1 = lane_value(b1, 16 * u) * __builtin_amdgcn_rcpf(f), c2 = lane_value(b2, 16 * u);
-      const float qku = lane_value(qk, 16 * u), fq = f * lane_value(rq, 16 * u);
-      float s1[CPL], s2[CPL];
+    } else { // a block cut short, decays that have to go into the state token by token, or several columns
 #pragma unroll
-      for (int e = 0; e < CPL; ++e) {
-        s1[e] = S[0][e] * kf[0];
-        s2[e] = S[0][e] * qf[0];
+      for (int u = 0; u < U; ++u) {
+        if (u >= count) break;
+        if (KEPT || !in) {
+          const float x = f * lane_value(al, 16 * u);
 #pragma unroll
-        for (int i = 1; i < KPL; ++i) {
-          s1[e] = __builtin_fmaf(S[i][e], kf[i], s1[e]);
-          s2[e] = __builtin_fmaf(S[i][e], qf[i], s2[e]);
+          for (int i = 0; i < KPL; ++i)
+#pragma unroll
+            for (int e = 0; e < CPL; ++e) S[i][e] *= x;
+          f = 1.f;
+        } else {
+          f = fu[u];
         }
-      }
-#pragma unroll
-      for (int e = 0; e < CPL; ++e) {
-        const float v = u == 0 ? dpp<0x150>(vf[e]) : u == 1 ? dpp<0x151>(vf[e]) : u == 2 ? dpp<0x152>(vf[e]) : dpp<0x153>(vf[e]);
-        const float w = __builtin_fmaf(-c2, row_sum16(s1[e]), c1 * v); // u / f
-        const float out = fq * __builtin_fmaf(qku, w, row_sum16(s2[e]));
-        held[e] = kk == u ? out : held[e];
-#pragma unroll
-        for (int i = 0; i < KPL; ++i) S[i][e] = __builtin_fmaf(kf[i], w, S[i][e]);
-      }
-      if constexpr (TOK) {
-        const int st = __builtin_amdgcn_readlane(b.st, 16 * u);
-        if (st < -1 || st >= a.n_slots) {
-#pragma unroll
-          for (int e = 0; e < CPL; ++e) held[e] = kk == u ? nan : held[e];
-        } else if (st >= 0) {
-          store_state(st);
-        }
+        token(b, u, rq, qk, b1, b2, vf, held);
       }
     }
     if (kk < count) {
@@ -406,13 +445,14 @@ __global__ __launch_bounds__(256) void k_recurrent_run(RecurrentArgs a) {
   };
   if (t0 <= last) {
     Block x, y;
+    if constexpr (KEPT) rows_of(at_rows, t0);
     load(x, t0);
     for (int t = t0; t <= last; t += 2 * U) {
       load(y, t + U);
-      compute(x, t);
+      compute(x, t, min(U, last + 1 - t));
       if (t + U > last) break;
       load(x, t + 2 * U);
-      compute(y, t + U);
+      compute(y, t + U, min(U, last + 1 - t - U));
     }
   }
   if (sp.out >= 0) store_state(sp.out);

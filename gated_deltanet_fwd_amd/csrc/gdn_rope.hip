@@ -40,14 +40,6 @@ __device__ __forceinline__ float group_sum(float x) {
   return x;
 }
 
-// 1 / sqrt(x): the hardware's estimate (1 ulp) and one Newton step.
-__device__ __forceinline__ float inv_sqrt(float x) {
-  const float r = __builtin_amdgcn_rsqf(x);
-  const float h = 0.5f * x * r;
-  const float y = __builtin_fmaf(__builtin_fmaf(-h, r, 0.5f), r, r);
-  return __builtin_isfinite(r) && r != 0.f ? y : r; // at 0, infinity and NaN the step has nothing to add
-}
-
 // cos and sin of the angle pos * freq (freq in 2^-64 turns).
 __device__ __forceinline__ void turn_cs(int pos, uint64_t freq, float& c, float& s) {
   const uint32_t top = (uint32_t)(((uint64_t)(int64_t)pos * freq) >> 32) + 0x20000000u; // shifted by 1/8 turn
