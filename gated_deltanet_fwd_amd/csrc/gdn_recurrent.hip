@@ -229,8 +229,9 @@ __attribute__((amdgpu_waves_per_eu(KIND == ONE_TOKEN ? 3 : 1, KIND == ONE_TOKEN 
 }
 
 // ------------------------------------------------------------------------------------------------
-// Runs: what bounds them is the chain S -> s1 -> u -> S of each token, so a state is spread over more
-// waves and the keys' sums go through DPP adds, which leave the total in every lane. Lane (c, kk) =
+// Runs: what bounds them is issuing each token's instructions in turn (few sequences: one wave a SIMD,
+// about 60 instructions a token; many: the 3 operations of each state element and token). A state is
+// spread over more waves and the keys' sums go through DPP adds, which leave the total in every lane. Lane (c, kk) =
 // (lane / 16, lane % 16) holds the D / 16 keys from kk D / 16 on of CPL columns; a wave holds 4 CPL.
 // Tokens are taken 4 at a time: the rows of the next 4 are loaded while these are computed, lane row
 // c makes the norms, q.k and gates of token c, and the 4 outputs leave in one store.
@@ -289,9 +290,10 @@ __global__ __launch_bounds__(256) void k_recurrent_run(RecurrentArgs a) {
   // row offsets inside a block of tokens are 32-bit (the host checks the strides)
   const int ks = (int)a.ks, qs = (int)a.qs, vs = (int)a.vs, ko = j * D + kk * KPL, vo = h * D + col;
   // Rows of the block of tokens t .. t + 3, cut at the last token. With one column a lane a token is
-  // about 40 instructions, and the addresses of its rows are kept and moved on by a block (141 ns a
-  // token instead of 183 in the 64-wide f32 case); with more columns they are made for each block,
-  // to leave the registers to the waves.
+  // about 40 instructions, and the addresses of its rows are kept and moved on by a block (147 ns a
+  // token instead of 183, 64 wide, f32); with four they are made for each block, and the two paths of
+  // `compute` are one, to leave the registers to the waves (323 us instead of 349 for 12 sequences of
+  // up to 300 tokens of 48 heads).
   constexpr bool KEPT = CPL == 1;
   struct Rows {
     const TI *k[U], *q[U], *kn, *qn, *v;
@@ -471,16 +473,27 @@ static void run_c(const RecurrentArgs& a, hipStream_t s) {
   else hipLaunchKernelGGL((k_recurrent_run<TI, D, CPL, false>), grid, dim3(256), 0, s, a);
 }
 
+// The kernel by the longest sequence, as the host knows it. Up to 6 tokens the step is no slower, from
+// 8 on the run is faster (16 heads of 48, 128 wide, us step / run: 1 sequence of 4 tokens 7.6 / 8.9,
+// of 8 11.3 / 10.7, of 16 18.9 / 13.5; 32 sequences 42.0 / 42.3, 55.8 / 51.0, 88.9 / 79.0). With every
+// state kept the step's stores are the better ones for longer (8 sequences of 16 tokens 81 / 116).
+// A run takes four columns a lane once that gives 512 waves, one below (us for 200 tokens, one / four
+// columns: 1 sequence 78 / 96, 2 sequences, 768 waves, 109 / 98, 8 sequences 351 / 224).
 template <typename TI, int D>
 static int recurrent_t(const RecurrentArgs& a, hipStream_t s) {
-  const int64_t quads = (int64_t)a.live * a.HV * (D / 4); // waves of a run at one column a lane
+  const int64_t waves4 = (int64_t)a.live * a.HV * (D / 16); // of a run at four columns a lane
   const dim3 step = grid_of(a, D / 32);
-  if (!a.cu && !a.slot_tok) hipLaunchKernelGGL((k_recurrent_step<TI, D, ONE_TOKEN>), step, dim3(256), STEP_LDS, s, a);
-  else if (a.longest <= 8 && a.slot_tok) hipLaunchKernelGGL((k_recurrent_step<TI, D, KEEP_EACH>), step, dim3(256), STEP_LDS, s, a);
-  else if (a.longest <= 8) hipLaunchKernelGGL((k_recurrent_step<TI, D, RUN_OF_TOKENS>), step, dim3(256), STEP_LDS, s, a);
-  else if (quads >= 4 * 1024) run_c<TI, D, 4>(a, s);
-  else if (quads >= 2 * 1024) run_c<TI, D, 2>(a, s);
-  else run_c<TI, D, 1>(a, s);
+  if (!a.cu && !a.slot_tok) {
+    hipLaunchKernelGGL((k_recurrent_step<TI, D, ONE_TOKEN>), step, dim3(256), STEP_LDS, s, a);
+  } else if (a.slot_tok && a.longest <= 32) {
+    hipLaunchKernelGGL((k_recurrent_step<TI, D, KEEP_EACH>), step, dim3(256), STEP_LDS, s, a);
+  } else if (a.longest <= 6) {
+    hipLaunchKernelGGL((k_recurrent_step<TI, D, RUN_OF_TOKENS>), step, dim3(256), STEP_LDS, s, a);
+  } else if (waves4 >= 512) {
+    run_c<TI, D, 4>(a, s);
+  } else {
+    run_c<TI, D, 1>(a, s);
+  }
   return (int)hipGetLastError();
 }
 
