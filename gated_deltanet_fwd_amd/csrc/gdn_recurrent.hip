@@ -229,270 +229,273 @@ __attribute__((amdgpu_waves_per_eu(KIND == ONE_TOKEN ? 3 : 1, KIND == ONE_TOKEN 
 }
 
 // ------------------------------------------------------------------------------------------------
-// Runs: what bounds them is issuing each token's instructions in turn (few sequences: one wave a SIMD,
-// about 60 instructions a token; many: the 3 operations of each state element and token). A state is
-// spread over more waves and the keys' sums go through DPP adds, which leave the total in every lane. Lane (c, kk) =
-// (lane / 16, lane % 16) holds the D / 16 keys from kk D / 16 on of CPL columns; a wave holds 4 CPL.
-// Tokens are taken 4 at a time: the rows of the next 4 are loaded while these are computed, lane row
-// c makes the norms, q.k and gates of token c, and the 4 outputs leave in one store.
-// The decay is kept as a factor f of the whole state (S = f R: R += k (u / f)^T), one operation less
-// for each state element and token; R takes it over when f would leave [2^-24, 2^24].
-template <typename TI, int D, int CPL, bool TOK>
-__global__ __launch_bounds__(256) void k_recurrent_run(RecurrentArgs a) {
-  constexpr int KPL = D / 16, CB = D / (4 * CPL), U = 4;
-  typedef typename Vec<TI, KPL>::type kvec;
-  typedef typename Vec<TI, CPL>::type vvec;
-  typedef typename Vec<float, CPL>::type svec;
-  const int lane = threadIdx.x & 63, kk = lane & 15, c = lane >> 4;
-  int n, h, j, cb; // sequence, value head, q/k head, block of columns
-  if (!wave_of(a, CB, &n, &h, &j, &cb)) return;
-  const int col = (cb * 4 + c) * CPL;
+// Runs, 16 tokens at a time. With S the state before a block, G_i = a_0 .. a_i, D_ij = a_{j+1} .. a_i
+// (products of decays, 1 for i = j, none for i < j) and kh, qh the normalised rows, the recurrence
+// unrolls to
+//
+//   (I + L) U = diag(beta) (V - diag(G) Kh S),   L_ij = beta_i D_ij kh_i.kh_j  (j < i)
+//   O = diag(G) Qh S + P U,                      P_ij = D_ij qh_i.kh_j         (j <= i)
+//   S <- G_15 S + Kh^T diag(D_15,j) U
+//
+// in FP32 throughout, the products on v_mfma_f32_16x16x4. A workgroup holds 64 columns of a state, 16
+// in each of its first four waves, and takes 4 blocks a turn. What does not depend on S (Gram products,
+// decays, the inverse T of I + L by forward substitution) the other four waves prepare in LDS a turn
+// ahead, a block each. Lane (g, n) = (lane / 16, lane % 16) holds rows g D/4 .. of
+// column n of S; with the rows in the order (i, r) -> g D/4 + 4 r + i the same registers are the
+// products' B operand and the update's accumulators. A product sums over the key rows in any order, so
+// the K and Q rows lie in LDS in the order that makes their A operands whole 16-byte reads.
+// What bounds it is the matrix unit: 104 (D = 128) or 56 (64) instructions of 32 cycles a block and wave.
+template <typename TI, int D>
+__global__ __launch_bounds__(512) void k_recurrent_run(RecurrentArgs a) {
+  constexpr int C = 16, NB = 4, DG = D / 4, R = D / 16; // tokens a block, blocks a turn, rows a lane, tiles
+  constexpr int LD = D + 4, LT = 20;                    // LDS row strides
+  typedef typename Vec<TI, 8>::type vec8;
+  struct alignas(16) Prep { // of one block
+    float k[C][LD], q[C][LD]; // rows, permuted
+    float t[C][LT], p[C][LT]; // T diag(beta), P
+    float gk[C], gq[C], w[C], g_last[C]; // G rk, G rq, D_15,j rk_j, G_15
+  };
+  extern __shared__ __attribute__((aligned(16))) float lds[];
+  Prep* prep = reinterpret_cast<Prep*>(lds); // of two turns
+  const int lane = threadIdx.x & 63, g = lane >> 4, n16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wv = wave & 3;
+  const bool prepares = wave >= 4;
+  const int h = blockIdx.x / (D / 64), j = (int)(((uint64_t)h * a.g_mul) >> 32);
+  const int n = blockIdx.z * MAX_GRID_Y + blockIdx.y;
+  if (n >= a.N) return;
+  const int col = h * D + (blockIdx.x % (D / 64)) * 64 + wv * 16 + n16; // in a row of v and o
   const int os = a.HV * D;
   const SeqSpan sp = seq_span(a.cu, a.slot_in, a.slot_out, n, a.T, a.n_slots);
-  const float nan = __builtin_nanf("");
   if (!sp.ok) {
-    for (int t = sp.t0 + kk; t < sp.t1; t += 16)
-      for (int e = 0; e < CPL; ++e) ((TI*)a.o)[(int64_t)t * os + h * D + col + e] = (TI)nan;
+    for (int t = sp.t0 + g; t < sp.t1 && !prepares; t += 4) ((TI*)a.o)[(int64_t)t * os + col] = (TI)__builtin_nanf("");
     return;
   }
   const int64_t hd = (int64_t)a.HV * D * D, head = (int64_t)h * D * D;
-  const int at = kk * KPL * D + col;
-  float S[KPL][CPL];
+  const int at = g * DG * D + (col - h * D);
+  f32x4 S[R];
+  // this wave's block of the turn at t: lane (g, i) loads token i's rows g D/4 .. of k and q
+  struct Rows {
+    vec8 k[DG / 8], q[DG / 8];
+    float g, beta;
+  };
+  const auto load = [&](Rows& r, int t) {
+    const int tok = min(t + wv * C + n16, sp.t1 - 1);
+    const TI* kp = (const TI*)a.k + (int64_t)tok * a.ks + (j * D + g * DG);
+    const TI* qp = (const TI*)a.q + (int64_t)tok * a.qs + (j * D + g * DG);
+#pragma unroll
+    for (int e = 0; e < DG / 8; ++e) {
+      r.k[e] = reinterpret_cast<const vec8*>(kp)[e];
+      r.q[e] = reinterpret_cast<const vec8*>(qp)[e];
+    }
+    r.g = a.g[(int64_t)tok * a.HV + h];
+    r.beta = a.beta[(int64_t)tok * a.HV + h];
+  };
+  const auto load_v = [&](TI v[4], int t) { // tokens t + 4 g + s of this lane's column
+#pragma unroll
+    for (int s = 0; s < 4; ++s) v[s] = ((const TI*)a.v)[(int64_t)min(t + 4 * g + s, sp.t1 - 1) * a.vs + col];
+  };
+  const auto all_groups = [](float x) { // sum over g, in every lane
+    Pair p = swap16(x, copy_of(x));
+    p = swap32(p.x + p.y, copy_of(p.x + p.y));
+    return p.x + p.y;
+  };
+  const auto mfma1 = [](float x, float y, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(x, y, c, 0, 0, 0); };
+  const auto prepare = [&](Prep& b, const Rows& r, int t) {
+    const bool live = t + n16 < sp.t1; // tokens past the end: zero rows, no decay, nothing written
+    float kf[DG], qf[DG];
+#pragma unroll
+    for (int e = 0; e < DG / 8; ++e) {
+      unpack<TI, 8>(r.k[e], kf + 8 * e);
+      unpack<TI, 8>(r.q[e], qf + 8 * e);
+    }
+    float kk = 0.f, qq = 0.f;
+    f32x4 gram = zero4(), qk = zero4();
+#pragma unroll
+    for (int m = 0; m < DG; ++m) {
+      kf[m] = live ? kf[m] : 0.f;
+      qf[m] = live ? qf[m] : 0.f;
+      kk = __builtin_fmaf(kf[m], kf[m], kk);
+      qq = __builtin_fmaf(qf[m], qf[m], qq);
+      gram = mfma1(kf[m], kf[m], gram); // rows i = 4 g + s, column n16
+      qk = mfma1(qf[m], kf[m], qk);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int x = 0; x < R; x += 4) {
+        *reinterpret_cast<f32x4*>(&b.k[n16][g * DG + i * R + x]) =
+            f32x4{kf[4 * x + i], kf[4 * x + 4 + i], kf[4 * x + 8 + i], kf[4 * x + 12 + i]};
+        *reinterpret_cast<f32x4*>(&b.q[n16][g * DG + i * R + x]) =
+            f32x4{qf[4 * x + i], qf[4 * x + 4 + i], qf[4 * x + 8 + i], qf[4 * x + 12 + i]};
+      }
+    const float rk = a.l2norm ? inv_sqrt(all_groups(kk) + 1e-6f) : 1.f;
+    const float rq = a.l2norm ? inv_sqrt(all_groups(qq) + 1e-6f) : 1.f;
+    const float al = live ? __expf(r.g) : 1.f, be = live ? r.beta : 0.f;
+    // running products: G of token n16, and D_ij of this lane's column j = n16
+    float gp = 1.f, gi = 1.f, d = 0.f, dij[4];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const float ai = lane_value(al, i);
+      gp *= ai;
+      gi = i == n16 ? gp : gi;
+      d = i == n16 ? 1.f : d * ai;
+      dij[i & 3] = (i >> 2) == g ? d : dij[i & 3];
+    }
+    // scale the Gram products; L goes through b.t to be read row by row
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int i = 4 * g + s;
+      const float rki = __shfl(rk, i), rqi = __shfl(rq, i), bei = __shfl(be, i);
+      b.t[i][n16] = i > n16 ? bei * rki * rk * dij[s] * gram[s] : 0.f;
+      b.p[i][n16] = i >= n16 ? rqi * rk * dij[s] * qk[s] : 0.f;
+    }
+    if (g == 0) {
+      b.gk[n16] = gi * rk;
+      b.gq[n16] = gi * rq;
+      b.w[n16] = d * rk;
+      b.g_last[n16] = gp;
+    }
+    // T = (I + L)^-1, column n16: T_i = e_i - sum_{j < i} L_ij T_j (the wave's own LDS writes above
+    // are in order with these reads)
+    __builtin_amdgcn_wave_barrier();
+    float T[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      float x = i == n16 ? 1.f : 0.f;
+#pragma unroll
+      for (int q4 = 0; q4 < (i + 3) / 4; ++q4) {
+        const f32x4 l = *reinterpret_cast<const f32x4*>(&b.t[i][4 * q4]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (4 * q4 + e < i) x = __builtin_fmaf(-l[e], T[4 * q4 + e], x);
+      }
+      T[i] = x;
+    }
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+      if ((i >> 2) == g) b.t[i][n16] = T[i] * be;
+  };
+  // All of a block's operands are asked for before its first product: the waits for LDS, and for the
+  // next block's v, would otherwise stand between the products (122 ns a token instead of NSTOK,
+  // 64 wide, f32).
+  const auto block = [&](const Prep& b, TI v[4], int t) {
+    f32x4 ka[4][R / 4], qa[4][R / 4], ua[4][R / 4];
+    TI next[4];
+    load_v(next, t + C);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int x = 0; x < R / 4; ++x) {
+        ka[i][x] = *reinterpret_cast<const f32x4*>(&b.k[n16][g * DG + i * R + 4 * x]);
+        qa[i][x] = *reinterpret_cast<const f32x4*>(&b.q[n16][g * DG + i * R + 4 * x]);
+      }
+    const f32x4 gk = *reinterpret_cast<const f32x4*>(&b.gk[4 * g]), gq = *reinterpret_cast<const f32x4*>(&b.gq[4 * g]);
+    const f32x4 w = *reinterpret_cast<const f32x4*>(&b.w[4 * g]);
+    const f32x4 ta = *reinterpret_cast<const f32x4*>(&b.t[n16][4 * g]), pa = *reinterpret_cast<const f32x4*>(&b.p[n16][4 * g]);
+    const float last = b.g_last[0];
+    // the update's: lane (g, 4 y + i): rows y D/4 + 4 r + i of token 4 g + s
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int x = 0; x < R / 4; ++x)
+        ua[s][x] = *reinterpret_cast<const f32x4*>(&b.k[4 * g + s][(n16 >> 2) * DG + (n16 & 3) * R + 4 * x]);
+    __builtin_amdgcn_sched_barrier(0);
+    f32x4 ks = zero4(), qs = zero4();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        ks = mfma1(ka[i][r / 4][r % 4], S[r][i], ks);
+        qs = mfma1(qa[i][r / 4][r % 4], S[r][i], qs);
+      }
+    f32x4 rhs, u = zero4(), o;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      rhs[s] = __builtin_fmaf(-gk[s], ks[s], t + 4 * g + s < sp.t1 ? (float)v[s] : 0.f);
+      o[s] = gq[s] * qs[s];
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) S[r] *= last;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) u = mfma1(ta[s], rhs[s], u);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const float wu = w[s] * u[s]; // of token 4 g + s
+#pragma unroll
+      for (int r = 0; r < R; ++r) S[r] = mfma1(ua[s][r / 4][r % 4], wu, S[r]);
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s) o = mfma1(pa[s], u[s], o);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      if (t + 4 * g + s < sp.t1) ((TI*)a.o)[(int64_t)(t + 4 * g + s) * os + col] = (TI)o[s];
+      v[s] = next[s];
+    }
+  };
+  if (prepares) {
+    if (sp.t0 >= sp.t1) return;
+    Rows r;
+    load(r, sp.t0);
+    int buf = 0;
+    for (int t = sp.t0; t < sp.t1; t += NB * C, buf ^= NB) {
+      if (t + wv * C < sp.t1) prepare(prep[buf + wv], r, t + wv * C);
+      if (t + NB * C < sp.t1) load(r, t + NB * C);
+      __syncthreads(); // this turn is ready, and the one before it has been used
+    }
+    return;
+  }
   {
     const float* p = a.states + (sp.in < 0 ? 0 : sp.in) * hd + head + at;
 #pragma unroll
-    for (int i = 0; i < KPL; ++i) {
-      unpack<float, CPL>(*reinterpret_cast<const svec*>(p + i * D), S[i]);
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int e = 0; e < CPL; ++e) S[i][e] = keepf(S[i][e], sp.in >= 0);
+      for (int i = 0; i < 4; ++i) S[r][i] = keepf(p[(4 * r + i) * D], sp.in >= 0);
+  }
+  if (sp.t0 < sp.t1) {
+    TI v[4];
+    load_v(v, sp.t0);
+    int buf = 0;
+    for (int t = sp.t0; t < sp.t1; t += NB * C, buf ^= NB) {
+      __syncthreads();
+      const int end = min(t + NB * C, sp.t1);
+#pragma unroll 1
+      for (int tb = t; tb < end; tb += C) block(prep[buf + (tb - t) / C], v, tb);
     }
   }
-  float f = 1.f;
-  const auto store_state = [&](int slot) {
-    float* p = a.states + slot * hd + head + at;
+  if (sp.out >= 0) {
+    float* p = a.states + sp.out * hd + head + at;
 #pragma unroll
-    for (int i = 0; i < KPL; ++i) {
-      svec r;
-      if constexpr (CPL == 1) r = f * S[i][0];
-      else
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int e = 0; e < CPL; ++e) r[e] = f * S[i][e];
-      *reinterpret_cast<svec*>(p + i * D) = r;
-    }
-  };
-  struct Block {
-    kvec k[U], q[U], kn, qn;
-    vvec v;
-    float g, beta;
-    int st;
-  };
-  const int t0 = sp.t0, last = sp.t1 - 1;
-  // row offsets inside a block of tokens are 32-bit (the host checks the strides)
-  const int ks = (int)a.ks, qs = (int)a.qs, vs = (int)a.vs, ko = j * D + kk * KPL, vo = h * D + col;
-  // Rows of the block of tokens t .. t + 3, cut at the last token. With one column a lane a token is
-  // about 40 instructions, and the addresses of its rows are kept and moved on by a block (147 ns a
-  // token instead of 183, 64 wide, f32); with four they are made for each block, and the two paths of
-  // `compute` are one, to leave the registers to the waves (323 us instead of 349 for 12 sequences of
-  // up to 300 tokens of 48 heads).
-  constexpr bool KEPT = CPL == 1;
-  struct Rows {
-    const TI *k[U], *q[U], *kn, *qn, *v;
-    const float *g, *beta;
-    const int32_t* st;
-  } at_rows;
-  const auto rows_of = [&](Rows& r, int t) {
-    const int lim = last - t, tc = min(c, lim);
-    const TI* kp = (const TI*)a.k + (int64_t)t * a.ks;
-    const TI* qp = (const TI*)a.q + (int64_t)t * a.qs;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      r.k[u] = kp + (ko + min(u, lim) * ks);
-      r.q[u] = qp + (ko + min(u, lim) * qs);
-    }
-    r.kn = kp + (ko + tc * ks);
-    r.qn = qp + (ko + tc * qs);
-    r.v = (const TI*)a.v + (int64_t)t * a.vs + (vo + min(kk & 3, lim) * vs);
-    r.g = a.g + ((int64_t)t * a.HV + h) + tc * a.HV;
-    r.beta = a.beta + ((int64_t)t * a.HV + h) + tc * a.HV;
-    r.st = TOK ? a.slot_tok + t + tc : nullptr;
-  };
-  const auto load = [&](Block& b, int t) {
-    if constexpr (!KEPT) rows_of(at_rows, min(t, last));
-    Rows& r = at_rows;
-    b.kn = *reinterpret_cast<const kvec*>(r.kn);
-    b.qn = *reinterpret_cast<const kvec*>(r.qn);
-    b.g = *r.g;
-    b.beta = *r.beta;
-    b.v = *reinterpret_cast<const vvec*>(r.v);
-    if constexpr (TOK) b.st = *r.st;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      b.k[u] = *reinterpret_cast<const kvec*>(r.k[u]);
-      b.q[u] = *reinterpret_cast<const kvec*>(r.q[u]);
-    }
-    if constexpr (KEPT) {
-      if (t + 2 * U - 1 <= last) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          r.k[u] += U * ks;
-          r.q[u] += U * qs;
-        }
-        r.kn += U * ks;
-        r.qn += U * qs;
-        r.v += U * vs;
-        r.g += U * a.HV;
-        r.beta += U * a.HV;
-        if constexpr (TOK) r.st += U;
-      } else {
-        rows_of(r, min(t + U, last));
-      }
-    }
-  };
-  // one token of a block; f is the factor of R with its decay
-  const auto token = [&](const Block& b, int u, float rq, float qk, float b1, float b2, const float vf[CPL],
-                         float held[CPL]) {
-    float kf[KPL], qf[KPL], s1[CPL], s2[CPL];
-    unpack<TI, KPL>(b.k[u], kf);
-    unpack<TI, KPL>(b.q[u], qf);
-    const float c1 = lane_value(b1, 16 * u) * __builtin_amdgcn_rcpf(f), c2 = lane_value(b2, 16 * u);
-    const float qku = lane_value(qk, 16 * u), fq = f * lane_value(rq, 16 * u);
-#pragma unroll
-    for (int e = 0; e < CPL; ++e) {
-      s1[e] = S[0][e] * kf[0];
-      s2[e] = S[0][e] * qf[0];
-#pragma unroll
-      for (int i = 1; i < KPL; ++i) {
-        s1[e] = __builtin_fmaf(S[i][e], kf[i], s1[e]);
-        s2[e] = __builtin_fmaf(S[i][e], qf[i], s2[e]);
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < CPL; ++e) {
-      const float v = u == 0 ? dpp<0x150>(vf[e]) : u == 1 ? dpp<0x151>(vf[e]) : u == 2 ? dpp<0x152>(vf[e]) : dpp<0x153>(vf[e]);
-      const float w = __builtin_fmaf(-c2, row_sum16(s1[e]), c1 * v); // u / f
-      const float out = fq * __builtin_fmaf(qku, w, row_sum16(s2[e]));
-      held[e] = kk == u ? out : held[e];
-#pragma unroll
-      for (int i = 0; i < KPL; ++i) S[i][e] = __builtin_fmaf(kf[i], w, S[i][e]);
-    }
-    if constexpr (TOK) {
-      const int st = __builtin_amdgcn_readlane(b.st, 16 * u);
-      if (st < -1 || st >= a.n_slots) {
-#pragma unroll
-        for (int e = 0; e < CPL; ++e) held[e] = kk == u ? nan : held[e];
-      } else if (st >= 0) {
-        store_state(st);
-      }
-    }
-  };
-  const auto compute = [&](const Block& b, int t, int count) {
-    // of token c of the block, in lane row c
-    float rk = 1.f, rq = 1.f, qk = 0.f, vf[CPL], kf[KPL], qf[KPL], held[CPL];
-    unpack<TI, KPL>(b.kn, kf);
-    unpack<TI, KPL>(b.qn, qf);
-#pragma unroll
-    for (int i = 0; i < KPL; ++i) qk = __builtin_fmaf(qf[i], kf[i], qk);
-    qk = row_sum16(qk);
-    if (a.l2norm) {
-      float ss = 0.f, qq = 0.f;
-#pragma unroll
-      for (int i = 0; i < KPL; ++i) {
-        ss = __builtin_fmaf(kf[i], kf[i], ss);
-        qq = __builtin_fmaf(qf[i], qf[i], qq);
-      }
-      rk = inv_sqrt(row_sum16(ss) + 1e-6f);
-      rq = inv_sqrt(row_sum16(qq) + 1e-6f);
-    }
-    const float b1 = b.beta * rk, b2 = b1 * rk, al = __expf(b.g);
-    unpack<TI, CPL>(b.v, vf);
-    float fu[U], lo = f, hi = f;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      fu[u] = (u ? fu[u - 1] : f) * lane_value(al, 16 * u);
-      lo = fminf(lo, fu[u]);
-      hi = fmaxf(hi, fu[u]);
-    }
-    const bool in = lo >= 5.9604645e-8f && hi <= 1.6777216e7f; // a NaN passes, and its state is NaN either way
-    if (KEPT && count == U && in) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        f = fu[u];
-        token(b, u, rq, qk, b1, b2, vf, held);
-      }
-    } else { // a block cut short, decays that have to go into the state token by token, or several columns
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (u >= count) break;
-        if (KEPT || !in) {
-          const float x = f * lane_value(al, 16 * u);
-#pragma unroll
-          for (int i = 0; i < KPL; ++i)
-#pragma unroll
-            for (int e = 0; e < CPL; ++e) S[i][e] *= x;
-          f = 1.f;
-        } else {
-          f = fu[u];
-        }
-        token(b, u, rq, qk, b1, b2, vf, held);
-      }
-    }
-    if (kk < count) {
-      vvec r;
-      if constexpr (CPL == 1) r = (TI)held[0];
-      else
-#pragma unroll
-        for (int e = 0; e < CPL; ++e) r[e] = (TI)held[e];
-      *reinterpret_cast<vvec*>((TI*)a.o + (int64_t)t * os + (kk * os + vo)) = r;
-    }
-  };
-  if (t0 <= last) {
-    Block x, y;
-    if constexpr (KEPT) rows_of(at_rows, t0);
-    load(x, t0);
-    for (int t = t0; t <= last; t += 2 * U) {
-      load(y, t + U);
-      compute(x, t, min(U, last + 1 - t));
-      if (t + U > last) break;
-      load(x, t + 2 * U);
-      compute(y, t + U, min(U, last + 1 - t - U));
-    }
+      for (int i = 0; i < 4; ++i) p[(4 * r + i) * D] = S[r][i];
   }
-  if (sp.out >= 0) store_state(sp.out);
 }
+// LDS of a workgroup: the rows, T, P and factors of two turns of 4 blocks
+constexpr unsigned run_lds(int D) { return 8 * 4 * (2 * 16 * (D + 4) + 2 * 16 * 20 + 4 * 16); }
 
-static dim3 grid_of(const RecurrentArgs& a, int waves_per_state) {
+static dim3 grid_of(const RecurrentArgs& a, int x) {
   const unsigned n = (unsigned)a.N;
-  return dim3((unsigned)((a.HV * waves_per_state + 3) / 4), n < MAX_GRID_Y ? n : MAX_GRID_Y,
-              (n + MAX_GRID_Y - 1) / MAX_GRID_Y);
+  return dim3((unsigned)x, n < MAX_GRID_Y ? n : MAX_GRID_Y, (n + MAX_GRID_Y - 1) / MAX_GRID_Y);
 }
 
-template <typename TI, int D, int CPL>
-static void run_c(const RecurrentArgs& a, hipStream_t s) {
-  const dim3 grid = grid_of(a, D / (4 * CPL));
-  if (a.slot_tok) hipLaunchKernelGGL((k_recurrent_run<TI, D, CPL, true>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_recurrent_run<TI, D, CPL, false>), grid, dim3(256), 0, s, a);
-}
-
-// The kernel by the longest sequence, as the host knows it. Up to 6 tokens the step is no slower, from
-// 8 on the run is faster (16 heads of 48, 128 wide, us step / run: 1 sequence of 4 tokens 7.6 / 8.9,
-// of 8 11.3 / 10.7, of 16 18.9 / 13.5; 32 sequences 42.0 / 42.3, 55.8 / 51.0, 88.9 / 79.0). With every
-// state kept the step's stores are the better ones for longer (8 sequences of 16 tokens 81 / 116).
-// A run takes four columns a lane once that gives 512 waves, one below (us for 200 tokens, one / four
-// columns: 1 sequence 78 / 96, 2 sequences, 768 waves, 109 / 98, 8 sequences 351 / 224).
 template <typename TI, int D>
 static int recurrent_t(const RecurrentArgs& a, hipStream_t s) {
-  const int64_t waves4 = (int64_t)a.live * a.HV * (D / 16); // of a run at four columns a lane
-  const dim3 step = grid_of(a, D / 32);
+  const dim3 step = grid_of(a, (a.HV * (D / 32) + 3) / 4);
   if (!a.cu && !a.slot_tok) {
     hipLaunchKernelGGL((k_recurrent_step<TI, D, ONE_TOKEN>), step, dim3(256), STEP_LDS, s, a);
-  } else if (a.slot_tok && a.longest <= 32) {
+  } else if (a.slot_tok) {
     hipLaunchKernelGGL((k_recurrent_step<TI, D, KEEP_EACH>), step, dim3(256), STEP_LDS, s, a);
   } else if (a.longest <= 6) {
     hipLaunchKernelGGL((k_recurrent_step<TI, D, RUN_OF_TOKENS>), step, dim3(256), STEP_LDS, s, a);
-  } else if (waves4 >= 512) {
-    run_c<TI, D, 4>(a, s);
   } else {
-    run_c<TI, D, 1>(a, s);
+    if constexpr (run_lds(D) > 64 * 1024) {
+      // the runtime's limit without this is 64 KiB; it is set once for the process
+      static const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_recurrent_run<TI, D>),
+                                                      hipFuncAttributeMaxDynamicSharedMemorySize, (int)run_lds(D));
+      if (e != hipSuccess) return (int)e;
+    }
+    hipLaunchKernelGGL((k_recurrent_run<TI, D>), grid_of(a, a.HV * (D / 64)), dim3(512), run_lds(D), s, a);
   }
   return (int)hipGetLastError();
 }
