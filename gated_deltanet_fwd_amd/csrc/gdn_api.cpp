@@ -1082,8 +1082,8 @@ int gdn_recurrent(const gdn_recurrent_problem* p, const void* q, const void* k, 
   CHECK(token_stride(p->q_stride, (int64_t)p->h_qk * p->d, p->dtype, "q_stride", &a.qs));
   CHECK(token_stride(p->k_stride, (int64_t)p->h_qk * p->d, p->dtype, "k_stride", &a.ks));
   CHECK(token_stride(p->v_stride, (int64_t)p->h_v * p->d, p->dtype, "v_stride", &a.vs));
-  if (std::max(std::max(a.qs, a.ks), a.vs) > (int64_t)1 << 28) // the kernels' offsets inside a few tokens are 32-bit
-    return fail(GDN_EINVAL, "token strides must be at most 2^28 elements");
+  if (std::max(std::max(a.qs, a.ks), a.vs) > (int64_t)1 << 24) // the kernels' offsets inside a few tokens are 32-bit
+    return fail(GDN_EINVAL, "token strides must be at most 2^24 elements");
   const int64_t T = p->n_tokens;
   CHECK(check_tok(q, "q", T));
   CHECK(check_tok(k, "k", T));

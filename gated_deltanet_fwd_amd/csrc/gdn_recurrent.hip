@@ -290,9 +290,21 @@ __global__ __launch_bounds__(512) void k_recurrent_run(RecurrentArgs a) {
     r.g = a.g[(int64_t)tok * a.HV + h];
     r.beta = a.beta[(int64_t)tok * a.HV + h];
   };
-  const auto load_v = [&](TI v[4], int t) { // tokens t + 4 g + s of this lane's column
+  // v and o of the block at t, through a buffer that ends with the sequence: tokens past the end load
+  // zeros and are not stored, and no branch makes a wait of one block's access cover another's
+  const auto rows_at = [&](const TI* p, int t, int64_t stride) {
+    const int64_t from = (int64_t)t * stride;
+    return make_rsrc(p + from, max(min(sp.t1 - t, C), 0) * (int)stride * (int)sizeof(TI));
+  };
+  const int lane_v = (4 * g * (int)a.vs + col) * (int)sizeof(TI), lane_o = (4 * g * os + col) * (int)sizeof(TI);
+  const auto load_v = [&](float v[4], int t) { // tokens t + 4 g + s of this lane's column
+    const __amdgpu_buffer_rsrc_t r = rows_at((const TI*)a.v, min(t, sp.t1), a.vs);
 #pragma unroll
-    for (int s = 0; s < 4; ++s) v[s] = ((const TI*)a.v)[(int64_t)min(t + 4 * g + s, sp.t1 - 1) * a.vs + col];
+    for (int s = 0; s < 4; ++s) {
+      const int off = lane_v + s * (int)a.vs * (int)sizeof(TI);
+      if constexpr (sizeof(TI) == 2) v[s] = (float)__builtin_bit_cast(bf16, __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0));
+      else v[s] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+    }
   };
   const auto all_groups = [](float x) { // sum over g, in every lane
     Pair p = swap16(x, copy_of(x));
@@ -379,10 +391,8 @@ __global__ __launch_bounds__(512) void k_recurrent_run(RecurrentArgs a) {
   // All of a block's operands are asked for before its first product: the waits for LDS, and for the
   // next block's v, would otherwise stand between the products (122 ns a token instead of NSTOK,
   // 64 wide, f32).
-  const auto block = [&](const Prep& b, TI v[4], int t) {
+  const auto block = [&](const Prep& b, const float v[4], int t) {
     f32x4 ka[4][R / 4], qa[4][R / 4], ua[4][R / 4];
-    TI next[4];
-    load_v(next, t + C);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -412,7 +422,7 @@ __global__ __launch_bounds__(512) void k_recurrent_run(RecurrentArgs a) {
     f32x4 rhs, u = zero4(), o;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      rhs[s] = __builtin_fmaf(-gk[s], ks[s], t + 4 * g + s < sp.t1 ? (float)v[s] : 0.f);
+      rhs[s] = __builtin_fmaf(-gk[s], ks[s], v[s]);
       o[s] = gq[s] * qs[s];
     }
 #pragma unroll
@@ -427,10 +437,13 @@ __global__ __launch_bounds__(512) void k_recurrent_run(RecurrentArgs a) {
     }
 #pragma unroll
     for (int s = 0; s < 4; ++s) o = mfma1(pa[s], u[s], o);
+    const __amdgpu_buffer_rsrc_t to = rows_at((const TI*)a.o, t, os);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      if (t + 4 * g + s < sp.t1) ((TI*)a.o)[(int64_t)(t + 4 * g + s) * os + col] = (TI)o[s];
-      v[s] = next[s];
+      const int off = lane_o + s * os * (int)sizeof(TI);
+      const TI x = (TI)o[s];
+      if constexpr (sizeof(TI) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(short, x), to, off, 0, 0);
+      else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(int, x), to, off, 0, 0);
     }
   };
   if (prepares) {
@@ -453,14 +466,20 @@ __global__ __launch_bounds__(512) void k_recurrent_run(RecurrentArgs a) {
       for (int i = 0; i < 4; ++i) S[r][i] = keepf(p[(4 * r + i) * D], sp.in >= 0);
   }
   if (sp.t0 < sp.t1) {
-    TI v[4];
-    load_v(v, sp.t0);
+    float v0[4], v1[4];
+    load_v(v0, sp.t0);
     int buf = 0;
     for (int t = sp.t0; t < sp.t1; t += NB * C, buf ^= NB) {
       __syncthreads();
       const int end = min(t + NB * C, sp.t1);
 #pragma unroll 1
-      for (int tb = t; tb < end; tb += C) block(prep[buf + (tb - t) / C], v, tb);
+      for (int tb = t; tb < end; tb += 2 * C) {
+        load_v(v1, tb + C);
+        block(prep[buf + (tb - t) / C], v0, tb);
+        if (tb + C >= end) break;
+        load_v(v0, tb + 2 * C);
+        block(prep[buf + (tb - t) / C + 1], v1, tb + C);
+      }
     }
   }
   if (sp.out >= 0) {
