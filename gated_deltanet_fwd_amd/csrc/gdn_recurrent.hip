@@ -388,11 +388,10 @@ __global__ __launch_bounds__(512) void k_recurrent_run(RecurrentArgs a) {
     for (int i = 0; i < C; ++i)
       if ((i >> 2) == g) b.t[i][n16] = T[i] * be;
   };
-  // All of a block's operands are asked for before its first product: the waits for LDS, and for the
-  // next block's v, would otherwise stand between the products (122 ns a token instead of NSTOK,
-  // 64 wide, f32).
-  const auto block = [&](const Prep& b, const float v[4], int t) {
-    f32x4 ka[4][R / 4], qa[4][R / 4], ua[4][R / 4];
+  // The operands of the products with S, read while the block before is finished: the waits for LDS
+  // would otherwise stand between the products.
+  f32x4 ka[4][R / 4], qa[4][R / 4];
+  const auto operands = [&](const Prep& b) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -400,11 +399,16 @@ __global__ __launch_bounds__(512) void k_recurrent_run(RecurrentArgs a) {
         ka[i][x] = *reinterpret_cast<const f32x4*>(&b.k[n16][g * DG + i * R + 4 * x]);
         qa[i][x] = *reinterpret_cast<const f32x4*>(&b.q[n16][g * DG + i * R + 4 * x]);
       }
+  };
+  // block i of the sequence, at token t
+  const auto block = [&](int i, const float v[4], int t) {
+    const Prep& b = prep[i % (2 * NB)];
     const f32x4 gk = *reinterpret_cast<const f32x4*>(&b.gk[4 * g]), gq = *reinterpret_cast<const f32x4*>(&b.gq[4 * g]);
     const f32x4 w = *reinterpret_cast<const f32x4*>(&b.w[4 * g]);
     const f32x4 ta = *reinterpret_cast<const f32x4*>(&b.t[n16][4 * g]), pa = *reinterpret_cast<const f32x4*>(&b.p[n16][4 * g]);
     const float last = b.g_last[0];
     // the update's: lane (g, 4 y + i): rows y D/4 + 4 r + i of token 4 g + s
+    f32x4 ua[4][R / 4];
 #pragma unroll
     for (int s = 0; s < 4; ++s)
 #pragma unroll
@@ -413,22 +417,31 @@ __global__ __launch_bounds__(512) void k_recurrent_run(RecurrentArgs a) {
     __builtin_amdgcn_sched_barrier(0);
     f32x4 ks = zero4(), qs = zero4();
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int y = 0; y < 4; ++y)
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        ks = mfma1(ka[i][r / 4][r % 4], S[r][i], ks);
-        qs = mfma1(qa[i][r / 4][r % 4], S[r][i], qs);
+        ks = mfma1(ka[y][r / 4][r % 4], S[r][y], ks);
+        qs = mfma1(qa[y][r / 4][r % 4], S[r][y], qs);
       }
-    f32x4 rhs, u = zero4(), o;
+    __builtin_amdgcn_sched_barrier(0);
+    if (t + C < sp.t1) {
+      if (i % NB == NB - 1) __syncthreads(); // the next turn is ready; of this one everything is in registers
+      operands(prep[(i + 1) % (2 * NB)]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    f32x4 rhs, u = zero4(), u2 = zero4(), o;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       rhs[s] = __builtin_fmaf(-gk[s], ks[s], v[s]);
       o[s] = gq[s] * qs[s];
     }
+    u = mfma1(ta[0], rhs[0], u);
+    u2 = mfma1(ta[1], rhs[1], u2);
+    u = mfma1(ta[2], rhs[2], u);
+    u2 = mfma1(ta[3], rhs[3], u2);
 #pragma unroll
     for (int r = 0; r < R; ++r) S[r] *= last;
-#pragma unroll
-    for (int s = 0; s < 4; ++s) u = mfma1(ta[s], rhs[s], u);
+    u += u2;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const float wu = w[s] * u[s]; // of token 4 g + s
@@ -468,18 +481,16 @@ __global__ __launch_bounds__(512) void k_recurrent_run(RecurrentArgs a) {
   if (sp.t0 < sp.t1) {
     float v0[4], v1[4];
     load_v(v0, sp.t0);
-    int buf = 0;
-    for (int t = sp.t0; t < sp.t1; t += NB * C, buf ^= NB) {
-      __syncthreads();
-      const int end = min(t + NB * C, sp.t1);
+    __syncthreads(); // the first turn is ready
+    operands(prep[0]);
+    int i = 0;
 #pragma unroll 1
-      for (int tb = t; tb < end; tb += 2 * C) {
-        load_v(v1, tb + C);
-        block(prep[buf + (tb - t) / C], v0, tb);
-        if (tb + C >= end) break;
-        load_v(v0, tb + 2 * C);
-        block(prep[buf + (tb - t) / C + 1], v1, tb + C);
-      }
+    for (int t = sp.t0; t < sp.t1; t += 2 * C, i += 2) {
+      load_v(v1, t + C);
+      block(i, v0, t);
+      if (t + C >= sp.t1) break;
+      load_v(v0, t + 2 * C);
+      block(i + 1, v1, t + C);
     }
   }
   if (sp.out >= 0) {
