@@ -9,7 +9,7 @@
 //
 // Columns of S (value indices) never mix, so a wave owns some columns of one head's state and keeps
 // them in registers from the first token to the last. Two kernels: k_recurrent_step for calls bound
-// by moving the states, k_recurrent_run for longer runs, bound by the chain from token to token.
+// by moving the states, k_recurrent_run for longer runs, bound by what a token computes.
 #include "gdn_device.h"
 
 namespace gdn {
@@ -244,7 +244,9 @@ __attribute__((amdgpu_waves_per_eu(KIND == ONE_TOKEN ? 3 : 1, KIND == ONE_TOKEN 
 // column n of S; with the rows in the order (i, r) -> g D/4 + 4 r + i the same registers are the
 // products' B operand and the update's accumulators. A product sums over the key rows in any order, so
 // the K and Q rows lie in LDS in the order that makes their A operands whole 16-byte reads.
-// What bounds it is the matrix unit: 104 (D = 128) or 56 (64) instructions of 32 cycles a block and wave.
+// What bounds it is the matrix unit, and the products' latency one after the other: 104 (D = 128) or 56
+// (64) instructions of 32 cycles a block and wave, of about 3,000 cycles that a block takes at D = 64
+// (700 tokens, f32: 65 us, 92 ns a token; token by token in the step kernel 680 ns).
 template <typename TI, int D>
 __global__ __launch_bounds__(512) void k_recurrent_run(RecurrentArgs a) {
   constexpr int C = 16, NB = 4, DG = D / 4, R = D / 16; // tokens a block, blocks a turn, rows a lane, tiles
@@ -509,14 +511,21 @@ static dim3 grid_of(const RecurrentArgs& a, int x) {
   return dim3((unsigned)x, n < MAX_GRID_Y ? n : MAX_GRID_Y, (n + MAX_GRID_Y - 1) / MAX_GRID_Y);
 }
 
+// The kernel by the longest sequence and the number of sequences with tokens, as the host knows them.
+// A run's workgroup pays for whole blocks of 16 tokens and is alone on its CU (D = 128), so with more
+// workgroups than CUs it gains later (us step / run, 48 heads, 128 wide, bf16: 1 sequence of 4 tokens
+// 7.7 / 8.3, of 8 12.2 / 8.2, of 64 64 / 14; 32 sequences of 8 tokens 56 / 82, of 12 73 / 81, of 16
+// 89 / 83, of 64 278 / 158; 64 wide, f32, 4 sequences of 8 tokens 8.9 / 6.5, 64 of 16 58 / 61, of 24
+// 79 / 75). With slot_tok every token's state is wanted: always the step.
 template <typename TI, int D>
 static int recurrent_t(const RecurrentArgs& a, hipStream_t s) {
+  const int64_t run_groups = (int64_t)a.live * a.HV * (D / 64);
   const dim3 step = grid_of(a, (a.HV * (D / 32) + 3) / 4);
   if (!a.cu && !a.slot_tok) {
     hipLaunchKernelGGL((k_recurrent_step<TI, D, ONE_TOKEN>), step, dim3(256), STEP_LDS, s, a);
   } else if (a.slot_tok) {
     hipLaunchKernelGGL((k_recurrent_step<TI, D, KEEP_EACH>), step, dim3(256), STEP_LDS, s, a);
-  } else if (a.longest <= 6) {
+  } else if (a.longest <= (run_groups <= 256 ? 6 : 12)) {
     hipLaunchKernelGGL((k_recurrent_step<TI, D, RUN_OF_TOKENS>), step, dim3(256), STEP_LDS, s, a);
   } else {
     if constexpr (run_lds(D) > 64 * 1024) {
