@@ -106,6 +106,73 @@ def test_recurrent(name, l2norm):
     check("states", states, st_ref, K)
 
 
+# runs go 16 tokens at a time, 64 a turn: lengths at and beside both, and sequences that end in a block
+RUNS = {
+    "bf16_128": dict(lengths=[16, 17, 15, 64, 65, 63, 129, 1, 0, 128], H=2, HV=4, d=128, fresh=(3, 8)),
+    "f32_64_packed": dict(lengths=[80, 7, 33, 0, 192, 97], H=1, HV=3, d=64, dtype=torch.float32, packed=True, fresh=(1,)),
+    "f32_128": dict(lengths=[31, 48], H=2, HV=2, d=128, dtype=torch.float32),
+    "bf16_64_many": dict(lengths=[13] * 40 + [70], H=2, HV=8, d=64),
+    "keep_long": dict(lengths=[40, 3], H=1, HV=2, d=128, keep=True),
+}
+
+
+@pytest.mark.parametrize("gates", ["drawn", "strong", "rising", "none"])
+@pytest.mark.parametrize("name", RUNS)
+def test_runs(name, gates):
+    """Decays as the layer draws them; down to e^-80 and to nothing in places; log decays above 0; no
+    decay, full writes and nearly equal keys, where the block's inverse has the largest entries."""
+    s = make(**RUNS[name])
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(1)
+    if gates == "strong":
+        pick = torch.rand(s["g"].shape, generator=gen, device=DEV)
+        s["g"][pick < 0.2], s["g"][pick > 0.9] = -80.0, -1e30
+    elif gates == "rising":
+        s["g"] = 0.05 * torch.rand(s["g"].shape, generator=gen, device=DEV)
+    elif gates == "none":
+        s["g"][:], s["beta"][:] = 0.0, 1.0
+        s["k"].copy_((s["k"][:1].float() + 0.05 * s["k"].float()).to(s["k"].dtype))
+    o, states = run(s)
+    o_ref, st_ref = reference(s)
+    # with no decay a state remembers every token: its roundings add up over the run
+    k = K * (4 if gates in ("rising", "none") else 1)
+    check("o", o, o_ref, k)
+    check("states", states, st_ref, k)
+
+
+def test_a_run_does_not_see_its_neighbours():
+    """Rows before and after a sequence hold NaN (another sequence's): blocks that end inside the turn
+    and loads past the end must not let them in."""
+    s = make([20, 37, 70], 1, 2, 64)
+    clean = run(s)
+    for x in ("q", "k", "v", "g", "beta"):
+        s[x][:20], s[x][57:] = float("nan"), float("nan")
+    o, states = run(s)
+    assert torch.equal(o[20:57], clean[0][20:57])
+    slot = s["slot_out"][1].long()
+    assert torch.equal(states[slot], clean[1][slot])
+    assert torch.isnan(o[:20].float()).all() and torch.isnan(o[57:].float()).all()
+
+
+def test_a_run_then_steps_equal_the_whole_run():
+    s = make([50, 23], 2, 4, 128, dtype=torch.float32)
+    o, states = run(s)
+    cut = make([50, 23], 2, 4, 128, dtype=torch.float32)
+    rows = [slice(0, 41), slice(50, 64)]
+    part = {x: torch.cat([cut[x][r] for r in rows]) for x in ("q", "k", "v", "g", "beta")}
+    p = G.RecurrentProblem(2, 2, 4, 128, cut["slots"], cu_seqlens_host=[0, 41, 55], dtype=torch.float32)
+    st = cut["states"]
+    G.gdn_recurrent(p, *part.values(), st, cut["slot_in"], cut["slot_out"],
+                    cu_seqlens=torch.tensor([0, 41, 55], dtype=torch.int32, device=DEV))
+    one = G.RecurrentProblem(2, 2, 4, 128, cut["slots"], dtype=torch.float32)
+    for i in range(9):
+        at = torch.tensor([41 + i, 64 + i], device=DEV)
+        got = G.gdn_recurrent(one, *(cut[x][at] for x in ("q", "k", "v", "g", "beta")), st, cut["slot_out"], cut["slot_out"])
+        check("o", got, f64(o[at]), 2 * K)
+    torch.cuda.synchronize()
+    check("states", st, f64(states), 2 * K)
+
+
 def test_slots_not_named_are_untouched_and_sequences_may_share_a_start():
     s = make([1, 2, 3], 2, 4, 64)
     s["slot_in"][:] = s["slot_in"][0]  # one prompt's state, three continuations
