@@ -233,7 +233,9 @@ int gdn_conv_bwd(const gdn_conv_problem* p, const void* x, const float* weight, 
  * order and leaves its last state in states[slot_out[n]] (nowhere if -1; a sequence of no tokens
  * leaves its start state). slot_in[n] = slot_out[n] updates a state in place. slot_tok, if given,
  * names for each token the slot that keeps the state after it (-1: none), so that a run of drafted
- * tokens can be rolled back to any of them.
+ * tokens can be rolled back to any of them. All arithmetic is FP32. Longer sequences (by the host's
+ * lengths; without slot_tok) are taken 16 tokens at a time: an infinity or NaN in a row then reaches
+ * the outputs of its sequence's block of 16 tokens, not only the later ones.
  *
  *   q, k      [T, H, d], v [T, HV, d]  io dtype; a token's heads are contiguous, tokens are
  *                                      q_stride, k_stride, v_stride elements apart
@@ -258,9 +260,9 @@ typedef struct gdn_recurrent_problem {
   int32_t l2norm_qk;              /* 1: L2-normalise q and k rows inside the kernel */
   int32_t n_slots;                /* states in the cache, >= 1 */
   int32_t reserved0;              /* must be 0 */
-  int64_t q_stride;               /* elements from one token's q to the next (0: H * d); the same */
-  int64_t k_stride;               /* for k (0: H * d) and v (0: HV * d). Rows are 16-byte aligned */
-  int64_t v_stride;
+  int64_t q_stride;               /* elements from one token's q to the next (0: H * d, at most */
+  int64_t k_stride;               /* 2^24); the same for k (0: H * d) and v (0: HV * d). Rows are */
+  int64_t v_stride;               /* 16-byte aligned */
   const int32_t* cu_seqlens_host; /* host copy of cu_seqlens, read during each call only; NULL: one
                                      token a sequence */
 } gdn_recurrent_problem;
@@ -309,7 +311,7 @@ typedef struct gdn_qk_rope_problem {
   int64_t qo_stride;   /* of q_out and dq_out, */
   int64_t ko_stride;   /* of k_out and dk_out, */
   int64_t dq_stride;   /* of dq */
-  int64_t dk_stride;   /* and of dk (the backward's). Rows are 16-byte aligned */
+  int64_t dk_stride;   /* and of dk (the backward's). At most 2^27; rows are 16-byte aligned */
 } gdn_qk_rope_problem;
 
 /* Frequencies of the rotation, on the host: freqs[i] (rotary_dim / 2 of them) and the magnitude,

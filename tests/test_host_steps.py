@@ -34,7 +34,7 @@ def _recurrent(p, **over):
     ("n_seqs", 0, "n_seqs", 1), ("h_qk", 0, "head counts", 1), ("h_v", 5, "multiple", 1), ("d", 96, "64 or 128", 2),
     ("dtype", 7, "dtype", 2), ("n_slots", 0, "n_slots", 1), ("reserved0", 1, "reserved0", 1),
     ("n_tokens", 5, "n_tokens", 1), ("q_stride", 8, "q_stride", 1), ("k_stride", 2 * 64 + 4, "aligned", 1),
-    ("v_stride", -512, "v_stride", 1)])
+    ("v_stride", -512, "v_stride", 1), ("v_stride", 1 << 25, "2^24", 1), ("h_v", 65538, "65536", 1)])
 def test_recurrent_refuses_bad_problems(field, value, fragment, code):
     p = G.RecurrentProblem(3, 2, 4, 64, 8)
     setattr(p.st, field, value)
@@ -107,7 +107,7 @@ def _rope(p, back=False, **over):
     ("rotary_dim", 12, "rotary_dim", 1), ("rotary_dim", -8, "rotary_dim", 1), ("eps", -1.0, "eps", 1),
     ("eps", float("nan"), "eps", 1), ("magnitude", float("inf"), "magnitude", 1), ("reserved0", 1, "reserved0", 1),
     ("q_stride", 64, "q_stride", 1), ("k_stride", 132, "aligned", 1), ("qo_stride", -8, "qo_stride", 1),
-    ("ko_stride", 130, "aligned", 1)])
+    ("ko_stride", 130, "aligned", 1), ("q_stride", 1 << 28, "2^27", 1)])
 def test_rope_refuses_bad_problems(field, value, fragment, code, back):
     p = G.QkRopeProblem(10, 2, 2, 64)
     setattr(p.st, field, value)
