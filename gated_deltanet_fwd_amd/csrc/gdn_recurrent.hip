@@ -10,27 +10,23 @@
 // Columns of S (value indices) never mix, so a wave owns some columns of one head's state and keeps
 // them in registers from the first token to the last. Two kernels: k_recurrent_step for calls bound
 // by moving the states, k_recurrent_run for longer runs, bound by what a token computes.
+#include <atomic>
+
 #include "gdn_device.h"
 
 namespace gdn {
 
 constexpr unsigned MAX_GRID_Y = 65535;
 
-template <typename T, int N>
+template <typename T, int N> // N elements of a row; rows are 16-byte aligned, no more
 struct Vec {
-  typedef T type __attribute__((ext_vector_type(N)));
-};
-template <typename T>
-struct Vec<T, 1> {
-  typedef T type;
+  typedef T type __attribute__((ext_vector_type(N), aligned(16)));
 };
 
 template <typename T, int N>
 __device__ __forceinline__ void unpack(const typename Vec<T, N>::type& r, float* v) {
-  if constexpr (N == 1) v[0] = (float)r;
-  else
 #pragma unroll
-    for (int e = 0; e < N; ++e) v[e] = (float)r[e];
+  for (int e = 0; e < N; ++e) v[e] = (float)r[e];
 }
 
 __device__ __forceinline__ float lane_value(float x, int lane) {
@@ -237,20 +233,22 @@ __attribute__((amdgpu_waves_per_eu(KIND == ONE_TOKEN ? 3 : 1, KIND == ONE_TOKEN 
 //   O = diag(G) Qh S + P U,                      P_ij = D_ij qh_i.kh_j         (j <= i)
 //   S <- G_15 S + Kh^T diag(D_15,j) U
 //
-// in FP32 throughout, the products on v_mfma_f32_16x16x4. A workgroup holds 64 columns of a state, 16
-// in each of its first four waves, and takes 4 blocks a turn. What does not depend on S (Gram products,
-// decays, the inverse T of I + L by forward substitution) the other four waves prepare in LDS a turn
-// ahead, a block each. Lane (g, n) = (lane / 16, lane % 16) holds rows g D/4 .. of
+// in FP32 throughout, the products on v_mfma_f32_16x16x4. A workgroup holds 16 NB columns of a state, 16
+// in each of its first NB waves, and takes NB blocks a turn. What does not depend on S (Gram products,
+// decays, the inverse T of I + L by forward substitution) the other NB waves prepare in LDS a turn
+// ahead, a block each. With NB = 2 every wave has a SIMD to itself, and neither half waits for the
+// other's matrix instructions; with NB = 4 half as much is prepared for the same columns. Lane (g, n) = (lane / 16, lane % 16) holds rows g D/4 .. of
 // column n of S; with the rows in the order (i, r) -> g D/4 + 4 r + i the same registers are the
 // products' B operand and the update's accumulators. A product sums over the key rows in any order, so
 // the K and Q rows lie in LDS in the order that makes their A operands whole 16-byte reads.
 // What bounds it is the matrix unit, and the products' latency one after the other: 104 (D = 128) or 56
-// (64) instructions of 32 cycles a block and wave, of about 3,000 cycles that a block takes at D = 64
-// (700 tokens, f32: 65 us, 92 ns a token; token by token in the step kernel 680 ns).
-template <typename TI, int D>
-__global__ __launch_bounds__(512) void k_recurrent_run(RecurrentArgs a) {
-  constexpr int C = 16, NB = 4, DG = D / 4, R = D / 16; // tokens a block, blocks a turn, rows a lane, tiles
-  constexpr int LD = D + 4, LT = 20;                    // LDS row strides
+// (64) instructions of 32 cycles a block and wave, of about 2,300 cycles that a block takes at D = 64
+// (700 tokens, f32: 50 us with 8 heads and 5 sequences, 72 ns a token; with nothing left to prepare
+// 49 us; token by token in the step kernel 680 ns a token).
+template <typename TI, int D, int NB>
+__global__ __launch_bounds__(128 * NB, 2) void k_recurrent_run(RecurrentArgs a) {
+  constexpr int C = 16, DG = D / 4, R = D / 16; // tokens a block, rows a lane, tiles
+  constexpr int LD = D + 4, LT = 20;            // LDS row strides
   typedef typename Vec<TI, 8>::type vec8;
   struct alignas(16) Prep { // of one block
     float k[C][LD], q[C][LD]; // rows, permuted
@@ -260,12 +258,12 @@ __global__ __launch_bounds__(512) void k_recurrent_run(RecurrentArgs a) {
   extern __shared__ __attribute__((aligned(16))) float lds[];
   Prep* prep = reinterpret_cast<Prep*>(lds); // of two turns
   const int lane = threadIdx.x & 63, g = lane >> 4, n16 = lane & 15;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wv = wave & 3;
-  const bool prepares = wave >= 4;
-  const int h = blockIdx.x / (D / 64), j = (int)(((uint64_t)h * a.g_mul) >> 32);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wv = wave & (NB - 1);
+  const bool prepares = wave >= NB;
+  const int h = blockIdx.x / (D / (16 * NB)), j = (int)(((uint64_t)h * a.g_mul) >> 32);
   const int n = blockIdx.z * MAX_GRID_Y + blockIdx.y;
   if (n >= a.N) return;
-  const int col = h * D + (blockIdx.x % (D / 64)) * 64 + wv * 16 + n16; // in a row of v and o
+  const int col = h * D + (blockIdx.x % (D / (16 * NB))) * (16 * NB) + wv * 16 + n16; // in a row of v and o
   const int os = a.HV * D;
   const SeqSpan sp = seq_span(a.cu, a.slot_in, a.slot_out, n, a.T, a.n_slots);
   if (!sp.ok) {
@@ -275,13 +273,13 @@ __global__ __launch_bounds__(512) void k_recurrent_run(RecurrentArgs a) {
   const int64_t hd = (int64_t)a.HV * D * D, head = (int64_t)h * D * D;
   const int at = g * DG * D + (col - h * D);
   f32x4 S[R];
-  // this wave's block of the turn at t: lane (g, i) loads token i's rows g D/4 .. of k and q
+  // the block at t: lane (g, i) loads token i's rows g D/4 .. of k and q
   struct Rows {
     vec8 k[DG / 8], q[DG / 8];
     float g, beta;
   };
   const auto load = [&](Rows& r, int t) {
-    const int tok = min(t + wv * C + n16, sp.t1 - 1);
+    const int tok = min(t + n16, sp.t1 - 1);
     const TI* kp = (const TI*)a.k + (int64_t)tok * a.ks + (j * D + g * DG);
     const TI* qp = (const TI*)a.q + (int64_t)tok * a.qs + (j * D + g * DG);
 #pragma unroll
@@ -314,7 +312,7 @@ __global__ __launch_bounds__(512) void k_recurrent_run(RecurrentArgs a) {
     return p.x + p.y;
   };
   const auto mfma1 = [](float x, float y, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(x, y, c, 0, 0, 0); };
-  const auto prepare = [&](Prep& b, const Rows& r, int t) {
+  const auto prepare = [&](Prep& b, Rows& r, int t) { // r then takes the wave's block of the next turn
     const bool live = t + n16 < sp.t1; // tokens past the end: zero rows, no decay, nothing written
     float kf[DG], qf[DG];
 #pragma unroll
@@ -342,9 +340,13 @@ __global__ __launch_bounds__(512) void k_recurrent_run(RecurrentArgs a) {
         *reinterpret_cast<f32x4*>(&b.q[n16][g * DG + i * R + x]) =
             f32x4{qf[4 * x + i], qf[4 * x + 4 + i], qf[4 * x + 8 + i], qf[4 * x + 12 + i]};
       }
+    const float al = live ? __expf(r.g) : 1.f, be = live ? r.beta : 0.f;
+    // What follows hides the loads: run 700 above 55 us instead of 58 with NB = 2 and consumers that
+    // only wait. With NB = 4 the rest is the longer half, and they cost it 3% (12 sequences of 300
+    // tokens, 48 heads, 128 wide: 151 us, 146 with the loads at the end).
+    if constexpr (NB == 2) load(r, t + NB * C);
     const float rk = a.l2norm ? inv_sqrt(all_groups(kk) + 1e-6f) : 1.f;
     const float rq = a.l2norm ? inv_sqrt(all_groups(qq) + 1e-6f) : 1.f;
-    const float al = live ? __expf(r.g) : 1.f, be = live ? r.beta : 0.f;
     // running products: G of token n16, and D_ij of this lane's column j = n16
     float gp = 1.f, gi = 1.f, d = 0.f, dij[4];
 #pragma unroll
@@ -389,6 +391,7 @@ __global__ __launch_bounds__(512) void k_recurrent_run(RecurrentArgs a) {
 #pragma unroll
     for (int i = 0; i < C; ++i)
       if ((i >> 2) == g) b.t[i][n16] = T[i] * be;
+    if constexpr (NB > 2) load(r, t + NB * C);
   };
   // The operands of the products with S, read while the block before is finished: the waits for LDS
   // would otherwise stand between the products.
@@ -464,11 +467,10 @@ __global__ __launch_bounds__(512) void k_recurrent_run(RecurrentArgs a) {
   if (prepares) {
     if (sp.t0 >= sp.t1) return;
     Rows r;
-    load(r, sp.t0);
+    load(r, sp.t0 + wv * C);
     int buf = 0;
     for (int t = sp.t0; t < sp.t1; t += NB * C, buf ^= NB) {
       if (t + wv * C < sp.t1) prepare(prep[buf + wv], r, t + wv * C);
-      if (t + NB * C < sp.t1) load(r, t + NB * C);
       __syncthreads(); // this turn is ready, and the one before it has been used
     }
     return;
@@ -503,38 +505,54 @@ __global__ __launch_bounds__(512) void k_recurrent_run(RecurrentArgs a) {
       for (int i = 0; i < 4; ++i) p[(4 * r + i) * D] = S[r][i];
   }
 }
-// LDS of a workgroup: the rows, T, P and factors of two turns of 4 blocks
-constexpr unsigned run_lds(int D) { return 8 * 4 * (2 * 16 * (D + 4) + 2 * 16 * 20 + 4 * 16); }
+// LDS of a workgroup: the rows, T, P and factors of two turns of NB blocks
+constexpr unsigned run_lds(int D, int NB) { return 2 * NB * 4 * (2 * 16 * (D + 4) + 2 * 16 * 20 + 4 * 16); }
 
 static dim3 grid_of(const RecurrentArgs& a, int x) {
   const unsigned n = (unsigned)a.N;
   return dim3((unsigned)x, n < MAX_GRID_Y ? n : MAX_GRID_Y, (n + MAX_GRID_Y - 1) / MAX_GRID_Y);
 }
 
+template <typename TI, int D, int NB>
+static int run_t(const RecurrentArgs& a, hipStream_t s) {
+  constexpr unsigned lds = run_lds(D, NB);
+  if constexpr (lds > 64 * 1024) { // more than the runtime gives unasked: asked for once on each device
+    static std::atomic<uint64_t> asked{0};
+    int dev = 0;
+    if (const hipError_t e = hipGetDevice(&dev)) return (int)e;
+    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+    if (!(asked.load(std::memory_order_relaxed) & bit)) {
+      const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_recurrent_run<TI, D, NB>),
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+      if (e != hipSuccess) return (int)e;
+      asked.fetch_or(bit, std::memory_order_relaxed);
+    }
+  }
+  hipLaunchKernelGGL((k_recurrent_run<TI, D, NB>), grid_of(a, a.HV * (D / (16 * NB))), dim3(128 * NB), lds, s, a);
+  return (int)hipGetLastError();
+}
+
 // The kernel by the longest sequence and the number of sequences with tokens, as the host knows them.
-// A run's workgroup pays for whole blocks of 16 tokens and is alone on its CU (D = 128), so with more
-// workgroups than CUs it gains later (us step / run, 48 heads, 128 wide, bf16: 1 sequence of 4 tokens
-// 7.7 / 8.3, of 8 12.2 / 8.2, of 64 64 / 14; 32 sequences of 8 tokens 56 / 82, of 12 73 / 81, of 16
-// 89 / 83, of 64 278 / 158; 64 wide, f32, 4 sequences of 8 tokens 8.9 / 6.5, 64 of 16 58 / 61, of 24
-// 79 / 75). With slot_tok every token's state is wanted: always the step.
+// A run's workgroup pays for whole blocks of 16 tokens and is alone on its CU (D = 128, NB = 4), so with
+// more workgroups than CUs it gains later (us step / run, 48 heads, 128 wide, bf16: 1 sequence of 4
+// tokens 7.7 / 8.3, of 8 12.2 / 8.2, of 64 64 / 14; 32 sequences of 8 tokens 56 / 82, of 12 73 / 81, of
+// 16 89 / 83, of 64 278 / 158; 64 wide, f32, 4 sequences of 8 tokens 8.9 / 6.5, 64 of 16 58 / 61, of 24
+// 79 / 75). 32 columns a workgroup while each then has a CU, 64 beyond (us with 32 / 64, 48 heads, 256
+// tokens, 128 wide, bf16: 1 sequence 35 / 43, 2 61 / 47; 64 wide, f32: 2 sequences 23 / 27, 3 37 / 29).
+// With slot_tok every token's state is wanted: always the step.
 template <typename TI, int D>
 static int recurrent_t(const RecurrentArgs& a, hipStream_t s) {
+  constexpr int CUS = 256;
   const int64_t run_groups = (int64_t)a.live * a.HV * (D / 64);
   const dim3 step = grid_of(a, (a.HV * (D / 32) + 3) / 4);
-  if (!a.cu && !a.slot_tok) {
-    hipLaunchKernelGGL((k_recurrent_step<TI, D, ONE_TOKEN>), step, dim3(256), STEP_LDS, s, a);
-  } else if (a.slot_tok) {
+  if (a.slot_tok) {
     hipLaunchKernelGGL((k_recurrent_step<TI, D, KEEP_EACH>), step, dim3(256), STEP_LDS, s, a);
-  } else if (a.longest <= (run_groups <= 256 ? 6 : 12)) {
+  } else if (!a.cu) {
+    hipLaunchKernelGGL((k_recurrent_step<TI, D, ONE_TOKEN>), step, dim3(256), STEP_LDS, s, a);
+  } else if (a.longest <= (run_groups <= CUS ? 6 : 12)) {
     hipLaunchKernelGGL((k_recurrent_step<TI, D, RUN_OF_TOKENS>), step, dim3(256), STEP_LDS, s, a);
   } else {
-    if constexpr (run_lds(D) > 64 * 1024) {
-      // the runtime's limit without this is 64 KiB; it is set once for the process
-      static const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_recurrent_run<TI, D>),
-                                                      hipFuncAttributeMaxDynamicSharedMemorySize, (int)run_lds(D));
-      if (e != hipSuccess) return (int)e;
-    }
-    hipLaunchKernelGGL((k_recurrent_run<TI, D>), grid_of(a, a.HV * (D / 64)), dim3(512), run_lds(D), s, a);
+    return 2 * run_groups <= CUS ? run_t<TI, D, 2>(a, s) : run_t<TI, D, 4>(a, s);
   }
   return (int)hipGetLastError();
 }

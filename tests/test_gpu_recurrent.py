@@ -140,6 +140,37 @@ def test_runs(name, gates):
     check("states", states, st_ref, k)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_runs_of_many_columns(dtype, d):
+    """More columns of 32 than the card has CUs: workgroups of 64 columns and 64 tokens a turn."""
+    s = make([80, 7, 33, 0, 129, 64, 65, 63, 16, 1], H=4, HV=32, d=d, dtype=dtype, fresh=(2, 3))
+    o, states = run(s)
+    o_ref, st_ref = reference(s)
+    check("o", o, o_ref, K)
+    check("states", states, st_ref, K)
+
+
+@pytest.mark.parametrize("HV", [2, 48])
+def test_runs_in_a_graph(HV):
+    s = make([40, 70, 5], H=2, HV=HV, d=128)
+    p = G.RecurrentProblem(3, 2, HV, 128, s["slots"], cu_seqlens_host=s["cu_host"])
+    out = torch.tensor([i for i in range(s["slots"]) if i not in s["slot_in"].tolist()], dtype=torch.int32, device=DEV)
+    call = lambda st: G.gdn_recurrent(p, *(s[x] for x in ("q", "k", "v", "g", "beta")), st, s["slot_in"], out, cu_seqlens=s["cu"])
+    eager_states = s["states"].clone()
+    eager = call(eager_states)
+    states = s["states"].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o = call(states)
+    for _ in range(3):
+        states.copy_(s["states"])
+        o.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, eager) and torch.equal(states, eager_states)
+
+
 def test_a_run_does_not_see_its_neighbours():
     """Rows before and after a sequence hold NaN (another sequence's): blocks that end inside the turn
     and loads past the end must not let them in."""
