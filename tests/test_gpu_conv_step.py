@@ -152,6 +152,29 @@ def test_on_a_stream_of_its_own():
     assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
 
 
+@pytest.mark.parametrize("T", [3, 4000], ids=["short", "long"])
+def test_outputs_made_by_the_call_do_not_meet(T):
+    """A short call's outputs are parts of one allocation, a long one's are not."""
+    s = make([1] * T, [24, 8, 136])
+    p = G.ConvStepProblem(T, s["groups"], s["slots"])
+    call = lambda **kw: G.gdn_conv_step(p, s["x"], s["weight"], s["bias"], s["windows"].clone(), s["slot_in"], s["slot_out"], **kw)
+    given = [torch.empty(T, c, dtype=torch.bfloat16, device=DEV) for c in s["groups"]]
+    call(outs=given)
+    made = call()
+    for y, z in zip(made, given):
+        assert y.shape == z.shape and y.dtype == z.dtype and y.is_contiguous() and y.data_ptr() % 512 == 0
+        assert torch.equal(y, z)
+    for i, y in enumerate(made):
+        y.fill_(float("nan"))
+        for x, z in list(zip(made, given))[i + 1:]:
+            assert torch.equal(x, z)
+    assert all(torch.isnan(y).all() for y in made)
+    assert len({y.untyped_storage().data_ptr() for y in made}) == (1 if T == 3 else 3)
+    kept = call()[1]  # the others are released: the part keeps its memory
+    fill = [torch.full((1 << 16,), 7.0, device=DEV) for _ in range(4)]
+    assert torch.equal(kept, given[1]) and len(fill) == 4
+
+
 def test_binding_refuses_wrong_tensors():
     s = make([1, 1], [16, 8])
     p = G.ConvStepProblem(2, s["groups"], s["slots"])
