@@ -20,7 +20,7 @@ constexpr unsigned MAX_GRID_Y = 65535;
 
 template <typename T, int N> // N elements of a row; rows are 16-byte aligned, no more
 struct Vec {
-  typedef T type __attribute__((ext_vector_type(N), aligned(16)));
+  typedef T type __attribute__((ext_vector_type(N), aligned(N * sizeof(T) < 16 ? N * sizeof(T) : 16)));
 };
 
 template <typename T, int N>
@@ -56,9 +56,10 @@ __device__ __forceinline__ float copy_of(float x) {
   return x;
 }
 
-// The wave's place in a grid of (heads x blocks of columns / 4, sequences); cb counts within a state.
+// The wave's place in a grid of (heads x blocks of columns / waves a workgroup, sequences); cb counts
+// within a state.
 __device__ __forceinline__ bool wave_of(const RecurrentArgs& a, int blocks, int* n, int* h, int* j, int* cb) {
-  const int w = (int)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int w = (int)(blockIdx.x * (blockDim.x >> 6)) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   *n = (int)(blockIdx.z * MAX_GRID_Y + blockIdx.y);
   *h = w / blocks;
   *cb = w % blocks;
@@ -70,8 +71,10 @@ __device__ __forceinline__ bool wave_of(const RecurrentArgs& a, int blocks, int*
 constexpr int NT = 2, WRITE_THROUGH = 19;
 
 // ------------------------------------------------------------------------------------------------
-// One token, or a few: a wave holds 32 columns, lane (kg, cg) = (lane / 8, lane % 8) the D / 8 keys
-// from kg D / 8 on of columns 4 cg .. 4 cg + 3, so a load or store covers whole 128-byte lines.
+// One token, or a few: a wave holds COLS = 32 columns, lane (kg, cg) = (lane / 8, lane % 8) the D / 8
+// keys from kg D / 8 on of columns 4 cg .. 4 cg + 3, so a load or store covers whole 128-byte lines.
+// (COLS = 16, for few waves and several tokens: half the lanes a row, twice the groups of keys, and
+// half of the arithmetic a token, which is what a chain of tokens waits for.)
 // What it costs is moving the states. They are read and written non-temporally: they are not used
 // again before the next step, and the same pattern without it moves a tenth less. With one token a
 // sequence each row of the new state leaves as it is made, and few waves share a CU: a workgroup asks
@@ -86,19 +89,19 @@ constexpr unsigned STEP_LDS = 64 * 1024;
 
 enum StepKind { ONE_TOKEN, RUN_OF_TOKENS, KEEP_EACH }; // one token a sequence; several; with slot_tok
 
-template <typename TI, int D, StepKind KIND>
+template <typename TI, int D, StepKind KIND, int COLS>
 __global__ __launch_bounds__(256)
 __attribute__((amdgpu_waves_per_eu(KIND == ONE_TOKEN ? 3 : 1, KIND == ONE_TOKEN ? 3 : 8))) void k_recurrent_step(RecurrentArgs a) {
-  constexpr int KPL = D / 8, CB = D / 32;
+  constexpr int CG = COLS / 4, KPL = D * CG / 64, CB = D / COLS; // lanes a row, keys a lane, waves a state
   typedef typename Vec<TI, KPL>::type kvec;
-  const int lane = threadIdx.x & 63, cg = lane & 7, kg = lane >> 3;
+  const int lane = threadIdx.x & 63, cg = lane % CG, kg = lane / CG;
   int n, h, j, cb; // sequence, value head, q/k head, block of columns
   if (!wave_of(a, CB, &n, &h, &j, &cb)) return;
-  cb *= 32;
+  cb *= COLS;
   // after the sums over the keys a lane keeps the totals of one column, 2 (lane / 32) + lane / 16 % 2
   // of its four, and the value and output of that column
   const int col = cb + 4 * cg + 2 * (lane >> 5) + ((lane >> 4) & 1);
-  const bool writes = !(lane & 8);
+  const bool writes = !(lane & (16 - CG));
   TI* o = (TI*)a.o + (int64_t)h * D + col;
   const int64_t os = (int64_t)a.HV * D;
   const SeqSpan sp = seq_span(a.cu, a.slot_in, a.slot_out, n, a.T, a.n_slots);
@@ -138,8 +141,12 @@ __attribute__((amdgpu_waves_per_eu(KIND == ONE_TOKEN ? 3 : 1, KIND == ONE_TOKEN 
     r.beta = a.beta[(int64_t)t * a.HV + h];
     if constexpr (KIND == KEEP_EACH) r.st = a.slot_tok[t];
   };
-  const auto all = [](float x) { // sum over the key groups, in every lane
-    x += dpp<0x128>(x);
+  const auto row_sum = [](float x) { // over the key groups of a row of 16 lanes, in every lane
+    if constexpr (COLS == 16) x += dpp<0x124>(x);
+    return x + dpp<0x128>(x);
+  };
+  const auto all = [&](float x) { // sum over the key groups, in every lane
+    x = row_sum(x);
     Pair p = swap16(x, copy_of(x));
     p = swap32(p.x + p.y, copy_of(p.x + p.y));
     return p.x + p.y;
@@ -169,8 +176,8 @@ __attribute__((amdgpu_waves_per_eu(KIND == ONE_TOKEN ? 3 : 1, KIND == ONE_TOKEN 
       }
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      s1[c] += dpp<0x128>(s1[c]);
-      s2[c] += dpp<0x128>(s2[c]);
+      s1[c] = row_sum(s1[c]);
+      s2[c] = row_sum(s2[c]);
     }
     Pair x0 = swap32(s1[0], s1[2]), x1 = swap32(s1[1], s1[3]);
     Pair y0 = swap32(s2[0], s2[2]), y1 = swap32(s2[1], s2[3]);
@@ -532,6 +539,29 @@ static int run_t(const RecurrentArgs& a, hipStream_t s) {
   return (int)hipGetLastError();
 }
 
+// The step kernel, its columns a wave and waves a workgroup by the number of waves of 32 columns. With
+// few, a wave to a workgroup spreads them over more CUs, so that their stores do not queue at one (us
+// in workgroups of 4 / 1, 128 wide, bf16: one token 192 waves 4.3 / 3.7, 768 5.4 / 5.2, 1152 8.0 / 6.8,
+// 3072 19.0 / 21.1; 6 kept tokens 192 waves 12.4 / 10.1, 768 15.8 / 15.8, 1152 27 / 25, 3072 67 / 72).
+// With fewer still, and several tokens, 16 columns (us with 32 / 16: 6 kept tokens, one wave a
+// workgroup, 64 waves 9.7 / 8.1, 192 10.1 / 9.6, 384 11.6 / 11.8, 576 13.6 / 16.1; 5 tokens, four waves a
+// workgroup, 64 waves 8.0 / 6.3, 384 9.4 / 7.2, 576 9.8 / 9.4, 1152 15 / 16).
+template <typename TI, int D, StepKind KIND>
+static int step_t(const RecurrentArgs& a, hipStream_t s) {
+  constexpr int64_t SPREAD = 1280, HALVED = 384;
+  const int64_t waves = (int64_t)a.live * a.HV * (D / 32);
+  if (KIND != ONE_TOKEN && a.longest > 1 && waves <= HALVED) {
+    constexpr int GROUP = KIND == KEEP_EACH ? 1 : 4, COLS = KIND == ONE_TOKEN ? 32 : 16;
+    hipLaunchKernelGGL((k_recurrent_step<TI, D, KIND, COLS>), grid_of(a, (a.HV * (D / COLS) + GROUP - 1) / GROUP),
+                       dim3(64 * GROUP), 0, s, a);
+  } else {
+    const int group = waves <= SPREAD ? 1 : 4;
+    hipLaunchKernelGGL((k_recurrent_step<TI, D, KIND, 32>), grid_of(a, (a.HV * (D / 32) + group - 1) / group),
+                       dim3(64 * group), group == 1 ? 0 : STEP_LDS, s, a);
+  }
+  return (int)hipGetLastError();
+}
+
 // The kernel by the longest sequence and the number of sequences with tokens, as the host knows them.
 // A run's workgroup pays for whole blocks of 16 tokens and is alone on its CU (D = 128, NB = 4), so with
 // more workgroups than CUs it gains later (us step / run, 48 heads, 128 wide, bf16: 1 sequence of 4
@@ -544,17 +574,10 @@ template <typename TI, int D>
 static int recurrent_t(const RecurrentArgs& a, hipStream_t s) {
   constexpr int CUS = 256;
   const int64_t run_groups = (int64_t)a.live * a.HV * (D / 64);
-  const dim3 step = grid_of(a, (a.HV * (D / 32) + 3) / 4);
-  if (a.slot_tok) {
-    hipLaunchKernelGGL((k_recurrent_step<TI, D, KEEP_EACH>), step, dim3(256), STEP_LDS, s, a);
-  } else if (!a.cu) {
-    hipLaunchKernelGGL((k_recurrent_step<TI, D, ONE_TOKEN>), step, dim3(256), STEP_LDS, s, a);
-  } else if (a.longest <= (run_groups <= CUS ? 6 : 12)) {
-    hipLaunchKernelGGL((k_recurrent_step<TI, D, RUN_OF_TOKENS>), step, dim3(256), STEP_LDS, s, a);
-  } else {
-    return 2 * run_groups <= CUS ? run_t<TI, D, 2>(a, s) : run_t<TI, D, 4>(a, s);
-  }
-  return (int)hipGetLastError();
+  if (a.slot_tok) return step_t<TI, D, KEEP_EACH>(a, s);
+  if (!a.cu) return step_t<TI, D, ONE_TOKEN>(a, s);
+  if (a.longest <= (run_groups <= CUS ? 6 : 12)) return step_t<TI, D, RUN_OF_TOKENS>(a, s);
+  return 2 * run_groups <= CUS ? run_t<TI, D, 2>(a, s) : run_t<TI, D, 4>(a, s);
 }
 
 int launch_recurrent(const RecurrentArgs& a, int dtype, void* stream) {

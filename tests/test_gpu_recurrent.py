@@ -106,6 +106,17 @@ def test_recurrent(name, l2norm):
     check("states", states, st_ref, K)
 
 
+@pytest.mark.parametrize("keep", [True, False], ids=["keep", "last"])
+@pytest.mark.parametrize("N", [1, 3, 8], ids=["16_columns", "one_wave_groups", "four_wave_groups"])
+@pytest.mark.parametrize("d,dtype", [(128, torch.bfloat16), (64, torch.float32)], ids=["bf16_128", "f32_64"])
+def test_few_tokens_by_the_number_of_waves(d, dtype, N, keep):
+    s = make([3, 0, 2, 4, 1, 3, 2, 4, 2][:N + (N > 1)], H=16, HV=48 * (128 // d), d=d, dtype=dtype, keep=keep, fresh=(0,))
+    o, states = run(s)
+    o_ref, st_ref = reference(s)
+    check("o", o, o_ref, K)
+    check("states", states, st_ref, K)
+
+
 # runs go 16 tokens at a time, 64 a turn: lengths at and beside both, and sequences that end in a block
 RUNS = {
     "bf16_128": dict(lengths=[16, 17, 15, 64, 65, 63, 129, 1, 0, 128], H=2, HV=4, d=128, fresh=(3, 8)),
