@@ -244,42 +244,55 @@ __attribute__((amdgpu_waves_per_eu(KIND == ONE_TOKEN ? 3 : 1, KIND == ONE_TOKEN 
 // in each of its first NB waves, and takes NB blocks a turn. What does not depend on S (Gram products,
 // decays, the inverse T of I + L by forward substitution) the other NB waves prepare in LDS a turn
 // ahead, a block each. With NB = 2 every wave has a SIMD to itself, and neither half waits for the
-// other's matrix instructions; with NB = 4 half as much is prepared for the same columns. Lane (g, n) = (lane / 16, lane % 16) holds rows g D/4 .. of
-// column n of S; with the rows in the order (i, r) -> g D/4 + 4 r + i the same registers are the
-// products' B operand and the update's accumulators. A product sums over the key rows in any order, so
-// the K and Q rows lie in LDS in the order that makes their A operands whole 16-byte reads.
+// other's matrix instructions; with NB = 4 half as much is prepared for the same columns. Lane (g, n) =
+// (lane / 16, lane % 16) holds rows g D/4 .. of column n of S; with the rows in the order (i, r) ->
+// g D/4 + 4 r + i the same registers are the products' B operand and the update's accumulators. A
+// product sums over the key rows in any order, so the K and Q rows lie in LDS in the order that makes
+// their A operands whole 16-byte reads.
 // What bounds it is the matrix unit, and the products' latency one after the other: 104 (D = 128) or 56
-// (64) instructions of 32 cycles a block and wave, of about 2,300 cycles that a block takes at D = 64
-// (700 tokens, f32: 50 us with 8 heads and 5 sequences, 72 ns a token; with nothing left to prepare
-// 49 us; token by token in the step kernel 680 ns a token).
-template <typename TI, int D, int NB>
+// (64) instructions of 32 cycles a block and wave. So with CUs to spare and long runs a workgroup takes
+// 16 columns, two waves with half of the rows (r) of each (KS = 2) and four that prepare; the halves add
+// up K S through LDS while they multiply Q S, and the second's share of the outputs goes to the first.
+// 700 tokens, f32, 64 wide, 8 heads and 5 sequences: 43 us, 62 ns a token; with KS = 1 50 us (49 with
+// nothing left to prepare); token by token in the step kernel 680 ns a token.
+template <typename TI, int D, int NB, int KS>
 __global__ __launch_bounds__(128 * NB, 2) void k_recurrent_run(RecurrentArgs a) {
   constexpr int C = 16, DG = D / 4, R = D / 16; // tokens a block, rows a lane, tiles
-  constexpr int LD = D + 4, LT = 20;            // LDS row strides
+  constexpr int RH = R / KS, VW = RH < 4 ? RH : 4; // tiles of a wave, floats of an operand read
+  constexpr int COLS = KS == 1 ? 16 * NB : 16;     // columns of a workgroup
+  constexpr int LD = D + 4, LT = 20;               // LDS row strides
   typedef typename Vec<TI, 8>::type vec8;
   struct alignas(16) Prep { // of one block
     float k[C][LD], q[C][LD]; // rows, permuted
     float t[C][LT], p[C][LT]; // T diag(beta), P
     float gk[C], gq[C], w[C], g_last[C]; // G rk, G rq, D_15,j rk_j, G_15
   };
+  typedef float opnd __attribute__((ext_vector_type(VW)));
   extern __shared__ __attribute__((aligned(16))) float lds[];
   Prep* prep = reinterpret_cast<Prep*>(lds); // of two turns
+  struct Exchange { // KS = 2
+    f32x4 ks[2][2][64], o[2][64]; // of even and odd blocks: each half's K S, the second half's outputs
+  };
+  Exchange* xch = reinterpret_cast<Exchange*>(prep + 2 * NB);
+  int* done = reinterpret_cast<int*>(&prep[0].t[0][C]); // blocks that each half has exchanged (in padding)
   const int lane = threadIdx.x & 63, g = lane >> 4, n16 = lane & 15;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wv = wave & (NB - 1);
-  const bool prepares = wave >= NB;
-  const int h = blockIdx.x / (D / (16 * NB)), j = (int)(((uint64_t)h * a.g_mul) >> 32);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // KS = 2: waves 0 and 1 hold the halves, 2, 3, 6 and 7 prepare, 4 and 5 would share the halves' SIMDs
+  const bool prepares = KS == 1 ? wave >= NB : (wave & 2) != 0, idle = KS == 2 && (wave & 6) == 4;
+  const int wv = KS == 1 ? wave & (NB - 1) : (wave >> 2) * 2 + (wave & 1), kh = KS == 1 ? 0 : wave & 1;
+  const int h = blockIdx.x / (D / COLS), j = (int)(((uint64_t)h * a.g_mul) >> 32);
   const int n = blockIdx.z * MAX_GRID_Y + blockIdx.y;
   if (n >= a.N) return;
-  const int col = h * D + (blockIdx.x % (D / (16 * NB))) * (16 * NB) + wv * 16 + n16; // in a row of v and o
+  const int col = h * D + (blockIdx.x % (D / COLS)) * COLS + (KS == 1 ? wv * 16 : 0) + n16; // in a row of v and o
   const int os = a.HV * D;
   const SeqSpan sp = seq_span(a.cu, a.slot_in, a.slot_out, n, a.T, a.n_slots);
   if (!sp.ok) {
-    for (int t = sp.t0 + g; t < sp.t1 && !prepares; t += 4) ((TI*)a.o)[(int64_t)t * os + col] = (TI)__builtin_nanf("");
+    for (int t = sp.t0 + g; t < sp.t1 && !prepares && !idle && kh == 0; t += 4) ((TI*)a.o)[(int64_t)t * os + col] = (TI)__builtin_nanf("");
     return;
   }
   const int64_t hd = (int64_t)a.HV * D * D, head = (int64_t)h * D * D;
-  const int at = g * DG * D + (col - h * D);
-  f32x4 S[R];
+  const int at = (g * DG + 4 * kh * RH) * D + (col - h * D);
+  f32x4 S[RH];
   // the block at t: lane (g, i) loads token i's rows g D/4 .. of k and q
   struct Rows {
     vec8 k[DG / 8], q[DG / 8];
@@ -351,7 +364,7 @@ __global__ __launch_bounds__(128 * NB, 2) void k_recurrent_run(RecurrentArgs a) 
     // What follows hides the loads: run 700 above 55 us instead of 58 with NB = 2 and consumers that
     // only wait. With NB = 4 the rest is the longer half, and they cost it 3% (12 sequences of 300
     // tokens, 48 heads, 128 wide: 151 us, 146 with the loads at the end).
-    if constexpr (NB == 2) load(r, t + NB * C);
+    if constexpr (NB == 2 || KS == 2) load(r, t + NB * C);
     const float rk = a.l2norm ? inv_sqrt(all_groups(kk) + 1e-6f) : 1.f;
     const float rq = a.l2norm ? inv_sqrt(all_groups(qq) + 1e-6f) : 1.f;
     // running products: G of token n16, and D_ij of this lane's column j = n16
@@ -398,20 +411,47 @@ __global__ __launch_bounds__(128 * NB, 2) void k_recurrent_run(RecurrentArgs a) 
 #pragma unroll
     for (int i = 0; i < C; ++i)
       if ((i >> 2) == g) b.t[i][n16] = T[i] * be;
-    if constexpr (NB > 2) load(r, t + NB * C);
+    if constexpr (NB > 2 && KS == 1) load(r, t + NB * C);
   };
   // The operands of the products with S, read while the block before is finished: the waits for LDS
   // would otherwise stand between the products.
-  f32x4 ka[4][R / 4], qa[4][R / 4];
+  opnd ka[4][RH / VW], qa[4][RH / VW];
   const auto operands = [&](const Prep& b) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int x = 0; x < R / 4; ++x) {
-        ka[i][x] = *reinterpret_cast<const f32x4*>(&b.k[n16][g * DG + i * R + 4 * x]);
-        qa[i][x] = *reinterpret_cast<const f32x4*>(&b.q[n16][g * DG + i * R + 4 * x]);
+      for (int x = 0; x < RH / VW; ++x) {
+        ka[i][x] = *reinterpret_cast<const opnd*>(&b.k[n16][g * DG + i * R + kh * RH + VW * x]);
+        qa[i][x] = *reinterpret_cast<const opnd*>(&b.q[n16][g * DG + i * R + kh * RH + VW * x]);
       }
   };
+  const auto store_o = [&](const f32x4& x4, int t) {
+    const __amdgpu_buffer_rsrc_t to = rows_at((const TI*)a.o, t, os);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int off = lane_o + s * os * (int)sizeof(TI);
+      const TI x = (TI)x4[s];
+      if constexpr (sizeof(TI) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(short, x), to, off, 0, 0);
+      else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(int, x), to, off, 0, 0);
+    }
+  };
+  // The halves' exchange: a half writes its part, then counts the block; the other reads the count, then
+  // the part. Parts of even and odd blocks have places of their own: one is written again two blocks
+  // later, and by then the other half has counted a block after reading it. Both halves go through the
+  // same blocks, so the wait ends.
+  const auto lds_order = [] { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup", "local"); };
+  const auto others_count = [&] {
+    return __builtin_amdgcn_readfirstlane(__hip_atomic_load(done + 1 - kh, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP));
+  };
+  const auto count = [&](int blocks) {
+    lds_order();
+    __hip_atomic_store(done + kh, blocks, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+  };
+  const auto wait_for = [&](int blocks) {
+    while (others_count() < blocks) {}
+    lds_order();
+  };
+  f32x4 o; // KS = 2: between the blocks, the first half's part of the outputs of the one before
   // block i of the sequence, at token t
   const auto block = [&](int i, const float v[4], int t) {
     const Prep& b = prep[i % (2 * NB)];
@@ -420,28 +460,70 @@ __global__ __launch_bounds__(128 * NB, 2) void k_recurrent_run(RecurrentArgs a) 
     const f32x4 ta = *reinterpret_cast<const f32x4*>(&b.t[n16][4 * g]), pa = *reinterpret_cast<const f32x4*>(&b.p[n16][4 * g]);
     const float last = b.g_last[0];
     // the update's: lane (g, 4 y + i): rows y D/4 + 4 r + i of token 4 g + s
-    f32x4 ua[4][R / 4];
+    opnd ua[4][RH / VW];
 #pragma unroll
     for (int s = 0; s < 4; ++s)
 #pragma unroll
-      for (int x = 0; x < R / 4; ++x)
-        ua[s][x] = *reinterpret_cast<const f32x4*>(&b.k[4 * g + s][(n16 >> 2) * DG + (n16 & 3) * R + 4 * x]);
+      for (int x = 0; x < RH / VW; ++x)
+        ua[s][x] = *reinterpret_cast<const opnd*>(&b.k[4 * g + s][(n16 >> 2) * DG + (n16 & 3) * R + kh * RH + VW * x]);
     __builtin_amdgcn_sched_barrier(0);
-    f32x4 ks = zero4(), qs = zero4();
+    f32x4 ks = zero4(), qs = zero4(), other;
+    int seen = 0;
+    if constexpr (KS == 1) {
 #pragma unroll
-    for (int y = 0; y < 4; ++y)
+      for (int y = 0; y < 4; ++y)
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        ks = mfma1(ka[y][r / 4][r % 4], S[r][y], ks);
-        qs = mfma1(qa[y][r / 4][r % 4], S[r][y], qs);
-      }
+        for (int r = 0; r < RH; ++r) {
+          ks = mfma1(ka[y][r / VW][r % VW], S[r][y], ks);
+          qs = mfma1(qa[y][r / VW][r % VW], S[r][y], qs);
+        }
+    } else {
+      f32x4 ks2 = zero4(), qs2 = zero4();
+#pragma unroll
+      for (int y = 0; y < 4; y += 2)
+#pragma unroll
+        for (int r = 0; r < RH; ++r) {
+          ks = mfma1(ka[y][0][r], S[r][y], ks);
+          ks2 = mfma1(ka[y + 1][0][r], S[r][y + 1], ks2);
+        }
+      __builtin_amdgcn_sched_barrier(0);
+      const auto q_part = [&](int y) {
+#pragma unroll
+        for (int r = 0; r < RH; ++r) {
+          f32x4& to = r & 1 ? qs2 : qs;
+          to = mfma1(qa[y][0][r], S[r][y], to);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      q_part(0);
+      ks += ks2;
+      xch->ks[i & 1][kh][lane] = ks;
+      count(i + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      q_part(1);
+      q_part(2);
+      seen = others_count();
+      lds_order();
+      other = xch->ks[i & 1][1 - kh][lane];
+      __builtin_amdgcn_sched_barrier(0);
+      q_part(3);
+      qs += qs2;
+    }
     __builtin_amdgcn_sched_barrier(0);
     if (t + C < sp.t1) {
       if (i % NB == NB - 1) __syncthreads(); // the next turn is ready; of this one everything is in registers
-      operands(prep[(i + 1) % (2 * NB)]);
+      if constexpr (KS == 1) operands(prep[(i + 1) % (2 * NB)]);
     }
     __builtin_amdgcn_sched_barrier(0);
-    f32x4 rhs, u = zero4(), u2 = zero4(), o;
+    if constexpr (KS == 2) {
+      if (seen <= i) {
+        wait_for(i + 1);
+        other = xch->ks[i & 1][1 - kh][lane];
+      }
+      ks += other;
+      if (kh == 0 && i > 0) store_o(o + xch->o[(i - 1) & 1][lane], t - C);
+    }
+    f32x4 rhs, u = zero4(), u2 = zero4();
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       rhs[s] = __builtin_fmaf(-gk[s], ks[s], v[s]);
@@ -451,26 +533,27 @@ __global__ __launch_bounds__(128 * NB, 2) void k_recurrent_run(RecurrentArgs a) 
     u2 = mfma1(ta[1], rhs[1], u2);
     u = mfma1(ta[2], rhs[2], u);
     u2 = mfma1(ta[3], rhs[3], u2);
+    if constexpr (KS == 2) operands(prep[(i + 1) % (2 * NB)]); // of no use after the last block
 #pragma unroll
-    for (int r = 0; r < R; ++r) S[r] *= last;
+    for (int r = 0; r < RH; ++r) S[r] *= last;
     u += u2;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const float wu = w[s] * u[s]; // of token 4 g + s
 #pragma unroll
-      for (int r = 0; r < R; ++r) S[r] = mfma1(ua[s][r / 4][r % 4], wu, S[r]);
+      for (int r = 0; r < RH; ++r) S[r] = mfma1(ua[s][r / VW][r % VW], wu, S[r]);
     }
+    if (KS == 1 || kh == 1) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s) o = mfma1(pa[s], u[s], o);
-    const __amdgpu_buffer_rsrc_t to = rows_at((const TI*)a.o, t, os);
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int off = lane_o + s * os * (int)sizeof(TI);
-      const TI x = (TI)o[s];
-      if constexpr (sizeof(TI) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(short, x), to, off, 0, 0);
-      else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(int, x), to, off, 0, 0);
+      for (int s = 0; s < 4; ++s) o = mfma1(pa[s], u[s], o);
     }
+    if constexpr (KS == 1) store_o(o, t);
+    else if (kh == 1) xch->o[i & 1][lane] = o;
   };
+  if (idle) {
+    for (int t = sp.t0; t < sp.t1; t += NB * C) __syncthreads();
+    return;
+  }
   if (prepares) {
     if (sp.t0 >= sp.t1) return;
     Rows r;
@@ -485,13 +568,14 @@ __global__ __launch_bounds__(128 * NB, 2) void k_recurrent_run(RecurrentArgs a) 
   {
     const float* p = a.states + (sp.in < 0 ? 0 : sp.in) * hd + head + at;
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int r = 0; r < RH; ++r)
 #pragma unroll
       for (int i = 0; i < 4; ++i) S[r][i] = keepf(p[(4 * r + i) * D], sp.in >= 0);
   }
   if (sp.t0 < sp.t1) {
     float v0[4], v1[4];
     load_v(v0, sp.t0);
+    if constexpr (KS == 2) done[kh] = 0; // seen by the other half after the barrier
     __syncthreads(); // the first turn is ready
     operands(prep[0]);
     int i = 0;
@@ -503,39 +587,51 @@ __global__ __launch_bounds__(128 * NB, 2) void k_recurrent_run(RecurrentArgs a) 
       load_v(v0, t + 2 * C);
       block(i + 1, v1, t + C);
     }
+    if constexpr (KS == 2) {
+      const int blocks = (sp.t1 - sp.t0 + C - 1) / C;
+      if (kh == 1) {
+        count(blocks + 1);
+      } else {
+        wait_for(blocks + 1);
+        store_o(o + xch->o[(blocks - 1) & 1][lane], sp.t0 + (blocks - 1) * C);
+      }
+    }
   }
   if (sp.out >= 0) {
     float* p = a.states + sp.out * hd + head + at;
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int r = 0; r < RH; ++r)
 #pragma unroll
       for (int i = 0; i < 4; ++i) p[(4 * r + i) * D] = S[r][i];
   }
 }
-// LDS of a workgroup: the rows, T, P and factors of two turns of NB blocks
-constexpr unsigned run_lds(int D, int NB) { return 2 * NB * 4 * (2 * 16 * (D + 4) + 2 * 16 * 20 + 4 * 16); }
+// LDS of a workgroup: the rows, T, P and factors of two turns of NB blocks, and what the halves exchange
+// (D = 128, KS = 2: all of the 160 KiB)
+constexpr unsigned run_lds(int D, int NB, int KS) {
+  return 2 * NB * 4 * (2 * 16 * (D + 4) + 2 * 16 * 20 + 4 * 16) + (KS == 2 ? 6 * 1024 : 0);
+}
 
 static dim3 grid_of(const RecurrentArgs& a, int x) {
   const unsigned n = (unsigned)a.N;
   return dim3((unsigned)x, n < MAX_GRID_Y ? n : MAX_GRID_Y, (n + MAX_GRID_Y - 1) / MAX_GRID_Y);
 }
 
-template <typename TI, int D, int NB>
+template <typename TI, int D, int NB, int KS>
 static int run_t(const RecurrentArgs& a, hipStream_t s) {
-  constexpr unsigned lds = run_lds(D, NB);
+  constexpr unsigned lds = run_lds(D, NB, KS);
   if constexpr (lds > 64 * 1024) { // more than the runtime gives unasked: asked for once on each device
     static std::atomic<uint64_t> asked{0};
     int dev = 0;
     if (const hipError_t e = hipGetDevice(&dev)) return (int)e;
     const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
     if (!(asked.load(std::memory_order_relaxed) & bit)) {
-      const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_recurrent_run<TI, D, NB>),
+      const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_recurrent_run<TI, D, NB, KS>),
                                                hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
       if (e != hipSuccess) return (int)e;
       asked.fetch_or(bit, std::memory_order_relaxed);
     }
   }
-  hipLaunchKernelGGL((k_recurrent_run<TI, D, NB>), grid_of(a, a.HV * (D / (16 * NB))), dim3(128 * NB), lds, s, a);
+  hipLaunchKernelGGL((k_recurrent_run<TI, D, NB, KS>), grid_of(a, a.HV * (KS == 1 ? D / (16 * NB) : D / 16)), dim3(128 * NB), lds, s, a);
   return (int)hipGetLastError();
 }
 
@@ -569,6 +665,9 @@ static int step_t(const RecurrentArgs& a, hipStream_t s) {
 // 16 89 / 83, of 64 278 / 158; 64 wide, f32, 4 sequences of 8 tokens 8.9 / 6.5, 64 of 16 58 / 61, of 24
 // 79 / 75). 32 columns a workgroup while each then has a CU, 64 beyond (us with 32 / 64, 48 heads, 256
 // tokens, 128 wide, bf16: 1 sequence 35 / 43, 2 61 / 47; 64 wide, f32: 2 sequences 23 / 27, 3 37 / 29).
+// Two waves a column while each 16 columns have a CU and the run is long enough to pay for the start (us
+// with two / one, 8 heads, 1 sequence, 128 wide, bf16: 64 tokens 12.9 / 12.9, 256 27 / 34; 64 wide, f32:
+// 16 tokens 6.3 / 5.9, 64 9.8 / 9.6, 256 19 / 22).
 // With slot_tok every token's state is wanted: always the step.
 template <typename TI, int D>
 static int recurrent_t(const RecurrentArgs& a, hipStream_t s) {
@@ -577,7 +676,8 @@ static int recurrent_t(const RecurrentArgs& a, hipStream_t s) {
   if (a.slot_tok) return step_t<TI, D, KEEP_EACH>(a, s);
   if (!a.cu) return step_t<TI, D, ONE_TOKEN>(a, s);
   if (a.longest <= (run_groups <= CUS ? 6 : 12)) return step_t<TI, D, RUN_OF_TOKENS>(a, s);
-  return 2 * run_groups <= CUS ? run_t<TI, D, 2>(a, s) : run_t<TI, D, 4>(a, s);
+  if (4 * run_groups <= CUS && a.longest > 64) return run_t<TI, D, 4, 2>(a, s);
+  return 2 * run_groups <= CUS ? run_t<TI, D, 2, 1>(a, s) : run_t<TI, D, 4, 1>(a, s);
 }
 
 int launch_recurrent(const RecurrentArgs& a, int dtype, void* stream) {

@@ -162,6 +162,23 @@ def test_runs_of_many_columns(dtype, d):
     check("states", states, st_ref, K)
 
 
+@pytest.mark.parametrize("l2norm", [True, False], ids=["l2norm", "given"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_long_runs_of_few_columns(dtype, d, l2norm):
+    """Two waves share a column: odd and even numbers of blocks and turns, short sequences beside long."""
+    s = make([65, 16, 0, 33, 128, 1, 112, 200, 17], H=1, HV=2, d=d, dtype=dtype, fresh=(0, 4), packed=d == 64)
+    if not l2norm:
+        s["q"].copy_((s["q"].float() * d ** -0.5).to(dtype))
+        s["k"].copy_((s["k"].float() * d ** -0.5).to(dtype))
+    o, states = run(s, l2norm)
+    again = run(s, l2norm)
+    assert torch.equal(o, again[0]) and torch.equal(states, again[1])
+    o_ref, st_ref = reference(s, l2norm)
+    check("o", o, o_ref, K)
+    check("states", states, st_ref, K)
+
+
 @pytest.mark.parametrize("HV", [2, 48])
 def test_runs_in_a_graph(HV):
     s = make([40, 70, 5], H=2, HV=HV, d=128)
