@@ -355,7 +355,7 @@ __global__ __launch_bounds__(256) void k_rope_bwd(RopeArgs a) {
 }
 
 // dq_weight and dk_weight: the workgroups' partial sums, added in a fixed order: 8 columns a
-// workgroup, 128 slices of the rows each, then the slices.
+// workgroup, 128 slices of the rows each, then the slices, 8 by 8 and the 16 sums of those.
 __global__ __launch_bounds__(1024) void k_rope_reduce(RopeArgs a) {
   __shared__ float red[128][9];
   const int c = threadIdx.x & 7, s = threadIdx.x >> 3, side = blockIdx.x * 8 >= a.D;
@@ -368,10 +368,18 @@ __global__ __launch_bounds__(1024) void k_rope_reduce(RopeArgs a) {
   for (int b = b0 + s; b < b1; b += 128) x += a.part[(size_t)b * a.D + col];
   red[s][c] = x;
   __syncthreads();
+  if (s < 16) {
+    x = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x += red[8 * s + i][c];
+  }
+  __syncthreads();
+  if (s < 16) red[s][c] = x;
+  __syncthreads();
   if (s != 0) return;
   x = 0.f;
 #pragma unroll
-  for (int i = 0; i < 128; ++i) x += red[i][c];
+  for (int i = 0; i < 16; ++i) x += red[i][c];
   dw[col] = x;
 }
 
