@@ -584,7 +584,8 @@ class ConvStepProblem:
 def gdn_conv_step(p: ConvStepProblem, x, weight, bias, windows, slot_in, slot_out, slot_tok=None, cu_seqlens=None,
                   outs=None, stream=None):
     """One serving step of the conv front-end on cached windows (slots as in gdn_recurrent). Returns
-    the list of outputs, [T, group_channels[g]]; `windows` is updated in place (None at width 1)."""
+    the list of outputs, [T, group_channels[g]] (of a short call parts of one allocation, as are those
+    of gdn_qk_rope_fwd and _bwd); `windows` is updated in place (None at width 1)."""
     return _call("conv_step", x, stream, p.at, x, weight, bias, windows, slot_in, slot_out, slot_tok, cu_seqlens,
                  None if outs is None else list(outs))
 

@@ -236,6 +236,8 @@ int gdn_conv_bwd(const gdn_conv_problem* p, const void* x, const float* weight, 
  * tokens can be rolled back to any of them. All arithmetic is FP32. Longer sequences (by the host's
  * lengths; without slot_tok) are taken 16 tokens at a time: an infinity or NaN in a row then reaches
  * the outputs of its sequence's block of 16 tokens, not only the later ones.
+ * The order of the sums follows from the call's sizes, so the same call gives the same bits, and a
+ * sequence in calls of different sizes may differ by rounding.
  *
  *   q, k      [T, H, d], v [T, HV, d]  io dtype; a token's heads are contiguous, tokens are
  *                                      q_stride, k_stride, v_stride elements apart
