@@ -1095,10 +1095,8 @@ int gdn_recurrent(const gdn_recurrent_problem* p, const void* q, const void* k, 
   CHECK(check_step_arrays(p->cu_seqlens_host, cu_seqlens, slot_in, slot_out, slot_tok));
   a.T = (int)T;
   a.N = p->n_seqs;
-  a.H = p->h_qk;
   a.HV = p->h_v;
-  a.G = p->h_v / p->h_qk;
-  a.g_mul = ((uint64_t)1 << 32) / a.G + 1;
+  a.g_mul = ((uint64_t)1 << 32) / (p->h_v / p->h_qk) + 1;
   a.D = p->d;
   a.l2norm = p->l2norm_qk ? 1 : 0;
   a.n_slots = p->n_slots;
@@ -1110,6 +1108,16 @@ int gdn_recurrent(const gdn_recurrent_problem* p, const void* q, const void* k, 
       const int len = p->cu_seqlens_host[n + 1] - p->cu_seqlens_host[n];
       a.longest = std::max(a.longest, len);
       a.live += len > 0;
+    }
+    if (p->n_seqs <= 16) {
+      int by_length[16];
+      for (int n = 0; n < p->n_seqs; ++n) by_length[n] = n;
+      const int32_t* c = p->cu_seqlens_host;
+      std::sort(by_length, by_length + p->n_seqs, [&](int x, int y) {
+        const int lx = c[x + 1] - c[x], ly = c[y + 1] - c[y];
+        return lx != ly ? lx > ly : x < y;
+      });
+      for (int n = 0; n < p->n_seqs; ++n) a.order |= (uint64_t)by_length[n] << (4 * n);
     }
   }
   a.q = q;

@@ -187,7 +187,8 @@ int launch_conv_step(const ConvStepArgs& a, int dtype, void* stream);
 struct RecurrentArgs {
   int64_t qs, ks, vs; // elements between the tokens of q, k, v
   uint64_t g_mul;     // 2^32 / G rounded up: h / G = h g_mul >> 32 for h, G <= 65536
-  int T, N, H, HV, G, D, l2norm, n_slots;
+  uint64_t order;     // up to 16 sequences, longest first by the host's lengths, 4 bits each
+  int T, N, HV, D, l2norm, n_slots;
   int longest, live; // by the host's lengths: the longest sequence, and how many have tokens
   const void* q;
   const void* k;

@@ -281,8 +281,11 @@ __global__ __launch_bounds__(128 * NB, 2) void k_recurrent_run(RecurrentArgs a) 
   const bool prepares = KS == 1 ? wave >= NB : (wave & 2) != 0, idle = KS == 2 && (wave & 6) == 4;
   const int wv = KS == 1 ? wave & (NB - 1) : (wave >> 2) * 2 + (wave & 1), kh = KS == 1 ? 0 : wave & 1;
   const int h = blockIdx.x / (D / COLS), j = (int)(((uint64_t)h * a.g_mul) >> 32);
-  const int n = blockIdx.z * MAX_GRID_Y + blockIdx.y;
+  int n = blockIdx.z * MAX_GRID_Y + blockIdx.y;
   if (n >= a.N) return;
+  // the longest sequences first: where the workgroups outnumber the CUs, one of those would end last (12
+  // sequences of up to 300 tokens, 48 heads, 128 wide, bf16: 138 us, 146 as they come)
+  if (a.N <= 16) n = (int)(a.order >> (4 * n)) & 15;
   const int col = h * D + (blockIdx.x % (D / COLS)) * COLS + (KS == 1 ? wv * 16 : 0) + n16; // in a row of v and o
   const int os = a.HV * D;
   const SeqSpan sp = seq_span(a.cu, a.slot_in, a.slot_out, n, a.T, a.n_slots);
@@ -361,9 +364,8 @@ __global__ __launch_bounds__(128 * NB, 2) void k_recurrent_run(RecurrentArgs a) 
             f32x4{qf[4 * x + i], qf[4 * x + 4 + i], qf[4 * x + 8 + i], qf[4 * x + 12 + i]};
       }
     const float al = live ? __expf(r.g) : 1.f, be = live ? r.beta : 0.f;
-    // What follows hides the loads: run 700 above 55 us instead of 58 with NB = 2 and consumers that
-    // only wait. With NB = 4 the rest is the longer half, and they cost it 3% (12 sequences of 300
-    // tokens, 48 heads, 128 wide: 151 us, 146 with the loads at the end).
+    // What follows hides the loads. With 64 columns a workgroup the other half is the longer one, and
+    // they cost it 3% here (12 sequences of 300 tokens, 48 heads, 128 wide), so they come last.
     if constexpr (NB == 2 || KS == 2) load(r, t + NB * C);
     const float rk = a.l2norm ? inv_sqrt(all_groups(kk) + 1e-6f) : 1.f;
     const float rq = a.l2norm ? inv_sqrt(all_groups(qq) + 1e-6f) : 1.f;
@@ -659,12 +661,13 @@ static int step_t(const RecurrentArgs& a, hipStream_t s) {
 }
 
 // The kernel by the longest sequence and the number of sequences with tokens, as the host knows them.
-// A run's workgroup pays for whole blocks of 16 tokens and is alone on its CU (D = 128, NB = 4), so with
-// more workgroups than CUs it gains later (us step / run, 48 heads, 128 wide, bf16: 1 sequence of 4
-// tokens 7.7 / 8.3, of 8 12.2 / 8.2, of 64 64 / 14; 32 sequences of 8 tokens 56 / 82, of 12 73 / 81, of
-// 16 89 / 83, of 64 278 / 158; 64 wide, f32, 4 sequences of 8 tokens 8.9 / 6.5, 64 of 16 58 / 61, of 24
-// 79 / 75). 32 columns a workgroup while each then has a CU, 64 beyond (us with 32 / 64, 48 heads, 256
-// tokens, 128 wide, bf16: 1 sequence 35 / 43, 2 61 / 47; 64 wide, f32: 2 sequences 23 / 27, 3 37 / 29).
+// A run's workgroup pays for whole blocks of 16 tokens and for the start of its two halves, so it gains
+// from 7 tokens on, and with more workgroups than CUs later (us step / run, 48 heads, 128 wide, bf16: 1
+// sequence of 4 tokens 6.2 / 7.6, of 8 9.0 / 7.8, of 24 20 / 9.6; 32 sequences of 8 tokens 57 / 84, of 12
+// 71 / 84, of 16 86 / 85, of 24 118 / 112; 64 wide, f32, 4 sequences of 6 tokens 6.3 / 6.5, of 8 7.3 /
+// 6.5, 16 of 12 17 / 19, of 16 21 / 19). 32 columns a workgroup while each then has a CU, 64 beyond (us
+// with 32 / 64, 48 heads, 256 tokens, 128 wide, bf16: 1 sequence 35 / 43, 2 61 / 47; 64 wide, f32: 2
+// sequences 23 / 27, 3 37 / 29).
 // Two waves a column while each 16 columns have a CU and the run is long enough to pay for the start (us
 // with two / one, 8 heads, 1 sequence, 128 wide, bf16: 64 tokens 12.9 / 12.9, 256 27 / 34; 64 wide, f32:
 // 16 tokens 6.3 / 5.9, 64 9.8 / 9.6, 256 19 / 22).
