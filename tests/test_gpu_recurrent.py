@@ -179,6 +179,16 @@ def test_long_runs_of_few_columns(dtype, d, l2norm):
     check("states", states, st_ref, K)
 
 
+@pytest.mark.parametrize("N", [15, 16, 17])
+def test_sequences_of_any_length_in_any_order(N):
+    """Up to 16 sequences run longest first: each still gets its own rows and slots."""
+    s = make([(7 * n * n) % 41 for n in range(N)], 1, 2, 64, fresh=(3, N - 1))
+    o, states = run(s)
+    o_ref, st_ref = reference(s)
+    check("o", o, o_ref, K)
+    check("states", states, st_ref, K)
+
+
 @pytest.mark.parametrize("HV", [2, 48])
 def test_runs_in_a_graph(HV):
     s = make([40, 70, 5], H=2, HV=HV, d=128)
