@@ -640,10 +640,11 @@ static int run_t(const RecurrentArgs& a, hipStream_t s) {
 // The step kernel, its columns a wave and waves a workgroup by the number of waves of 32 columns. With
 // few, a wave to a workgroup spreads them over more CUs, so that their stores do not queue at one (us
 // in workgroups of 4 / 1, 128 wide, bf16: one token 192 waves 4.3 / 3.7, 768 5.4 / 5.2, 1152 8.0 / 6.8,
-// 3072 19.0 / 21.1; 6 kept tokens 192 waves 12.4 / 10.1, 768 15.8 / 15.8, 1152 27 / 25, 3072 67 / 72).
-// With fewer still, and several tokens, 16 columns (us with 32 / 16: 6 kept tokens, one wave a
-// workgroup, 64 waves 9.7 / 8.1, 192 10.1 / 9.6, 384 11.6 / 11.8, 576 13.6 / 16.1; 5 tokens, four waves a
-// workgroup, 64 waves 8.0 / 6.3, 384 9.4 / 7.2, 576 9.8 / 9.4, 1152 15 / 16).
+// 16 sequences of 48 heads 19.0 / 21.1; 6 kept tokens 192 waves 12.4 / 10.1, 768 15.8 / 15.8, 1152 27 /
+// 25, 16 sequences of 48 heads 67 / 72). With fewer still, and several tokens, 16 columns (us with 32 /
+// 16: 6 kept tokens, one wave a workgroup, 64 waves 9.7 / 8.1, 192 10.1 / 9.6, 384 11.6 / 11.8, 576 13.6
+// / 16.1; 5 tokens, four waves a workgroup, 64 waves 8.0 / 6.3, 384 9.4 / 7.2, 576 9.8 / 9.4, 1152 15 /
+// 16).
 template <typename TI, int D, StepKind KIND>
 static int step_t(const RecurrentArgs& a, hipStream_t s) {
   constexpr int64_t SPREAD = 1280, HALVED = 384;
