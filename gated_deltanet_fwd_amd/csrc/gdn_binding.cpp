@@ -10,6 +10,7 @@
 #include <c10/core/Storage.h>
 #include <c10/core/TensorImpl.h>
 #include <c10/hip/HIPStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdarg>
@@ -163,16 +164,15 @@ P problem(PyObject* address) {
   return *(const P*)at;
 }
 
-// Runs f with C++ exceptions turned into Python ones.
+// Runs f with C++ exceptions turned into the Python ones that torch makes of them (an allocation that
+// fails is a torch.OutOfMemoryError, as where the package allocates in Python).
 template <typename F>
 PyObject* guarded(F f) {
   try {
     return f();
   } catch (const Raised&) {
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
   } catch (...) {
-    PyErr_SetString(PyExc_RuntimeError, "unknown C++ exception");
+    torch::translate_exception_to_python(std::current_exception());
   }
   return nullptr;
 }

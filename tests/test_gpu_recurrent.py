@@ -403,3 +403,23 @@ def test_binding_refuses_wrong_tensors():
         G.gdn_recurrent(p, **good, cu_seqlens=s["cu"])
     torch.cuda.synchronize()
     assert torch.equal(before, s["states"])
+
+
+def test_an_allocation_that_fails_is_torchs_own_error():
+    """Servers catch torch.OutOfMemoryError to shrink a batch: an output that does not fit raises it, as
+    it does from the calls that allocate in Python."""
+    T, HV, d = 4096, 32, 128
+    p = G.RecurrentProblem(1, 1, HV, d, 1, cu_seqlens_host=[0, T])
+    s = make([T], 1, HV, d, spare=0)
+    a = (s["q"], s["k"], s["v"], s["g"], s["beta"], s["states"], s["slot_in"], s["slot_out"])
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    total = torch.cuda.get_device_properties(0).total_memory
+    torch.cuda.set_per_process_memory_fraction(torch.cuda.memory_reserved() / total)  # nothing more
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            G.gdn_recurrent(p, *a, cu_seqlens=s["cu"])
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert G.gdn_recurrent(p, *a, cu_seqlens=s["cu"]).shape == (T, HV, d)
+    torch.cuda.synchronize()
