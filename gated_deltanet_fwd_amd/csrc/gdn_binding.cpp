@@ -192,7 +192,6 @@ PyObject* recurrent(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::ScalarType io = io_type(p.dtype);
     const int64_t T = p.n_tokens, N = p.n_seqs;
     const int64_t qs[] = {T, p.h_qk, p.d}, vs[] = {T, p.h_v, p.d}, gs[] = {T, p.h_v}, ss[] = {p.n_slots, p.h_v, p.d, p.d};
-    const Tensor o = a[11] == Py_None ? empty(vs, io, dev) : tensor(a[11], "o");
     void* vp = expect(v, "v", vs, io, dev, &p.v_stride);
     void* qp = expect(tensor(a[1], "q"), "q", qs, io, dev, &p.q_stride);
     void* kp = expect(tensor(a[2], "k"), "k", qs, io, dev, &p.k_stride);
@@ -203,6 +202,7 @@ PyObject* recurrent(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* out = expect(tensor(a[8], "slot_out"), "slot_out", {N}, at::kInt, dev);
     const int32_t* tok = optional<int32_t>(a[9], "slot_tok", {T}, at::kInt, dev);
     const int32_t* cu = optional<int32_t>(a[10], "cu_seqlens", {N + 1}, at::kInt, dev);
+    const Tensor o = a[11] == Py_None ? empty(vs, io, dev) : tensor(a[11], "o");
     void* op = expect(o, "o", vs, io, dev);
     check(g_lib.recurrent(&p, qp, kp, vp, (float*)gp, (float*)bp, cu, (int32_t*)in, (int32_t*)out, tok, (float*)sp, op,
                           stream_of(dev)));
@@ -228,6 +228,8 @@ PyObject* conv_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* out = expect(tensor(a[6], "slot_out"), "slot_out", {N}, at::kInt, dev);
     const int32_t* tok = optional<int32_t>(a[7], "slot_tok", {T}, at::kInt, dev);
     const int32_t* cu = optional<int32_t>(a[8], "cu_seqlens", {N + 1}, at::kInt, dev);
+    for (int i = 0; i < p.n_groups && i < 4; ++i)
+      if (p.group_channels[i] < 0) refuse("group %d has %d channels", i, (int)p.group_channels[i]);
     const bool given = a[9] != Py_None;
     if (given && (!PyList_Check(a[9]) || PyList_GET_SIZE(a[9]) != p.n_groups))
       refuse("outs has to be a list of %d tensors", p.n_groups);
@@ -278,17 +280,15 @@ PyObject* rope_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::ScalarType io = io_type(p.dtype);
     const int64_t qs[] = {p.n_tokens, p.h_q, p.d}, ks[] = {p.n_tokens, p.h_k, p.d};
     void* qp = expect(q, "q", qs, io, dev, &p.q_stride);
+    void* kp = a[2] == Py_None ? nullptr : expect(tensor(a[2], "k"), "k", ks, io, dev, &p.k_stride);
+    const RopeInputs r(p, a + 3, dev);
     Tensor qo, ko;
     Buffers made(dev);
     made.want(qo, a[7], "q_out", qs, io);
     if (a[2] != Py_None) made.want(ko, a[8], "k_out", ks, io);
     made.allocate();
-    void *qop = expect(qo, "q_out", qs, io, dev, &p.qo_stride), *kp = nullptr, *kop = nullptr;
-    if (ko.defined()) {
-      kp = expect(tensor(a[2], "k"), "k", ks, io, dev, &p.k_stride);
-      kop = expect(ko, "k_out", ks, io, dev, &p.ko_stride);
-    }
-    const RopeInputs r(p, a + 3, dev);
+    void* qop = expect(qo, "q_out", qs, io, dev, &p.qo_stride);
+    void* kop = ko.defined() ? expect(ko, "k_out", ks, io, dev, &p.ko_stride) : nullptr;
     check(g_lib.rope_fwd(&p, qp, kp, r.pos, r.freqs, r.wq, r.wk, qop, kop, stream_of(dev)));
     return Py_BuildValue("NN", THPVariable_Wrap(qo), wrap_or_none(ko));
   });

@@ -190,3 +190,10 @@ def test_binding_refuses_wrong_tensors():
         G.gdn_conv_step(p, **good, outs=[s["x"]])
     with pytest.raises(G.GdnError, match="n_groups"):
         G.ConvStepProblem(2, [8] * 5, 4)
+
+
+def test_negative_groups_are_refused_before_anything_is_allocated():
+    s = make([1, 1], [16, 8])
+    p = G.ConvStepProblem(2, [32, -8], s["slots"])
+    with pytest.raises(G.GdnError, match="channels"):
+        G.gdn_conv_step(p, s["x"], s["weight"], s["bias"], s["windows"], s["slot_in"], s["slot_out"])

@@ -423,3 +423,16 @@ def test_an_allocation_that_fails_is_torchs_own_error():
         torch.cuda.set_per_process_memory_fraction(1.0)
     assert G.gdn_recurrent(p, *a, cu_seqlens=s["cu"]).shape == (T, HV, d)
     torch.cuda.synchronize()
+
+
+def test_bad_problems_are_refused_before_anything_is_allocated():
+    """A descriptor that no tensor fits (here a negative width) is a GdnError, not the allocator's."""
+    s = make([1, 1], 2, 4, 64)
+    a = (s["q"], s["k"], s["v"], s["g"], s["beta"], s["states"], s["slot_in"], s["slot_out"])
+    for field, value in (("d", -64), ("h_v", -4), ("n_tokens", -2)):
+        p = G.RecurrentProblem(2, 2, 4, 64, s["slots"])
+        setattr(p.st, field, value)
+        before = torch.cuda.memory_stats()["allocation.all.allocated"]
+        with pytest.raises(G.GdnError):
+            G.gdn_recurrent(p, *a)
+        assert torch.cuda.memory_stats()["allocation.all.allocated"] == before

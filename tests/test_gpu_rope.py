@@ -237,3 +237,10 @@ def test_binding_refuses_wrong_tensors():
                           workspace=torch.zeros(16, dtype=torch.uint8, device=DEV))
     with pytest.raises(G.GdnError, match="needs a norm"):
         G.gdn_qk_rope_fwd(G.QkRopeProblem(4, 2, 2, 64, norm="none"), q, k, pos, f, q_weight=s["wq"])
+
+
+def test_bad_problems_are_refused_before_anything_is_allocated():
+    s = make(4, 2, 1, 64)
+    s["p"].st.h_k = -1
+    with pytest.raises(G.GdnError):
+        G.gdn_qk_rope_fwd(*args(s))
