@@ -316,7 +316,8 @@ PyObject* rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Tensor dq, dk, dwq, dwk, ws;
     Buffers made(dev);
     made.want(dq, a[9], "dq", qs, io);
-    if (dkop) made.want(dk, a[10], "dk", ks, io);
+    const bool with_k = a[8] != Py_None; // (of no tokens the addresses are NULL)
+    if (with_k) made.want(dk, a[10], "dk", ks, io);
     if (r.wq) made.want(dwq, a[11], "dq_weight", {p.d}, at::kFloat);
     if (r.wk) made.want(dwk, a[12], "dk_weight", {p.d}, at::kFloat);
     size_t bytes = 0;
@@ -331,7 +332,7 @@ PyObject* rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     made.allocate();
     void* dqp = expect(dq, "dq", qs, io, dev, &p.dq_stride);
-    void* dkp = dkop ? expect(dk, "dk", ks, io, dev, &p.dk_stride) : nullptr;
+    void* dkp = with_k ? expect(dk, "dk", ks, io, dev, &p.dk_stride) : nullptr;
     float* dwqp = r.wq ? (float*)expect(dwq, "dq_weight", {p.d}, at::kFloat, dev) : nullptr;
     float* dwkp = r.wk ? (float*)expect(dwk, "dk_weight", {p.d}, at::kFloat, dev) : nullptr;
     check(g_lib.rope_bwd(&p, qp, kp, r.pos, r.freqs, r.wq, r.wk, dqop, dkop, dqp, dkp, dwqp, dwkp,

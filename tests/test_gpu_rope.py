@@ -244,3 +244,10 @@ def test_bad_problems_are_refused_before_anything_is_allocated():
     s["p"].st.h_k = -1
     with pytest.raises(G.GdnError):
         G.gdn_qk_rope_fwd(*args(s))
+
+
+def test_no_tokens_give_empty_gradients_of_both():
+    s = make(0, 2, 1, 64)
+    g = G.gdn_qk_rope_bwd(*args(s), s["dyq"], s["dyk"], q_weight=s["wq"], k_weight=s["wk"])
+    assert g["dq"].shape == (0, 2, 64) and g["dk"].shape == (0, 1, 64)
+    assert not g["dq_weight"].any() and not g["dk_weight"].any()
