@@ -1022,11 +1022,17 @@ int gdn_conv_bwd(const gdn_conv_problem* p, const void* x, const float* weight, 
 
 namespace {
 
+// Tokens and sequences of one call: the kernels' 32-bit counters run a little past the last one (the
+// conv step's by two grid rows of sequences, 131,070).
+constexpr int64_t STEP_MOST = 0x7ff00000;
+
 // Sequences of a serving step: host cu_seqlens, or one token a sequence.
 int check_steps(int n_seqs, int64_t n_tokens, int n_slots, int reserved, const int32_t* cu) {
   if (n_seqs < 1) return fail(GDN_EINVAL, "n_seqs must be >= 1 (got %d)", n_seqs);
   if (n_slots < 1) return fail(GDN_EINVAL, "n_slots must be >= 1 (got %d)", n_slots);
   if (reserved != 0) return fail(GDN_EINVAL, "reserved0 must be 0");
+  if (n_tokens > STEP_MOST || n_seqs > STEP_MOST)
+    return fail(GDN_EINVAL, "too many tokens or sequences for one call (at most %lld)", (long long)STEP_MOST);
   if (!cu) {
     if (n_tokens != n_seqs)
       return fail(GDN_EINVAL, "without cu_seqlens n_tokens (%lld) must equal n_seqs (%d)", (long long)n_tokens, n_seqs);
@@ -1258,7 +1264,7 @@ int check_rope(const gdn_qk_rope_problem* p) {
   if (!(p->eps >= 0.f) || !std::isfinite(p->eps)) return fail(GDN_EINVAL, "eps must be >= 0");
   if (!std::isfinite(p->magnitude)) return fail(GDN_EINVAL, "magnitude must be finite");
   if (p->reserved0 != 0) return fail(GDN_EINVAL, "reserved0 must be 0");
-  if (p->n_tokens > (int64_t)0x7ff00000) return fail(GDN_EINVAL, "too many tokens for one call");
+  if (p->n_tokens > STEP_MOST) return fail(GDN_EINVAL, "too many tokens for one call");
   return GDN_OK;
 }
 

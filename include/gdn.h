@@ -253,7 +253,7 @@ int gdn_conv_bwd(const gdn_conv_problem* p, const void* x, const float* weight, 
  * [-1, n_slots) writes no state and fills its o rows (those inside [0, T]) with NaN, as does a
  * token with such a slot_tok for its own state and row. */
 typedef struct gdn_recurrent_problem {
-  int32_t n_seqs;                 /* N >= 1 sequences (of zero tokens or more) */
+  int32_t n_seqs;                 /* N >= 1 sequences (of zero tokens or more); N and T at most 2^31 - 2^20 */
   int32_t h_qk;                   /* H q/k heads */
   int32_t h_v;                    /* HV value heads, a multiple of H */
   int32_t d;                      /* head dim, 64 or 128 */

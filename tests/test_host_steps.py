@@ -158,3 +158,13 @@ def test_native_binding_checks_tensors():
         G.gdn_qk_rope_fwd(G.QkRopeProblem(3, 2, 2, 64), None, x, x, x)
     with pytest.raises(G.GdnError, match="expected a GPU"):
         G.gdn_conv_step(G.ConvStepProblem(3, [128], 8), x, x, None, x, x, x)
+
+
+@pytest.mark.parametrize("tokens", [0x7ff00001, 2 ** 31 - 1])
+def test_counts_near_the_end_of_32_bits_are_refused(tokens):
+    """The kernels step over tokens and sequences in 32 bits, some beyond the last one: the steps' limit is
+    the rotation's."""
+    _refused(_conv(G.ConvStepProblem(1, [8], 8, cu_seqlens_host=[0, tokens]), cu=PTR[0]), "too many")
+    _refused(_conv(G.ConvStepProblem(tokens, [8], 8)), "too many")
+    _refused(_recurrent(G.RecurrentProblem(1, 1, 1, 64, 8, cu_seqlens_host=[0, tokens])), "too many")
+    _refused(_recurrent(G.RecurrentProblem(tokens, 1, 1, 64, 8)), "too many")
