@@ -1224,7 +1224,7 @@ int gdn_rope_frequencies(const gdn_rope_scaling* s, uint64_t* freqs_host, float*
     hi = std::min(std::ceil(index(s->slow)), (double)(r - 1));
     if (hi - lo < 0.001) hi = lo + 0.001;
   }
-  for (int i = 0; i < r / 2; ++i) {
+  const auto turns = [&](int i) { // per position
     long double f = std::pow((long double)base, -2.0L * i / r);
     if (s->kind == GDN_ROPE_LINEAR) f /= s->factor;
     if (blend) {
@@ -1234,8 +1234,15 @@ int gdn_rope_frequencies(const gdn_rope_scaling* s, uint64_t* freqs_host, float*
       ramp = std::min(std::max(ramp, 0.0L), 1.0L);
       f = f * (1.0L - ramp) + f / s->factor * ramp;
     }
-    f /= 6.283185307179586476925286766559L; // turns per position; whole turns do not matter
-    f -= std::floor(f);
+    return f / 6.283185307179586476925286766559L;
+  };
+  // Bases and factors at the ends of their range make frequencies that are infinite or NaN, or whose
+  // whole turns leave nothing of the 64 bits to the fraction.
+  for (int i = 0; i < r / 2; ++i)
+    if (!(turns(i) < 4294967296.0L)) return fail(GDN_EINVAL, "frequency %d is not a number below 2^32 turns", i);
+  for (int i = 0; i < r / 2; ++i) {
+    long double f = turns(i);
+    f -= std::floor(f); // whole turns do not matter
     const long double scaled = std::round(f * 18446744073709551616.0L);
     freqs_host[i] = scaled >= 18446744073709551616.0L ? 0 : (uint64_t)scaled;
   }

@@ -173,3 +173,13 @@ def test_frequencies_refusals(kw, fragment):
     a.update(kw)
     with pytest.raises(G.GdnError, match=fragment):
         G.gdn_rope_frequencies(**a)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(scaling="linear", factor=1e-320), dict(scaling="ntk", factor=1e-300),
+    dict(scaling="yarn", factor=4.0, original_length=1e300, fast=2e-300, slow=1e-300),
+    dict(scaling="bands", factor=1e-300, original_length=1e-3)], ids=str)
+def test_frequencies_that_are_no_numbers_are_refused(kw):
+    """Settings in range one by one whose frequencies are infinite, NaN or without a fraction."""
+    with pytest.raises(G.GdnError, match="frequency"):
+        G.gdn_rope_frequencies(64, **kw)
