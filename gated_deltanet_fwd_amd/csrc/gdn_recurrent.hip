@@ -255,6 +255,11 @@ __attribute__((amdgpu_waves_per_eu(KIND == ONE_TOKEN ? 3 : 1, KIND == ONE_TOKEN 
 // up K S through LDS while they multiply Q S, and the second's share of the outputs goes to the first.
 // 700 tokens, f32, 64 wide, 8 heads and 5 sequences: 43 us, 62 ns a token; with KS = 1 50 us (49 with
 // nothing left to prepare); token by token in the step kernel 680 ns a token.
+// What is not finite in a block, be it an input, a product of rising decays or a sum, reaches all of its
+// tokens through the zeros above the diagonals (0 inf is NaN), also where the recurrence has ordinary
+// numbers: before a NaN, or where the decays rise over an empty state. It goes through U into every row of S
+// and never leaves S again. So where the last state is not finite a wave runs its columns of the sequence
+// once more from the start, token by token as the step kernel does.
 template <typename TI, int D, int NB, int KS>
 __global__ __launch_bounds__(128 * NB, 2) void k_recurrent_run(RecurrentArgs a) {
   constexpr int C = 16, DG = D / 4, R = D / 16; // tokens a block, rows a lane, tiles
@@ -271,10 +276,10 @@ __global__ __launch_bounds__(128 * NB, 2) void k_recurrent_run(RecurrentArgs a) 
   extern __shared__ __attribute__((aligned(16))) float lds[];
   Prep* prep = reinterpret_cast<Prep*>(lds); // of two turns
   struct Exchange { // KS = 2
-    f32x4 ks[2][2][64], o[2][64]; // of even and odd blocks: each half's K S, the second half's outputs
+    f32x4 ks[2][2][64], o[2][64]; // each half's K S, of even and odd exchanges; the second half's outputs, of blocks
   };
   Exchange* xch = reinterpret_cast<Exchange*>(prep + 2 * NB);
-  int* done = reinterpret_cast<int*>(&prep[0].t[0][C]); // blocks that each half has exchanged (in padding)
+  int* done = reinterpret_cast<int*>(&prep[0].t[0][C]); // exchanges that each half has made (in padding)
   const int lane = threadIdx.x & 63, g = lane >> 4, n16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // KS = 2: waves 0 and 1 hold the halves, 2, 3, 6 and 7 prepare, 4 and 5 would share the halves' SIMDs
@@ -437,20 +442,21 @@ __global__ __launch_bounds__(128 * NB, 2) void k_recurrent_run(RecurrentArgs a) 
       else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(int, x), to, off, 0, 0);
     }
   };
-  // The halves' exchange: a half writes its part, then counts the block; the other reads the count, then
-  // the part. Parts of even and odd blocks have places of their own: one is written again two blocks
-  // later, and by then the other half has counted a block after reading it. Both halves go through the
-  // same blocks, so the wait ends.
+  // The halves' exchange: a half writes its part, then counts the exchange; the other reads the count, then
+  // the part. Parts of even and odd exchanges have places of their own: one is written again two exchanges
+  // later, and by then the other half has counted one after reading it. Both halves go through the same
+  // blocks (an exchange each), agree at the end, and go through the same tokens if they run again, so the
+  // wait ends.
   const auto lds_order = [] { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup", "local"); };
   const auto others_count = [&] {
     return __builtin_amdgcn_readfirstlane(__hip_atomic_load(done + 1 - kh, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP));
   };
-  const auto count = [&](int blocks) {
+  const auto count = [&](int exchanges) {
     lds_order();
-    __hip_atomic_store(done + kh, blocks, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+    __hip_atomic_store(done + kh, exchanges, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
   };
-  const auto wait_for = [&](int blocks) {
-    while (others_count() < blocks) {}
+  const auto wait_for = [&](int exchanges) {
+    while (others_count() < exchanges) {}
     lds_order();
   };
   f32x4 o; // KS = 2: between the blocks, the first half's part of the outputs of the one before
@@ -567,13 +573,14 @@ __global__ __launch_bounds__(128 * NB, 2) void k_recurrent_run(RecurrentArgs a) 
     }
     return;
   }
-  {
+  const auto load_state = [&] {
     const float* p = a.states + (sp.in < 0 ? 0 : sp.in) * hd + head + at;
 #pragma unroll
     for (int r = 0; r < RH; ++r)
 #pragma unroll
       for (int i = 0; i < 4; ++i) S[r][i] = keepf(p[(4 * r + i) * D], sp.in >= 0);
-  }
+  };
+  load_state();
   if (sp.t0 < sp.t1) {
     float v0[4], v1[4];
     load_v(v0, sp.t0);
@@ -589,13 +596,64 @@ __global__ __launch_bounds__(128 * NB, 2) void k_recurrent_run(RecurrentArgs a) 
       load_v(v0, t + 2 * C);
       block(i + 1, v1, t + C);
     }
-    if constexpr (KS == 2) {
-      const int blocks = (sp.t1 - sp.t0 + C - 1) / C;
-      if (kh == 1) {
-        count(blocks + 1);
-      } else {
-        wait_for(blocks + 1);
-        store_o(o + xch->o[(blocks - 1) & 1][lane], sp.t0 + (blocks - 1) * C);
+    float sum = 0.f; // of 0 s over the state's values s: NaN if one is not finite
+#pragma unroll
+    for (int r = 0; r < RH; ++r)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) sum = __builtin_fmaf(0.f, S[r][y], sum);
+    bool finite = __ballot(sum != sum) == 0;
+    int x = 0; // KS = 2: exchanges made
+    if constexpr (KS == 2) { // the halves agree
+      x = (sp.t1 - sp.t0 + C - 1) / C; // one a block
+      xch->ks[x & 1][kh][lane] = f32x4{finite ? 0.f : 1.f, 0.f, 0.f, 0.f};
+      count(++x);
+      wait_for(x);
+      finite = finite && xch->ks[(x - 1) & 1][1 - kh][lane][0] == 0.f;
+      if (kh == 0) store_o(o + xch->o[x & 1][lane], sp.t0 + (x - 2) * C); // of the last block, x - 2
+    }
+    if (__builtin_expect(!finite, 0)) {
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent"); // the outputs so far are written before they are again
+      load_state();
+#pragma unroll 1
+      for (int t = sp.t0; t < sp.t1; ++t) {
+        const TI* kp = (const TI*)a.k + (int64_t)t * a.ks + (j * D + g * DG);
+        const TI* qp = (const TI*)a.q + (int64_t)t * a.qs + (j * D + g * DG);
+        float kk = 0.f, qq = 0.f, qk = 0.f, s1 = 0.f, s2 = 0.f, k[RH][4];
+#pragma unroll 1
+        for (int m = 0; m < DG; ++m) {
+          const float km = (float)kp[m], qm = (float)qp[m];
+          kk = __builtin_fmaf(km, km, kk);
+          qq = __builtin_fmaf(qm, qm, qq);
+          qk = __builtin_fmaf(qm, km, qk);
+        }
+#pragma unroll
+        for (int r = 0; r < RH; ++r)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            k[r][y] = (float)kp[4 * (kh * RH + r) + y];
+            s1 = __builtin_fmaf(S[r][y], k[r][y], s1);
+            s2 = __builtin_fmaf(S[r][y], (float)qp[4 * (kh * RH + r) + y], s2);
+          }
+        s1 = all_groups(s1);
+        s2 = all_groups(s2);
+        if constexpr (KS == 2) {
+          xch->ks[x & 1][kh][lane] = f32x4{s1, s2, 0.f, 0.f};
+          count(++x);
+          wait_for(x);
+          const f32x4 other = xch->ks[(x - 1) & 1][1 - kh][lane];
+          s1 += other[0];
+          s2 += other[1];
+        }
+        const float rk = a.l2norm ? inv_sqrt(all_groups(kk) + 1e-6f) : 1.f;
+        const float rq = a.l2norm ? inv_sqrt(all_groups(qq) + 1e-6f) : 1.f;
+        const float al = __expf(a.g[(int64_t)t * a.HV + h]);
+        const float u = a.beta[(int64_t)t * a.HV + h] * rk * __builtin_fmaf(-al * rk, s1, (float)((const TI*)a.v)[(int64_t)t * a.vs + col]);
+        const float out = rq * __builtin_fmaf(al, s2, all_groups(qk) * u);
+        if (g == 0 && kh == 0) ((TI*)a.o)[(int64_t)t * os + col] = (TI)out;
+#pragma unroll
+        for (int r = 0; r < RH; ++r)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) S[r][y] = __builtin_fmaf(k[r][y], u, al * S[r][y]);
       }
     }
   }

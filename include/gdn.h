@@ -234,8 +234,9 @@ int gdn_conv_bwd(const gdn_conv_problem* p, const void* x, const float* weight, 
  * leaves its start state). slot_in[n] = slot_out[n] updates a state in place. slot_tok, if given,
  * names for each token the slot that keeps the state after it (-1: none), so that a run of drafted
  * tokens can be rolled back to any of them. All arithmetic is FP32. Longer sequences (by the host's
- * lengths; without slot_tok) are taken 16 tokens at a time: an infinity or NaN in a row then reaches
- * the outputs of its sequence's block of 16 tokens, not only the later ones.
+ * lengths; without slot_tok) are taken 16 tokens at a time; where that ends in a state that is not
+ * finite, once more token by token, so an infinity or NaN reaches what the recurrence takes it to and
+ * no earlier token, and log decays may rise as far as the recurrence itself stays in FP32's range.
  * The order of the sums follows from the call's sizes, so the same call gives the same bits, and a
  * sequence in calls of different sizes may differ by rounding.
  *

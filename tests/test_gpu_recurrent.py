@@ -436,3 +436,71 @@ def test_bad_problems_are_refused_before_anything_is_allocated():
         with pytest.raises(G.GdnError):
             G.gdn_recurrent(p, *a)
         assert torch.cuda.memory_stats()["allocation.all.allocated"] == before
+
+
+# the run kernel's forms: 32 columns a workgroup, two waves a column, 64 columns a workgroup
+FORMS = {
+    "32_columns": dict(lengths=[40, 17, 0, 64, 3], H=2, HV=4),
+    "two_waves": dict(lengths=[100, 17, 0, 65, 3], H=1, HV=2),
+    "64_columns": dict(lengths=[80, 17, 0, 129, 3, 64, 65], H=4, HV=32),
+}
+
+
+@pytest.mark.parametrize("d,dtype", [(128, torch.bfloat16), (64, torch.float32)], ids=["bf16_128", "f32_64"])
+@pytest.mark.parametrize("form", FORMS)
+def test_runs_whose_decay_products_leave_the_range(form, d, dtype):
+    """Log decays of 12 on a state that is empty until just before it is read: the products of a block's
+    decays overflow, the recurrence does not, and its outputs are ordinary numbers."""
+    s = make(**FORMS[form], d=d, dtype=dtype)
+    s["slot_in"][:] = -1
+    for a, e in zip(s["cu_host"][:-1], s["cu_host"][1:]):
+        at = torch.arange(int(e) - int(a), device=DEV)
+        s["g"][a:e] = torch.where(at % 11 == 0, -1e30, 12.0)[:, None]  # the state is forgotten, then multiplied up
+        s["beta"][a:e] *= (at % 11 >= 9)[:, None]  # and written only shortly before it is forgotten
+    o, states = run(s)
+    o_ref, st_ref = reference(s)
+    check("o", o, o_ref, K)
+    check("states", states, st_ref, K)
+
+
+def finite_where_the_recurrence_is(s):
+    """Masks (o, last states) of what a float64 token recurrence in torch makes finite."""
+    H, HV, d = s["q"].shape[1], s["v"].shape[1], s["q"].shape[2]
+    head = torch.arange(HV) // (HV // H)
+    q, k, v, g, beta, states = (s[x].double().cpu() for x in ("q", "k", "v", "g", "beta", "states"))
+    q, k = (x / (x.square().sum(-1, keepdim=True) + 1e-6).sqrt() for x in (q, k))
+    o, last = torch.zeros_like(v), states.clone()
+    for n, (a, e) in enumerate(zip(s["cu_host"][:-1], s["cu_host"][1:])):
+        S = states[s["slot_in"][n]].clone()
+        for t in range(int(a), int(e)):
+            S = S * g[t].exp()[:, None, None]
+            kt = k[t, head][:, :, None]
+            u = beta[t][:, None] * (v[t] - (S * kt).sum(1))
+            S = S + kt * u[:, None]
+            o[t] = (S * q[t, head][:, :, None]).sum(1)
+        last[s["slot_out"][n]] = S
+    return torch.isfinite(o), torch.isfinite(last)
+
+
+@pytest.mark.parametrize("bad", ["v_nan", "v_inf", "k_nan", "q_inf", "g_nan", "beta_inf"])
+@pytest.mark.parametrize("form", FORMS)
+def test_a_bad_row_reaches_no_earlier_token_of_a_run(form, bad):
+    """One value that is not finite, inside a block of 16 tokens: the tokens before it keep their outputs
+    to rounding, other sequences and heads theirs bit for bit, as without it."""
+    s = make(**FORMS[form], d=64, dtype=torch.float32)
+    clean = run(s)
+    name, value = bad.split("_")
+    t = 21  # of the first sequence, in its second block
+    at = (t, 0, 5) if name in "qkv" else (t, 0)
+    s[name][at] = float(value)
+    o, states = run(s)
+    good_o, good_states = (x.to(DEV) for x in finite_where_the_recurrence_is(s))
+    assert torch.equal(torch.isfinite(o), good_o) and torch.equal(torch.isfinite(states), good_states)
+    assert not good_o[t, 0].all() and good_o[:t].all()
+    check("o before it", o[:t], f64(clean[0][:t]), K)
+    end = int(s["cu_host"][1])
+    assert torch.equal(o[end:], clean[0][end:])
+    heads = s["v"].shape[1] // s["q"].shape[1] if name in "qk" else 1
+    assert torch.equal(o[:, heads:], clean[0][:, heads:])
+    others = [x for x in range(s["slots"]) if x != s["slot_out"][0].item()]
+    assert torch.equal(states[others], clean[1][others])
