@@ -1114,6 +1114,7 @@ int gdn_recurrent(const gdn_recurrent_problem* p, const void* q, const void* k, 
       const int len = p->cu_seqlens_host[n + 1] - p->cu_seqlens_host[n];
       a.longest = std::max(a.longest, len);
       a.live += len > 0;
+      a.longs += len > gdn::SHORT_RUN;
     }
     if (p->n_seqs <= 16) {
       int by_length[16];

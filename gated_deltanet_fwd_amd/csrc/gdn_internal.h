@@ -184,12 +184,14 @@ struct ConvStepArgs {
 int launch_conv_step(const ConvStepArgs& a, int dtype, void* stream);
 
 // Recurrent gated delta rule (gdn_recurrent.hip).
+constexpr int SHORT_RUN = 8; // tokens up to which sequences beside longer ones are short
 struct RecurrentArgs {
   int64_t qs, ks, vs; // elements between the tokens of q, k, v
   uint64_t g_mul;     // 2^32 / G rounded up: h / G = h g_mul >> 32 for h, G <= 65536
   uint64_t order;     // up to 16 sequences, longest first by the host's lengths, 4 bits each
   int T, N, HV, D, l2norm, n_slots;
-  int longest, live; // by the host's lengths: the longest sequence, and how many have tokens
+  int longest, live, longs; // by the host's lengths: the longest sequence, how many have tokens and more than SHORT_RUN
+  int len_min, len_max;     // set by the launch: the kernel leaves sequences of other lengths to another
   const void* q;
   const void* k;
   const void* v;

@@ -11,6 +11,7 @@
 // them in registers from the first token to the last. Two kernels: k_recurrent_step for calls bound
 // by moving the states, k_recurrent_run for longer runs, bound by what a token computes.
 #include <atomic>
+#include <climits>
 
 #include "gdn_device.h"
 
@@ -105,6 +106,7 @@ __attribute__((amdgpu_waves_per_eu(KIND == ONE_TOKEN ? 3 : 1, KIND == ONE_TOKEN 
   TI* o = (TI*)a.o + (int64_t)h * D + col;
   const int64_t os = (int64_t)a.HV * D;
   const SeqSpan sp = seq_span(a.cu, a.slot_in, a.slot_out, n, a.T, a.n_slots);
+  if (KIND == RUN_OF_TOKENS && sp.t1 - sp.t0 > a.len_max) return;
   const float nan = __builtin_nanf("");
   if (!sp.ok) {
     for (int t = sp.t0; t < sp.t1; ++t)
@@ -294,6 +296,7 @@ __global__ __launch_bounds__(128 * NB, 2) void k_recurrent_run(RecurrentArgs a) 
   const int col = h * D + (blockIdx.x % (D / COLS)) * COLS + (KS == 1 ? wv * 16 : 0) + n16; // in a row of v and o
   const int os = a.HV * D;
   const SeqSpan sp = seq_span(a.cu, a.slot_in, a.slot_out, n, a.T, a.n_slots);
+  if (sp.t1 - sp.t0 < a.len_min) return;
   if (!sp.ok) {
     for (int t = sp.t0 + g; t < sp.t1 && !prepares && !idle && kh == 0; t += 4) ((TI*)a.o)[(int64_t)t * os + col] = (TI)__builtin_nanf("");
     return;
@@ -731,13 +734,30 @@ static int step_t(const RecurrentArgs& a, hipStream_t s) {
 // with two / one, 8 heads, 1 sequence, 128 wide, bf16: 64 tokens 12.9 / 12.9, 256 27 / 34; 64 wide, f32:
 // 16 tokens 6.3 / 5.9, 64 9.8 / 9.6, 256 19 / 22).
 // With slot_tok every token's state is wanted: always the step.
+// Beside longer sequences, short ones go to a step launch of their own when they alone would fill the CUs
+// several times with run workgroups, each of which prepares 16 tokens for a few. Each kernel leaves the
+// other's sequences by their length on the device. (us apart / in one run, 48 heads, 128 wide, bf16: 255
+// sequences of 1 token and one of 13 328 / 698, 16 and one of 100 41 / 66, 12 35 / 46, 12 of 6 and one of
+// 300 64 / 58; of 12 tokens, not taken as short, 24 and one of 300 123 / 113; 64 wide, f32, 8 heads: 127 of 6
+// and one of 100 28 / 30, 63 24 / 20.)
 template <typename TI, int D>
-static int recurrent_t(const RecurrentArgs& a, hipStream_t s) {
-  constexpr int CUS = 256;
-  const int64_t run_groups = (int64_t)a.live * a.HV * (D / 64);
+static int recurrent_t(RecurrentArgs a, hipStream_t s) {
+  constexpr int CUS = 256, SPLIT = 6;
+  a.len_min = INT_MIN;
+  a.len_max = INT_MAX;
   if (a.slot_tok) return step_t<TI, D, KEEP_EACH>(a, s);
   if (!a.cu) return step_t<TI, D, ONE_TOKEN>(a, s);
-  if (a.longest <= (run_groups <= CUS ? 6 : 12)) return step_t<TI, D, RUN_OF_TOKENS>(a, s);
+  const auto groups = [&](int n) { return (int64_t)n * a.HV * (D / 64); };
+  if (a.longest <= (groups(a.live) <= CUS ? 6 : 12)) return step_t<TI, D, RUN_OF_TOKENS>(a, s);
+  if (a.longs > 0 && groups(a.N - a.longs) > SPLIT * CUS) {
+    RecurrentArgs b = a;
+    b.len_max = b.longest = SHORT_RUN;
+    b.live = a.live - a.longs;
+    if (const int e = step_t<TI, D, RUN_OF_TOKENS>(b, s)) return e;
+    a.len_min = SHORT_RUN + 1;
+    a.live = a.longs;
+  }
+  const int64_t run_groups = groups(a.live);
   if (4 * run_groups <= CUS && a.longest > 64) return run_t<TI, D, 4, 2>(a, s);
   return 2 * run_groups <= CUS ? run_t<TI, D, 2, 1>(a, s) : run_t<TI, D, 4, 1>(a, s);
 }

@@ -237,7 +237,7 @@ int gdn_conv_bwd(const gdn_conv_problem* p, const void* x, const float* weight, 
  * lengths; without slot_tok) are taken 16 tokens at a time; where that ends in a state that is not
  * finite, once more token by token, so an infinity or NaN reaches what the recurrence takes it to and
  * no earlier token, and log decays may rise as far as the recurrence itself stays in FP32's range.
- * The order of the sums follows from the call's sizes, so the same call gives the same bits, and a
+ * The order of the sums follows from the call's sizes and lengths, so the same call gives the same bits, and a
  * sequence in calls of different sizes may differ by rounding.
  *
  *   q, k      [T, H, d], v [T, HV, d]  io dtype; a token's heads are contiguous, tokens are

@@ -504,3 +504,68 @@ def test_a_bad_row_reaches_no_earlier_token_of_a_run(form, bad):
     assert torch.equal(o[:, heads:], clean[0][:, heads:])
     others = [x for x in range(s["slots"]) if x != s["slot_out"][0].item()]
     assert torch.equal(states[others], clean[1][others])
+
+
+MIXED = {  # (sequences of at most 8 tokens fill the card with run workgroups several times; the others are longer)
+    "bf16_128": dict(lengths=[1, 8, 13, 0, 2, 9] * 9 + [90], H=8, HV=48, d=128, fresh=(2, 3)),
+    "f32_64": dict(lengths=[3, 1, 0, 8, 1] * 20 + [16, 9, 200], H=4, HV=32, d=64, dtype=torch.float32, fresh=(1, 101)),
+}
+
+
+@pytest.mark.parametrize("name", MIXED)
+def test_short_sequences_beside_long_ones(name):
+    s = make(**MIXED[name])
+    o, states = run(s)
+    again = run(s)
+    assert torch.equal(o, again[0]) and torch.equal(states, again[1])
+    o_ref, st_ref = reference(s)
+    check("o", o, o_ref, K)
+    check("states", states, st_ref, K)
+
+
+def test_lengths_on_the_device_may_differ_from_the_hosts():
+    """A captured mixed call replayed with other lengths, the short sequences long and the long short:
+    each sequence is taken by one of the call's kernels."""
+    d = dict(MIXED["bf16_128"], fresh=())
+    s, order = make(**d), list(reversed(d["lengths"]))
+    p = G.RecurrentProblem(len(order), d["H"], d["HV"], d["d"], s["slots"], cu_seqlens_host=s["cu_host"])
+    states, cu = s["states"].clone(), s["cu"].clone()
+    call = lambda: G.gdn_recurrent(p, *(s[x] for x in ("q", "k", "v", "g", "beta")), states, s["slot_in"],
+                                   s["slot_out"], cu_seqlens=cu)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o = call()
+    s["cu_host"] = np.concatenate([[0], np.cumsum(order)]).astype(np.int32)
+    cu.copy_(torch.from_numpy(s["cu_host"]))
+    states.copy_(s["states"])
+    o.fill_(float("nan"))
+    graph.replay()
+    torch.cuda.synchronize()
+    o_ref, st_ref = reference(s)
+    check("o", o, o_ref, K)
+    check("states", states, st_ref, K)
+
+
+def test_a_long_sequence_does_not_slow_the_short_ones_down():
+    """128 decoding sequences with one of 13 tokens among them: no more than half again over the 128 alone
+    (one kernel for all by the longest took twice as long)."""
+    def took(lengths):
+        s = make(lengths, H=16, HV=48, d=128, spare=0)
+        p = G.RecurrentProblem(len(lengths), 16, 48, 128, s["slots"], cu_seqlens_host=s["cu_host"])
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        best = float("inf")
+        for _ in range(6):
+            a.record()
+            for _ in range(10):
+                G.gdn_recurrent(p, *(s[x] for x in ("q", "k", "v", "g", "beta")), s["states"], s["slot_in"],
+                                s["slot_out"], cu_seqlens=s["cu"])
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b) / 10)
+        return best
+
+    alone, mixed = took([1] * 128), took([1] * 127 + [13])
+    print("128 sequences of one token %.3f ms, with one of 13 %.3f ms" % (alone, mixed), flush=True)
+    assert mixed < 1.5 * alone
