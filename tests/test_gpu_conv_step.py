@@ -197,3 +197,47 @@ def test_negative_groups_are_refused_before_anything_is_allocated():
     p = G.ConvStepProblem(2, [32, -8], s["slots"])
     with pytest.raises(G.GdnError, match="channels"):
         G.gdn_conv_step(p, s["x"], s["weight"], s["bias"], s["windows"], s["slot_in"], s["slot_out"])
+
+
+# a call for each kernel and each way through it: one or two sequences a lane, runs
+KERNELS = {
+    "one_sequence_a_lane": dict(lengths=[1] * 3, groups=[16, 8]),
+    "two_sequences_a_lane": dict(lengths=[1] * 1025, groups=[16, 8]),
+    "runs": dict(lengths=[2, 9, 3, 5], groups=[16, 8], dtype=torch.float32),
+}
+
+
+@pytest.mark.parametrize("name,what", [(x, y) for x in KERNELS for y in ("slot_in", "slot_out", "start", "end")
+                                       if y.startswith("slot") or max(KERNELS[x]["lengths"]) > 1])
+def test_every_kernel_refuses_what_is_out_of_range_on_the_device(name, what):
+    s = make(**KERNELS[name])
+    N = len(s["slot_in"])
+    n = dict(slot_in=N - 1, slot_out=1, start=0, end=N - 1)[what]
+    rows = slice(int(s["cu_host"][n]), int(s["cu_host"][n + 1]))
+    y_ref, win_ref = reference(s)
+    slot = s["slot_out"][n].item()
+    win_ref[slot] = f64(s["windows"][slot])
+    if what == "slot_in":
+        s["slot_in"][n] = s["slots"]
+    elif what == "slot_out":
+        s["slot_out"][n] = -2
+    else:
+        s["cu"][n if what == "start" else N] += -1 if what == "start" else 1
+    y, win = run(s)
+    assert torch.isnan(y[rows].float()).all()
+    good = torch.ones(y.shape[0], dtype=torch.bool)
+    good[rows] = False
+    check("y", y[good.to(DEV)], y_ref[good.numpy()], K)
+    assert np.array_equal(f64(win), win_ref)
+
+
+@pytest.mark.parametrize("name", KERNELS)
+def test_every_kernel_leaves_windows_nowhere_and_shares_starts(name):
+    s = make(**KERNELS[name])
+    free = [x for x in range(s["slots"]) if x not in s["slot_in"].tolist()]
+    s["slot_in"][1::2] = free[0]
+    s["slot_out"][::3] = -1
+    y, win = run(s)
+    y_ref, win_ref = reference(s)
+    check("y", y, y_ref, K)
+    assert np.array_equal(f64(win), win_ref)

@@ -569,3 +569,59 @@ def test_a_long_sequence_does_not_slow_the_short_ones_down():
     alone, mixed = took([1] * 128), took([1] * 127 + [13])
     print("128 sequences of one token %.3f ms, with one of 13 %.3f ms" % (alone, mixed), flush=True)
     assert mixed < 1.5 * alone
+
+
+# a call for each kernel and each way through it
+KERNELS = {
+    "one_token": dict(lengths=[1] * 5, H=2, HV=4, d=128),
+    "one_token_many": dict(lengths=[1] * 60, H=8, HV=48, d=64),
+    "few_tokens_16_columns": dict(lengths=[2, 4, 3, 1, 2], H=2, HV=4, d=128),
+    "few_tokens_32_columns": dict(lengths=[2, 4, 3, 1, 2] * 6, H=4, HV=48, d=64),
+    "run_two_waves": dict(lengths=[70, 33, 90, 16, 5], H=1, HV=2, d=64),
+    "run_two_waves_128": dict(lengths=[70, 33, 90, 16, 5], H=1, HV=2, d=128, dtype=torch.float32),
+    "run_32_columns": dict(lengths=[17, 33, 20, 16, 5], H=2, HV=4, d=128),
+    "run_64_columns": dict(lengths=[17, 33, 80, 16, 5], H=4, HV=48, d=128),
+    "mixed": MIXED["bf16_128"],
+}
+
+
+@pytest.mark.parametrize("name,what", [(x, y) for x in KERNELS for y in ("slot_in", "slot_out", "start", "end")
+                                       if y.startswith("slot") or max(KERNELS[x]["lengths"]) > 1])
+def test_every_kernel_refuses_what_is_out_of_range_on_the_device(name, what):
+    """A slot past the cache or a token range that leaves [0, T]: NaN rows for that sequence, no state of
+    it, the others right."""
+    s = make(**KERNELS[name])
+    N = len(s["slot_in"])
+    n = dict(slot_in=2, slot_out=1, start=0, end=N - 1)[what]
+    rows = slice(int(s["cu_host"][n]), int(s["cu_host"][n + 1]))
+    o_ref, st_ref = reference(s)
+    slot = s["slot_out"][n].item()
+    st_ref[slot] = f64(s["states"][slot])
+    if what == "slot_in":
+        s["slot_in"][n] = s["slots"]
+    elif what == "slot_out":
+        s["slot_out"][n] = -2
+    else:
+        s["cu"][n if what == "start" else N] += -1 if what == "start" else 1
+    o, states = run(s)
+    assert torch.isnan(o[rows].float()).all() and rows.stop > rows.start
+    good = torch.ones(o.shape[0], dtype=torch.bool)
+    good[rows] = False
+    check("o", o[good.to(DEV)], o_ref[good.numpy()], K)
+    check("states", states, st_ref, K)
+
+
+@pytest.mark.parametrize("name", KERNELS)
+def test_every_kernel_leaves_states_nowhere_and_shares_starts(name):
+    """slot_out = -1 keeps no state; sequences may start from one slot that none of them writes."""
+    s = make(**KERNELS[name])
+    free = [x for x in range(s["slots"]) if x not in s["slot_in"].tolist()]
+    s["slot_in"][1::2] = free[0]
+    s["slot_out"][::3] = -1
+    o, states = run(s)
+    o_ref, st_ref = reference(s)
+    check("o", o, o_ref, K)
+    check("states", states, st_ref, K)
+    named = set(s["slot_out"].tolist())
+    for slot in (x for x in range(s["slots"]) if x not in named):
+        assert torch.equal(states[slot], s["states"][slot])
