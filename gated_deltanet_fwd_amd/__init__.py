@@ -554,7 +554,8 @@ def gdn_recurrent(p: RecurrentProblem, q, k, v, g, beta, states, slot_in, slot_o
     """One serving step of the recurrent rule: runs every sequence's tokens from states[slot_in] (-1:
     zero), leaves its state in states[slot_out] (-1: nowhere) and, with slot_tok, the state after each
     token in states[slot_tok]. q, k and v may be parts of one row (a token's heads contiguous).
-    Returns o; `states` is updated in place."""
+    Returns o; `states` is updated in place. Rows that the lengths on the device leave to no sequence are
+    not written: with `o` given they keep its values, without they are uninitialised."""
     return _call("recurrent", v, stream, p.at, q, k, v, g, beta, states, slot_in, slot_out, slot_tok, cu_seqlens, o)
 
 
@@ -585,7 +586,8 @@ def gdn_conv_step(p: ConvStepProblem, x, weight, bias, windows, slot_in, slot_ou
                   outs=None, stream=None):
     """One serving step of the conv front-end on cached windows (slots as in gdn_recurrent). Returns
     the list of outputs, [T, group_channels[g]] (of a short call parts of one allocation, as are those
-    of gdn_qk_rope_fwd and _bwd); `windows` is updated in place (None at width 1)."""
+    of gdn_qk_rope_fwd and _bwd); `windows` is updated in place (None at width 1). Rows of no sequence are
+    as in gdn_recurrent."""
     return _call("conv_step", x, stream, p.at, x, weight, bias, windows, slot_in, slot_out, slot_tok, cu_seqlens,
                  None if outs is None else list(outs))
 

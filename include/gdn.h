@@ -252,7 +252,9 @@ int gdn_conv_bwd(const gdn_conv_problem* p, const void* x, const float* weight, 
  * The call may be captured into a graph; the device arrays are read at each replay. They are
  * checked on the device: a sequence with a token range outside [0, T] or a slot outside
  * [-1, n_slots) writes no state and fills its o rows (those inside [0, T]) with NaN, as does a
- * token with such a slot_tok for its own state and row. */
+ * token with such a slot_tok for its own state and row. Lengths on the device may differ from the
+ * host's (a graph replayed with other lengths, or a shorter batch: T and N stay, sequences may be
+ * empty): rows of o that no sequence covers are not written and keep what the buffer held. */
 typedef struct gdn_recurrent_problem {
   int32_t n_seqs;                 /* N >= 1 sequences (of zero tokens or more); N and T at most 2^31 - 2^20 */
   int32_t h_qk;                   /* H q/k heads */
@@ -369,7 +371,8 @@ int gdn_qk_rope_bwd(const gdn_qk_rope_problem* p, const void* q, const void* k, 
  * x, zeros before its first token, are its window). Slots, cu_seqlens, in-place updates and the
  * checks on the device are those of gdn_recurrent: a sequence reads windows[slot_in[n]] (zeros if
  * -1), writes its last window to windows[slot_out[n]], and slot_tok keeps the window after each
- * token. Where gdn_recurrent fills o rows with NaN, the rows of every y[g] are. */
+ * token. Where gdn_recurrent fills o rows with NaN, the rows of every y[g] are, and rows that no
+ * sequence covers are not written. */
 typedef struct gdn_conv_step_problem {
   int32_t n_seqs;                 /* N >= 1 sequences */
   int32_t channels;               /* C = sum of group_channels, a multiple of 8 */

@@ -241,3 +241,14 @@ def test_every_kernel_leaves_windows_nowhere_and_shares_starts(name):
     y_ref, win_ref = reference(s)
     check("y", y, y_ref, K)
     assert np.array_equal(f64(win), win_ref)
+
+
+def test_rows_of_no_sequence_keep_their_values():
+    s = make([2, 9, 3, 5], [16, 8])
+    s["cu"][-1] = 14
+    outs = [torch.full((19, c), 7.0, dtype=torch.bfloat16, device=DEV) for c in s["groups"]]
+    y, _ = run(s, outs=outs)
+    s["cu_host"][-1] = 14
+    y_ref, _ = reference(s)
+    assert (y[14:] == 7).all()
+    check("y", y[:14], y_ref[:14], K)

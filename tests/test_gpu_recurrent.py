@@ -625,3 +625,18 @@ def test_every_kernel_leaves_states_nowhere_and_shares_starts(name):
     named = set(s["slot_out"].tolist())
     for slot in (x for x in range(s["slots"]) if x not in named):
         assert torch.equal(states[slot], s["states"][slot])
+
+
+@pytest.mark.parametrize("name", ["few_tokens_16_columns", "run_two_waves", "run_32_columns", "run_64_columns", "mixed"])
+def test_rows_of_no_sequence_keep_their_values(name):
+    """The device's lengths end before T (a shorter batch): the rows behind them are not written."""
+    s = make(**KERNELS[name])
+    cut = int(s["cu_host"][-2])
+    s["cu"][-1] = cut
+    o = torch.full(s["v"].shape, 7.0, dtype=s["v"].dtype, device=DEV)
+    run(s, o=o)
+    s["cu_host"] = s["cu_host"].copy()
+    s["cu_host"][-1] = cut
+    o_ref, _ = reference(s)
+    assert (o[cut:] == 7).all() and cut < o.shape[0]
+    check("o", o[:cut], o_ref[:cut], K)
