@@ -585,9 +585,11 @@ class ConvStepProblem:
 def gdn_conv_step(p: ConvStepProblem, x, weight, bias, windows, slot_in, slot_out, slot_tok=None, cu_seqlens=None,
                   outs=None, stream=None):
     """One serving step of the conv front-end on cached windows (slots as in gdn_recurrent). Returns
-    the list of outputs, [T, group_channels[g]] (of a short call parts of one allocation, as are those
-    of gdn_qk_rope_fwd and _bwd); `windows` is updated in place (None at width 1). Rows of no sequence are
-    as in gdn_recurrent."""
+    the list of outputs, [T, group_channels[g]]; `windows` is updated in place (None at width 1). Rows of
+    no sequence are as in gdn_recurrent. The outputs of a short call (up to 1 MiB together) are parts of
+    one storage, as those of gdn_qk_rope_fwd and _bwd: one part keeps all of the memory and torch.save
+    of it writes all, and resize_ to more elements grows a part over the ones behind it, as with the
+    parts of torch.split. Clone a part before either, or give the outputs."""
     return _call("conv_step", x, stream, p.at, x, weight, bias, windows, slot_in, slot_out, slot_tok, cu_seqlens,
                  None if outs is None else list(outs))
 
