@@ -346,6 +346,11 @@ __device__ __forceinline__ float inv_sqrt(float x) {
   const float y = __builtin_fmaf(__builtin_fmaf(-h, r, 0.5f), r, r);
   return __builtin_isfinite(r) && r != 0.f ? y : r; // at 0, infinity and NaN the step has nothing to add
 }
+// The same where x may be subnormal, which the estimate takes for 0.
+__device__ __forceinline__ float inv_sqrt_any(float x) {
+  const bool tiny = x < 0x1p-100f;
+  return inv_sqrt(tiny ? x * 0x1p60f : x) * (tiny ? 0x1p30f : 1.f);
+}
 
 // One sequence of a serving step: its token range and slots, checked against the call's sizes. ok
 // is false when the device arrays hold a range outside [0, T] or a slot outside [-1, n_slots); the

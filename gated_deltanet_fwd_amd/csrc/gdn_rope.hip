@@ -264,7 +264,7 @@ __global__ __launch_bounds__(256) void k_rope_fwd(RopeArgs a) {
         float ss = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(v[e], v[e], ss);
-        const float r = inv_sqrt(__builtin_fmaf(group_sum<LPR>(ss), mean, a.eps));
+        const float r = inv_sqrt_any(__builtin_fmaf(group_sum<LPR>(ss), mean, a.eps));
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] *= r * w[e];
       }
@@ -325,12 +325,13 @@ __global__ __launch_bounds__(256) void k_rope_bwd(RopeArgs a) {
             ss = __builtin_fmaf(v[e], v[e], ss);
             vd = __builtin_fmaf(v[e], dn[e], vd);
           }
-          const float r = inv_sqrt(__builtin_fmaf(group_sum<LPR>(ss), mean, a.eps));
-          const float k = group_sum<LPR>(vd) * r * r * r * mean;
+          const float r = inv_sqrt_any(__builtin_fmaf(group_sum<LPR>(ss), mean, a.eps));
+          const float k = group_sum<LPR>(vd) * r * mean; // (r^3 overflows for rows that dx = r (dn - k n) fits)
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            sum[e] = mine ? __builtin_fmaf(d[e], v[e] * r, sum[e]) : sum[e];
-            d[e] = __builtin_fmaf(r, dn[e], -k * v[e]);
+            const float n = v[e] * r;
+            sum[e] = mine ? __builtin_fmaf(d[e], n, sum[e]) : sum[e];
+            d[e] = r * __builtin_fmaf(-k, n, dn[e]);
           }
         }
         if (m.on && mine)

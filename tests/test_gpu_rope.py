@@ -251,3 +251,22 @@ def test_no_tokens_give_empty_gradients_of_both():
     g = G.gdn_qk_rope_bwd(*args(s), s["dyq"], s["dyk"], q_weight=s["wq"], k_weight=s["wk"])
     assert g["dq"].shape == (0, 2, 64) and g["dk"].shape == (0, 1, 64)
     assert not g["dq_weight"].any() and not g["dk_weight"].any()
+
+
+@pytest.mark.parametrize("norm", ["rms", "l2"])
+@pytest.mark.parametrize("size", [1e-20, 1e-16, 1e-6, 1e15])
+def test_rows_of_any_size_without_eps(norm, size):
+    """eps = 0: the norm does not depend on a row's size, also where the mean square is subnormal (each
+    product then is off by up to 2^-150 of 1e-40, the root by 4e-6) or the root's cube overflows."""
+    s = make(20, 2, 1, 64, dtype=torch.float32, norm=norm, eps=0.0)
+    for x in ("q", "k"):
+        s[x].mul_(size).add_(torch.sign(s[x]) * size)  # no value far below the others
+    q, k = G.gdn_qk_rope_fwd(*args(s), q_weight=s["wq"], k_weight=s["wk"])
+    g = G.gdn_qk_rope_bwd(*args(s), s["dyq"], s["dyk"], q_weight=s["wq"], k_weight=s["wk"])
+    pos = s["pos"].cpu().numpy()
+    for x, y, w, dy, dx, dw in (("q", q, "wq", "dyq", g["dq"], g["dq_weight"]), ("k", k, "wk", "dyk", g["dk"], g["dk_weight"])):
+        more = 64 if size < 1e-19 else 0  # 64 2^-24 = 3.8e-6
+        check("y", y, rope_oracle.fwd(f64(s[x]), pos, s["f"], f64(s[w]), **oracle_kw(s)), K + more)
+        dx_ref, dw_ref = rope_oracle.bwd(f64(s[x]), f64(s[dy]), pos, s["f"], f64(s[w]), **oracle_kw(s))
+        check("dx", dx, dx_ref, K + 2 * more)
+        check("dw", dw, dw_ref, 40 * (K + more))
