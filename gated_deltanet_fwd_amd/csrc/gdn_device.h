@@ -354,7 +354,7 @@ __device__ __forceinline__ float inv_sqrt_any(float x) {
 
 // One sequence of a serving step: its token range and slots, checked against the call's sizes. ok
 // is false when the device arrays hold a range outside [0, T] or a slot outside [-1, n_slots); the
-// range is then cut to [0, T], for the NaN that its rows get.
+// range is then cut to [0, T], for the NaN that its rows get, and is empty where it falls.
 struct SeqSpan {
   int t0, t1, in, out;
   bool ok;
@@ -368,7 +368,7 @@ __device__ __forceinline__ SeqSpan seq_span(const int32_t* cu, const int32_t* sl
   s.out = slot_out[n];
   s.ok = s.t0 >= 0 && s.t1 >= s.t0 && s.t1 <= T && s.in >= -1 && s.in < n_slots && s.out >= -1 && s.out < n_slots;
   s.t0 = max(s.t0, 0);
-  s.t1 = min(s.t1, T);
+  s.t1 = max(min(s.t1, T), s.t0);
   return s;
 }
 

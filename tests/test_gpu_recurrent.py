@@ -640,3 +640,25 @@ def test_rows_of_no_sequence_keep_their_values(name):
     o_ref, _ = reference(s)
     assert (o[cut:] == 7).all() and cut < o.shape[0]
     check("o", o[:cut], o_ref[:cut], K)
+
+
+@pytest.mark.parametrize("end", [0, -1, -2 ** 31])
+@pytest.mark.parametrize("name", [x for x in KERNELS if not x.startswith("one")])
+def test_a_range_that_falls_is_empty(name, end):
+    """The second entry of the device's cu_seqlens below the first, down to the type's lowest value: no rows
+    for the first sequence, and for the second NaN from its cut start on if that lies below 0."""
+    s = make(**KERNELS[name])
+    s["cu"][0], s["cu"][1] = min(end + 1, 0), end
+    stop = int(s["cu_host"][2])
+    o_ref, st_ref = reference(s)
+    if end == 0:  # an empty first sequence, and one that begins too early
+        s["cu"][0] = 1
+    lost = s["slot_out"][:2].tolist()
+    o, states = run(s)
+    if end < 0:
+        assert torch.isnan(o[:stop].float()).all()
+    check("o", o[stop:], o_ref[stop:], K)
+    keep = [x for x in range(s["slots"]) if x not in lost]
+    check("states", states[keep], st_ref[keep], K)
+    assert torch.equal(states[lost[0]], s["states"][lost[0]])
+    assert (end == 0) or torch.equal(states[lost[1]], s["states"][lost[1]])
