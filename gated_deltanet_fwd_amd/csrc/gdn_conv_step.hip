@@ -7,10 +7,11 @@
 // A lane owns 4 consecutive channels and runs a sequence's tokens in order, the window in registers.
 // What bounds a batch is moving the windows and rows; a lane's taps (W floats a channel, more bytes
 // than its bf16 rows) come from the L2, so in a batch with one token a sequence a lane takes two
-// sequences and loads all of their rows at once: 256 sequences of 10,240 bf16 channels (42 MB) 9.8 us,
-// 10.8 with one, 10.3 with four; with 8 channels a lane 11.2, and a single sequence 3.9 us instead of
-// 3.1. What bounds a run is the wait for each token's row, so the rows of STEP_U tokens are loaded
-// together: 24 runs of up to 8 tokens 5.5 us, 6.7 one by one.
+// sequences and loads all of their rows at once: 256 sequences of 10,240 bf16 channels (42 MB) take 9.3
+// us, 1.0 more with one a lane, 0.5 more with four; with 8 channels a lane 1.4 more, and a single sequence
+// 3.9 us instead of 3.1. What bounds a run is the wait for each token's row, so the rows of STEP_U tokens
+// are loaded together: 24 runs of up to 8 tokens 5.6 us, 1.2 more one by one. A run's rounds of four wait
+// for each other: 700 tokens of 10,240 channels 215 us (29 MB), 5 such runs 237; 100 tokens 28.
 #include "gdn_device.h"
 
 namespace gdn {

@@ -255,7 +255,7 @@ __attribute__((amdgpu_waves_per_eu(KIND == ONE_TOKEN ? 3 : 1, KIND == ONE_TOKEN 
 // (64) instructions of 32 cycles a block and wave. So with CUs to spare and long runs a workgroup takes
 // 16 columns, two waves with half of the rows (r) of each (KS = 2) and four that prepare; the halves add
 // up K S through LDS while they multiply Q S, and the second's share of the outputs goes to the first.
-// 700 tokens, f32, 64 wide, 8 heads and 5 sequences: 43 us, 62 ns a token; with KS = 1 50 us (49 with
+// 700 tokens, f32, 64 wide, 8 heads and 5 sequences: 42 us, 60 ns a token; with KS = 1 50 us (49 with
 // nothing left to prepare); token by token in the step kernel 680 ns a token.
 // What is not finite in a block, be it an input, a product of rising decays or a sum, reaches all of its
 // tokens through the zeros above the diagonals (0 inf is NaN), also where the recurrence has ordinary
@@ -699,13 +699,10 @@ static int run_t(const RecurrentArgs& a, hipStream_t s) {
 }
 
 // The step kernel, its columns a wave and waves a workgroup by the number of waves of 32 columns. With
-// few, a wave to a workgroup spreads them over more CUs, so that their stores do not queue at one (us
-// in workgroups of 4 / 1, 128 wide, bf16: one token 192 waves 4.3 / 3.7, 768 5.4 / 5.2, 1152 8.0 / 6.8,
-// 16 sequences of 48 heads 19.0 / 21.1; 6 kept tokens 192 waves 12.4 / 10.1, 768 15.8 / 15.8, 1152 27 /
-// 25, 16 sequences of 48 heads 67 / 72). With fewer still, and several tokens, 16 columns (us with 32 /
-// 16: 6 kept tokens, one wave a workgroup, 64 waves 9.7 / 8.1, 192 10.1 / 9.6, 384 11.6 / 11.8, 576 13.6
-// / 16.1; 5 tokens, four waves a workgroup, 64 waves 8.0 / 6.3, 384 9.4 / 7.2, 576 9.8 / 9.4, 1152 15 /
-// 16).
+// few, a wave to a workgroup spreads them over more CUs, so that their stores do not queue at one (us in
+// workgroups of 4 / 1, 128 wide, bf16, one token: 1152 waves 8.0 / 6.8, 3072 19.0 / 21.1). With fewer
+// still, and several tokens, 16 columns (us with 32 / 16, 6 kept tokens: 192 waves 10.1 / 9.6, 576 13.6 /
+// 16.1).
 template <typename TI, int D, StepKind KIND>
 static int step_t(const RecurrentArgs& a, hipStream_t s) {
   constexpr int64_t SPREAD = 1280, HALVED = 384;
@@ -722,24 +719,18 @@ static int step_t(const RecurrentArgs& a, hipStream_t s) {
   return (int)hipGetLastError();
 }
 
-// The kernel by the longest sequence and the number of sequences with tokens, as the host knows them.
-// A run's workgroup pays for whole blocks of 16 tokens and for the start of its two halves, so it gains
-// from 7 tokens on, and with more workgroups than CUs later (us step / run, 48 heads, 128 wide, bf16: 1
-// sequence of 4 tokens 6.2 / 7.6, of 8 9.0 / 7.8, of 24 20 / 9.6; 32 sequences of 8 tokens 57 / 84, of 12
-// 71 / 84, of 16 86 / 85, of 24 118 / 112; 64 wide, f32, 4 sequences of 6 tokens 6.3 / 6.5, of 8 7.3 /
-// 6.5, 16 of 12 17 / 19, of 16 21 / 19). 32 columns a workgroup while each then has a CU, 64 beyond (us
-// with 32 / 64, 48 heads, 256 tokens, 128 wide, bf16: 1 sequence 35 / 43, 2 61 / 47; 64 wide, f32: 2
-// sequences 23 / 27, 3 37 / 29).
-// Two waves a column while each 16 columns have a CU and the run is long enough to pay for the start (us
-// with two / one, 8 heads, 1 sequence, 128 wide, bf16: 64 tokens 12.9 / 12.9, 256 27 / 34; 64 wide, f32:
-// 16 tokens 6.3 / 5.9, 64 9.8 / 9.6, 256 19 / 22).
-// With slot_tok every token's state is wanted: always the step.
+// The kernel by the host's lengths. A run's workgroup pays for whole blocks of 16 tokens and for the start
+// of its two halves, so it gains from 7 tokens on, and with more workgroups than CUs later (us step / run,
+// 48 heads, 128 wide, bf16: 1 sequence of 4 tokens 6.2 / 7.6, of 8 9.0 / 7.8; 32 sequences of 12 71 / 84, of
+// 24 118 / 112). 32 columns a workgroup while each then has a CU, 64 beyond (us with 32 / 64, of 256 tokens:
+// 1 sequence 35 / 43, 2 61 / 47). Two waves a column while each 16 columns have a CU and the run is long
+// enough to pay for the start (us with two / one, 8 heads: 64 tokens 12.9 / 12.9, 256 27 / 34). With slot_tok
+// every token's state is wanted: always the step.
 // Beside longer sequences, short ones go to a step launch of their own when they alone would fill the CUs
 // several times with run workgroups, each of which prepares 16 tokens for a few. Each kernel leaves the
-// other's sequences by their length on the device. (us apart / in one run, 48 heads, 128 wide, bf16: 255
-// sequences of 1 token and one of 13 328 / 698, 16 and one of 100 41 / 66, 12 35 / 46, 12 of 6 and one of
-// 300 64 / 58; of 12 tokens, not taken as short, 24 and one of 300 123 / 113; 64 wide, f32, 8 heads: 127 of 6
-// and one of 100 28 / 30, 63 24 / 20.)
+// other's sequences by their length on the device. (us apart / in one run launch, 48 heads: 255 sequences of
+// 1 token and one of 13 327 / 664, 16 of 6 and one of 100 47 / 67, 12 of 6 and one of 300 64 / 58; of 12
+// tokens, not taken as short, 24 and one of 300 123 / 113.)
 template <typename TI, int D>
 static int recurrent_t(RecurrentArgs a, hipStream_t s) {
   constexpr int CUS = 256, SPLIT = 6;

@@ -391,7 +391,9 @@ static int lanes_of(int D) { return D <= 64 ? 8 : D <= 128 ? 16 : 32; }
 // wide, forward, take 12.8 us in 8192 waves, 17 us in 32768, each with its own cosines and sines.
 // Long ones go over the groups with up to `most`, each wave the same number of groups: 32,768 such
 // tokens take 97 us in 32768 waves, 101 us in 8192; backward, where each workgroup leaves a row of
-// partial sums, 154 us in 4096 and 159 us in 8192 or more.
+// partial sums, 154 us in 4096 and 159 us in 8192 or more. A backward without weights has the same limit:
+// there more waves gain or lose by the sizes (4096 / 8192 / 32768 waves: 32,768 tokens, L2 150 / 150 / 144
+// us, the rotation alone 96 / 98 / 93; 65,536 tokens of 3 + 1 heads, the rotation alone 32 / 30 / 32).
 static void shape_side(RopeSide& s, int64_t T, int D, int all_heads, int64_t fill, int64_t most) {
   const int rpw = 64 / lanes_of(D);
   s.tpp = 1;

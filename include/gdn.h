@@ -228,7 +228,10 @@ int gdn_conv_bwd(const gdn_conv_problem* p, const void* x, const float* weight, 
 /* ---- The gated delta rule, recurrent: one serving step on cached states --------------------
  * The operation at the top of this file, token by token, on states that live in a cache between
  * calls: one token a sequence when decoding, a few when drafted tokens are checked or a prompt is
- * extended (whole prompts go through gdn_fwd, whose ht has the layout of one cached state).
+ * extended (whole prompts go through gdn_fwd, whose h0 and ht have the layout of cached states. It is
+ * faster from about 256 tokens on with one sequence, 85 with 4, 32 with 12 ((16, 48) heads, d = 128,
+ * bf16), and rounds its products' operands to bf16: an error of 2.4e-3 in the state after 512 tokens,
+ * where FP32 here leaves 1.6e-7).
  * Sequence n starts from states[slot_in[n]] (from zero if slot_in[n] = -1), runs its tokens in
  * order and leaves its last state in states[slot_out[n]] (nowhere if -1; a sequence of no tokens
  * leaves its start state). slot_in[n] = slot_out[n] updates a state in place. slot_tok, if given,
