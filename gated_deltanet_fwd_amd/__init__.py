@@ -19,10 +19,16 @@ allocates are allocated on its launch stream. The functions carry the C names:
     gdn_rope_frequencies(rotary_dim, ...)         -> (int64 tensor on the CPU, magnitude)
     gdn_qk_rope_fwd(rope_problem, q, k, positions, freqs, ...) -> (q_out, k_out)
     gdn_qk_rope_bwd(rope_problem, q, k, positions, freqs, dq_out, dk_out, ...) -> dict of gradients
+    gdn_linear_fwd(linear_problem, q, k, v, g, cu, ...)       -> (o, ht)
+    gdn_linear_bwd(linear_problem, q, k, v, g, cu, dO, ...)   -> dict of gradients
+    gdn_linear_step(linear_step_problem, q, k, v, g, states, slot_in, slot_out, ...) -> o
+    gdn_rms_norm_fwd(rms_norm_problem, x, ...)    -> (y, scales, residual_out)
+    gdn_rms_norm_bwd(rms_norm_problem, x, dy, ...) -> dict dx, dweight
+    gdn_step_maps(step_maps_problem, lengths, contexts, block_table, free_list, free_count, ...) -> dict
 
-gdn_recurrent, gdn_conv_step, gdn_qk_rope_fwd and gdn_qk_rope_bwd check their tensors (shape, type,
-layout, device) before the call and raise GdnError; their marshalling is native (csrc/gdn_binding.cpp),
-since a decoding step is shorter than it would take in Python.
+gdn_recurrent and everything below it in this list but gdn_rope_frequencies check their tensors (shape,
+type, layout, device) before the call and raise GdnError; their marshalling is native
+(csrc/gdn_binding.cpp), since a decoding step is shorter than it would take in Python.
 
 A missing or unloadable library raises ImportError-like errors at first use; there is no other
 code path.
@@ -48,9 +54,12 @@ ABI_VERSION = 2
 EXPORTS = ("gdn_saved_bytes", "gdn_workspace_bytes", "gdn_fwd", "gdn_fwd_recompute", "gdn_bwd", "gdn_status",
            "gdn_fwd_noalloc", "gdn_conv_workspace_bytes", "gdn_conv_fwd", "gdn_conv_bwd", "gdn_last_error",
            "gdn_abi_version", "gdn_recurrent", "gdn_conv_step", "gdn_rope_frequencies", "gdn_qk_rope_workspace_bytes",
-           "gdn_qk_rope_fwd", "gdn_qk_rope_bwd")
+           "gdn_qk_rope_fwd", "gdn_qk_rope_bwd", "gdn_linear_workspace_bytes", "gdn_linear_fwd", "gdn_linear_bwd",
+           "gdn_linear_step", "gdn_rms_norm_workspace_bytes", "gdn_rms_norm_fwd", "gdn_rms_norm_bwd", "gdn_step_maps")
 NORMS = {"none": 0, "l2": 1, "rms": 2}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
+DECAYS = {"token": 0, "head": 1}
+NORM_OUTS = {"io": 0, "e4m3": 1}
 
 
 class GdnError(RuntimeError):
@@ -162,6 +171,70 @@ class _RopeScaling(ctypes.Structure):
     ]
 
 
+class _LinearProblem(ctypes.Structure):
+    _fields_ = [
+        ("n_seqs", ctypes.c_int32),
+        ("h_qk", ctypes.c_int32),
+        ("h_v", ctypes.c_int32),
+        ("d", ctypes.c_int32),
+        ("n_tokens", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("decay", ctypes.c_int32),
+        ("has_h0", ctypes.c_int32),
+        ("want_ht", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("reserved0", ctypes.c_int32),
+        ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+        ("cu_seqlens_host", ctypes.POINTER(ctypes.c_int32)),
+    ]
+
+
+class _LinearStepProblem(ctypes.Structure):
+    _fields_ = [
+        ("n_seqs", ctypes.c_int32),
+        ("h_qk", ctypes.c_int32),
+        ("h_v", ctypes.c_int32),
+        ("d", ctypes.c_int32),
+        ("n_tokens", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("decay", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("n_slots", ctypes.c_int32),
+        ("reserved0", ctypes.c_int32),
+        ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+        ("cu_seqlens_host", ctypes.POINTER(ctypes.c_int32)),
+    ]
+
+
+class _RmsNormProblem(ctypes.Structure):
+    _fields_ = [
+        ("n_rows", ctypes.c_int64),
+        ("d", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("out", ctypes.c_int32),
+        ("group", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("reserved0", ctypes.c_int32),
+        ("x_stride", ctypes.c_int64),
+        ("residual_stride", ctypes.c_int64),
+    ]
+
+
+class _StepMapsProblem(ctypes.Structure):
+    _fields_ = [
+        ("n_seqs", ctypes.c_int32),
+        ("block", ctypes.c_int32),
+        ("n_tokens", ctypes.c_int64),
+        ("max_blocks", ctypes.c_int32),
+        ("n_free", ctypes.c_int32),
+        ("reserved0", ctypes.c_int32),
+    ]
+
+
 _lib = None
 
 
@@ -209,6 +282,24 @@ def load_library(path: str = LIB_PATH):
     lib.gdn_qk_rope_fwd.restype = I
     lib.gdn_qk_rope_bwd.argtypes = [rp] + [P] * 13 + [Z, P]
     lib.gdn_qk_rope_bwd.restype = I
+    lp = ctypes.POINTER(_LinearProblem)
+    lib.gdn_linear_workspace_bytes.argtypes = [lp, I]
+    lib.gdn_linear_workspace_bytes.restype = Z
+    lib.gdn_linear_fwd.argtypes = [lp] + [P] * 9 + [Z, P]
+    lib.gdn_linear_fwd.restype = I
+    lib.gdn_linear_bwd.argtypes = [lp] + [P] * 14 + [Z, P]
+    lib.gdn_linear_bwd.restype = I
+    lib.gdn_linear_step.argtypes = [ctypes.POINTER(_LinearStepProblem)] + [P] * 11
+    lib.gdn_linear_step.restype = I
+    np_ = ctypes.POINTER(_RmsNormProblem)
+    lib.gdn_rms_norm_workspace_bytes.argtypes = [np_]
+    lib.gdn_rms_norm_workspace_bytes.restype = Z
+    lib.gdn_rms_norm_fwd.argtypes = [np_] + [P] * 7
+    lib.gdn_rms_norm_fwd.restype = I
+    lib.gdn_rms_norm_bwd.argtypes = [np_] + [P] * 7 + [Z, P]
+    lib.gdn_rms_norm_bwd.restype = I
+    lib.gdn_step_maps.argtypes = [ctypes.POINTER(_StepMapsProblem)] + [P] * 7
+    lib.gdn_step_maps.restype = I
     lib.gdn_last_error.argtypes = []
     lib.gdn_last_error.restype = ctypes.c_char_p
     lib.gdn_abi_version.argtypes = []
@@ -507,7 +598,10 @@ def _native():
             raise OSError("_binding.so not loadable (%s): build it with `python -m gated_deltanet_fwd_amd.build`" % e)
         _binding.init(GdnError, *(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in
                                   ("gdn_recurrent", "gdn_conv_step", "gdn_qk_rope_fwd", "gdn_qk_rope_bwd",
-                                   "gdn_qk_rope_workspace_bytes", "gdn_last_error")))
+                                   "gdn_qk_rope_workspace_bytes", "gdn_last_error", "gdn_linear_fwd",
+                                   "gdn_linear_bwd", "gdn_linear_workspace_bytes", "gdn_linear_step",
+                                   "gdn_rms_norm_fwd", "gdn_rms_norm_bwd", "gdn_rms_norm_workspace_bytes",
+                                   "gdn_step_maps")))
         _marshal = _binding
     return _marshal
 
@@ -653,3 +747,153 @@ def gdn_qk_rope_bwd(p: QkRopeProblem, q, k, positions, freqs, dq_out, dk_out, q_
     dq, dk, dwq, dwk = _call("rope_bwd", dq_out, stream, p.at, q, k, positions, freqs, q_weight, k_weight, dq_out, dk_out,
                              g.get("dq"), g.get("dk"), g.get("dq_weight"), g.get("dk_weight"), workspace)
     return dict(dq=dq, dk=dk, dq_weight=dwq, dk_weight=dwk)
+
+
+# ------------------------------------------------------------------- linear attention with decays
+
+
+def _named(names, value, what) -> int:
+    if value not in names:
+        raise GdnError(GDN_EINVAL, "unknown %s %r" % (what, value))
+    return names[value]
+
+
+def _bytes(n: int) -> int:
+    if n == 0:
+        raise GdnError(GDN_EINVAL, load_library().gdn_last_error().decode())
+    return int(n)
+
+
+class LinearProblem:
+    """A gdn_linear_problem descriptor: linear attention with a log decay for each token and head
+    (decay "token": g is [T, h_v]) or for each head ("head": g is [h_v]) over packed documents."""
+
+    def __init__(self, cu_seqlens_host, h_qk: int, h_v: int, d: int, dtype=torch.bfloat16, scale: float = 1.0,
+                 decay: str = "token", has_h0: bool = False, want_ht: bool = False):
+        self.cu = np.ascontiguousarray(np.asarray(cu_seqlens_host, dtype=np.int32))
+        if self.cu.ndim != 1 or self.cu.shape[0] < 2:
+            raise GdnError(GDN_EINVAL, "cu_seqlens_host has shape %s, expected (N + 1,)" % (self.cu.shape,))
+        self.dtype = dtype
+        self.st = _LinearProblem(n_seqs=int(self.cu.shape[0] - 1), h_qk=int(h_qk), h_v=int(h_v), d=int(d),
+                                 n_tokens=int(self.cu[-1]), dtype=_io_dtype(dtype), decay=_named(DECAYS, decay, "decay"),
+                                 has_h0=int(bool(has_h0)), want_ht=int(bool(want_ht)), scale=float(scale),
+                                 cu_seqlens_host=self.cu.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)))
+        self.at = ctypes.addressof(self.st)
+
+    def ref(self):
+        return ctypes.byref(self.st)
+
+
+def gdn_linear_workspace_bytes(p: LinearProblem, op: int) -> int:
+    return _bytes(load_library().gdn_linear_workspace_bytes(p.ref(), int(op)))
+
+
+def gdn_linear_fwd(p: LinearProblem, q, k, v, g, cu_seqlens, h0=None, o=None, ht=None, workspace=None, stream=None):
+    """Linear attention with decays over packed documents: returns (o, ht or None). q, k and v may be parts
+    of one row (a token's heads contiguous)."""
+    return _call("linear_fwd", v, stream, p.at, q, k, v, g, cu_seqlens, h0, o, ht, workspace)
+
+
+def gdn_linear_bwd(p: LinearProblem, q, k, v, g, cu_seqlens, dO, h0=None, dht=None, want_dg: bool = True, grads=None,
+                   workspace=None, stream=None) -> Dict[str, torch.Tensor]:
+    """Its backward, from the forward's inputs: returns dict dq, dk, dv, dg (None unless wanted), dh0 (None
+    without h0). `grads` may name any of the buffers."""
+    b = grads or {}
+    dq, dk, dv, dg, dh0 = _call("linear_bwd", v, stream, p.at, q, k, v, g, cu_seqlens, h0, dO, dht, bool(want_dg),
+                                b.get("dq"), b.get("dk"), b.get("dv"), b.get("dg"), b.get("dh0"), workspace)
+    return dict(dq=dq, dk=dk, dv=dv, dg=dg, dh0=dh0)
+
+
+class LinearStepProblem:
+    """A gdn_linear_step_problem descriptor: `n_seqs` sequences on a cache of `n_slots` states, one token
+    each, or as many as the host copy of cu_seqlens says."""
+
+    def __init__(self, n_seqs: int, h_qk: int, h_v: int, d: int, n_slots: int, cu_seqlens_host=None,
+                 dtype=torch.bfloat16, scale: float = 1.0, decay: str = "token"):
+        self.cu, ptr, tokens = _step_lengths(cu_seqlens_host, n_seqs)
+        self.dtype = dtype
+        self.st = _LinearStepProblem(n_seqs=int(n_seqs), h_qk=int(h_qk), h_v=int(h_v), d=int(d), n_tokens=tokens,
+                                     dtype=_io_dtype(dtype), decay=_named(DECAYS, decay, "decay"), scale=float(scale),
+                                     n_slots=int(n_slots), cu_seqlens_host=ptr)
+        self.at = ctypes.addressof(self.st)
+
+    def ref(self):
+        return ctypes.byref(self.st)
+
+
+def gdn_linear_step(p: LinearStepProblem, q, k, v, g, states, slot_in, slot_out, slot_tok=None, cu_seqlens=None, o=None,
+                    stream=None):
+    """One serving step of linear attention with decays on cached states; slots, cu_seqlens, slot_tok and
+    rows of no sequence as in gdn_recurrent. Returns o; `states` is updated in place."""
+    return _call("linear_step", v, stream, p.at, q, k, v, g, states, slot_in, slot_out, slot_tok, cu_seqlens, o)
+
+
+# ------------------------------------------------------------------- RMS norm with the residual
+
+
+class RmsNormProblem:
+    """A gdn_rms_norm_problem descriptor: RMS norm of n_rows rows of d values, its output in the rows' type
+    (out "io") or in 8 bits with a scale a row or for each `group` values (out "e4m3")."""
+
+    def __init__(self, n_rows: int, d: int, dtype=torch.bfloat16, out: str = "io", group: int = 0, eps: float = 1e-6):
+        self.dtype = dtype
+        self.st = _RmsNormProblem(n_rows=int(n_rows), d=int(d), dtype=_io_dtype(dtype), out=_named(NORM_OUTS, out, "out"),
+                                  group=int(group), eps=float(eps))
+        self.at = ctypes.addressof(self.st)
+
+    def ref(self):
+        return ctypes.byref(self.st)
+
+
+def gdn_rms_norm_workspace_bytes(p: RmsNormProblem) -> int:
+    return _bytes(load_library().gdn_rms_norm_workspace_bytes(p.ref()))
+
+
+def gdn_rms_norm_fwd(p: RmsNormProblem, x, weight=None, residual=None, y=None, scales=None, residual_out=None,
+                     stream=None):
+    """RMS norm of the rows of x, or of x + residual: returns (y, scales or None, residual_out or None), with
+    y in torch.float8_e4m3fn and scales f32 [n_rows, d / group] where out is "e4m3". x and residual may be parts
+    of wider rows. Outputs of a short call share one storage, as those of gdn_conv_step."""
+    return _call("norm_fwd", x, stream, p.at, x, weight, residual, y, scales, residual_out)
+
+
+def gdn_rms_norm_bwd(p: RmsNormProblem, x, dy, weight=None, d_residual=None, grads=None, workspace=None,
+                     stream=None) -> Dict[str, torch.Tensor]:
+    """Its backward (out "io") at the normalised rows x (with a residual: the forward's residual_out), with the
+    gradient of residual_out in d_residual: returns dict dx (of x and residual alike), dweight (None without
+    weight). `grads` may name the buffers."""
+    b = grads or {}
+    dx, dw = _call("norm_bwd", x, stream, p.at, x, dy, weight, d_residual, b.get("dx"), b.get("dweight"), workspace)
+    return dict(dx=dx, dweight=dw)
+
+
+# ------------------------------------------------------------------- what a serving step reads
+
+
+class StepMapsProblem:
+    """A gdn_step_maps_problem descriptor: n_seqs requests, room for n_tokens new tokens, blocks of `block`
+    tokens, block tables of max_blocks columns, a free list of n_free entries."""
+
+    def __init__(self, n_seqs: int, n_tokens: int, block: int, max_blocks: int, n_free: int):
+        self.st = _StepMapsProblem(n_seqs=int(n_seqs), block=int(block), n_tokens=int(n_tokens),
+                                   max_blocks=int(max_blocks), n_free=int(n_free))
+        self.at = ctypes.addressof(self.st)
+
+    def ref(self):
+        return ctypes.byref(self.st)
+
+
+STEP_MAPS = ("cu_seqlens", "positions", "token_slots", "granted", "slot_in", "slot_out", "slot_tok")
+
+
+def gdn_step_maps(p: StepMapsProblem, lengths, contexts, block_table, free_list, free_count, contexts_out=None,
+                  free_count_out=None, outs=None, stream=None) -> Dict[str, torch.Tensor]:
+    """What a serving step reads, on the GPU (see gdn.h): returns dict cu_seqlens, positions, token_slots, granted,
+    slot_in, slot_out, slot_tok, contexts, free_count. block_table [n_seqs, max_blocks] takes the new blocks in place.
+    contexts and free_count move on in place unless contexts_out and free_count_out are given; `outs` may name the
+    other buffers. Outputs of a short call share one storage, as those of gdn_conv_step."""
+    b = outs or {}
+    r = _call("step_maps", lengths, stream, p.at, lengths, contexts, block_table, free_list, free_count,
+              *[b.get(n) for n in STEP_MAPS], contexts if contexts_out is None else contexts_out,
+              free_count if free_count_out is None else free_count_out)
+    return dict(zip(STEP_MAPS + ("contexts", "free_count"), r))

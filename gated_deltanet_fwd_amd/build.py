@@ -18,7 +18,8 @@ OUT = os.path.join(HERE, "libgdn.so")
 BINDING = os.path.join(HERE, "_binding.so")
 BUILD = os.path.join(HERE, "_build")
 SOURCES = ["gdn_fwd.hip", "gdn_bwd.hip", "gdn_api.cpp", "gdn_static.hip", "gdn_conv.hip", "gdn_conv_step.hip",
-           "gdn_recurrent.hip", "gdn_rope.hip"]
+           "gdn_recurrent.hip", "gdn_rope.hip", "gdn_linear.hip", "gdn_linear_step.hip", "gdn_norm.hip",
+           "gdn_maps.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950",

@@ -1399,3 +1399,489 @@ int gdn_qk_rope_bwd(const gdn_qk_rope_problem* p, const void* q, const void* k, 
 }
 
 } // extern "C"
+
+// ---------------------------------------------------------------------------------------------
+// Linear attention with a decay for each head
+
+namespace {
+
+// Log decays are read one by one, so a part of a longer tensor's tokens will do.
+int check_decays(const float* g, int decay, int64_t T) {
+  if (!g && (T > 0 || decay == GDN_DECAY_HEAD)) return fail(GDN_EINVAL, "g is NULL");
+  if ((uintptr_t)g & 3) return fail(GDN_EINVAL, "g is not 4-byte aligned");
+  return GDN_OK;
+}
+
+// What the kernels' 32-bit offsets inside 64 rows allow.
+constexpr int64_t LINEAR_ROW = (int64_t)1 << 22;
+
+int check_linear(const gdn_linear_problem* p) {
+  if (!p) return fail(GDN_EINVAL, "linear problem descriptor is NULL");
+  if (p->n_seqs < 1 || p->n_seqs > 65535) return fail(GDN_EINVAL, "n_seqs must be 1..65535 (got %d)", p->n_seqs);
+  if (p->h_qk < 1 || p->h_v < 1) return fail(GDN_EINVAL, "head counts must be >= 1");
+  if (p->h_v % p->h_qk != 0) return fail(GDN_EINVAL, "h_v (%d) must be a multiple of h_qk (%d)", p->h_v, p->h_qk);
+  if (p->d != 64 && p->d != 128) return fail(GDN_EUNSUPPORTED, "d must be 64 or 128 (got %d)", p->d);
+  if ((int64_t)p->h_v * p->d > LINEAR_ROW)
+    return fail(GDN_EINVAL, "h_v * d must be at most 2^22 (got %lld)", (long long)p->h_v * p->d);
+  if (p->dtype != GDN_DTYPE_BF16 && p->dtype != GDN_DTYPE_F32)
+    return fail(GDN_EUNSUPPORTED, "unsupported dtype %d", p->dtype);
+  if (p->decay != GDN_DECAY_TOKEN && p->decay != GDN_DECAY_HEAD) return fail(GDN_EINVAL, "decay must be token (0) or head (1)");
+  if (!std::isfinite(p->scale)) return fail(GDN_EINVAL, "scale must be finite");
+  if (p->reserved0 != 0) return fail(GDN_EINVAL, "reserved0 must be 0");
+  const int32_t* cu = p->cu_seqlens_host;
+  if (!cu) return fail(GDN_EINVAL, "cu_seqlens_host is NULL");
+  if (p->n_tokens > STEP_MOST) return fail(GDN_EINVAL, "too many tokens for one call (at most %lld)", (long long)STEP_MOST);
+  if (cu[0] != 0) return fail(GDN_EINVAL, "cu_seqlens[0] must be 0");
+  for (int n = 0; n < p->n_seqs; ++n)
+    if (cu[n + 1] < cu[n]) return fail(GDN_EINVAL, "cu_seqlens decreases at %d", n);
+  if ((int64_t)cu[p->n_seqs] != p->n_tokens)
+    return fail(GDN_EINVAL, "cu_seqlens[N] = %d but n_tokens = %lld", cu[p->n_seqs], (long long)p->n_tokens);
+  return GDN_OK;
+}
+
+// Tokens of a segment.
+int linear_segment(const gdn_linear_problem* p) {
+  constexpr int64_t GROUPS = 1024, SHORTEST = 256;
+  int longest = 0;
+  for (int n = 0; n < p->n_seqs; ++n) longest = std::max(longest, p->cu_seqlens_host[n + 1] - p->cu_seqlens_host[n]);
+  int64_t seg = std::max(p->n_tokens * p->h_v / GROUPS, SHORTEST);
+  seg = (seg + kChunk - 1) / kChunk * kChunk;
+  return longest <= seg + seg / 2 ? 0 : (int)seg;
+}
+
+struct LinearLayout {
+  int seg, slots;
+  size_t S, D, Sdecay, Ddecay, qdots, kdots, sums, part, total;
+};
+
+int linear_layout(const gdn_linear_problem* p, int op, LinearLayout* L) {
+  *L = {};
+  L->seg = linear_segment(p);
+  const int64_t slots = L->seg ? p->n_tokens / L->seg + p->n_seqs : p->n_seqs;
+  if (slots * p->h_v > (int64_t)0x0fffffff) return fail(GDN_EINVAL, "too many segments x heads");
+  L->slots = (int)slots;
+  size_t off = 0;
+  const auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align_up(off + bytes);
+    return at;
+  };
+  const size_t states = (size_t)slots * p->h_v * p->d * p->d * 4, rows = (size_t)p->n_tokens * p->h_v * 4;
+  if (L->seg) {
+    L->S = take(states);
+    L->Sdecay = take((size_t)slots * p->h_v * 4);
+  }
+  if (op == GDN_OP_BWD) {
+    if (L->seg) {
+      L->D = take(states);
+      L->Ddecay = take((size_t)slots * p->h_v * 4);
+    }
+    L->qdots = take(rows);
+    L->kdots = take(rows);
+    L->sums = take((size_t)slots * p->h_v * 8);
+    if (p->h_v != p->h_qk) L->part = take(rows * p->d);
+  }
+  L->total = std::max(off, kAlign);
+  return GDN_OK;
+}
+
+// Sizes, decays and the operands' strides of a call.
+struct LinearCall {
+  gdn::LinearArgs base;
+  gdn::LinearSide q, k, v;
+};
+int linear_call(LinearCall* c, const LinearLayout& L, const gdn_linear_problem* p, const void* q, const void* k, const void* v,
+                const float* g, const int32_t* cu) {
+  std::memset(c, 0, sizeof *c);
+  const int64_t T = p->n_tokens;
+  CHECK(check_tok(q, "q", T));
+  CHECK(check_tok(k, "k", T));
+  CHECK(check_tok(v, "v", T));
+  CHECK(check_decays(g, p->decay, T));
+  CHECK(check_ptr(cu, "cu_seqlens"));
+  CHECK(token_stride(p->q_stride, (int64_t)p->h_qk * p->d, p->dtype, "q_stride", &c->q.stride));
+  CHECK(token_stride(p->k_stride, (int64_t)p->h_qk * p->d, p->dtype, "k_stride", &c->k.stride));
+  CHECK(token_stride(p->v_stride, (int64_t)p->h_v * p->d, p->dtype, "v_stride", &c->v.stride));
+  if (std::max(std::max(c->q.stride, c->k.stride), c->v.stride) > LINEAR_ROW)
+    return fail(GDN_EINVAL, "token strides must be at most 2^22 elements");
+  c->q.p = q;
+  c->k.p = k;
+  c->v.p = v;
+  c->q.shared = c->k.shared = 1;
+  gdn::LinearArgs& a = c->base;
+  a.T = (int)T;
+  a.N = p->n_seqs;
+  a.H = p->h_qk;
+  a.HV = p->h_v;
+  a.G = p->h_v / p->h_qk;
+  a.D = p->d;
+  a.seg = L.seg;
+  a.slots = L.slots;
+  a.gs = p->decay == GDN_DECAY_TOKEN ? p->h_v : 0;
+  a.g = g;
+  a.cu = cu;
+  a.p_scale = a.in_scale = a.w_scale = 1.f;
+  return GDN_OK;
+}
+
+int check_linear_workspace(const LinearLayout& L, const void* workspace, size_t bytes) {
+  CHECK(check_ptr(workspace, "workspace"));
+  if (bytes < L.total) return fail(GDN_EWORKSPACE, "workspace has %zu bytes, needs %zu", bytes, L.total);
+  return GDN_OK;
+}
+
+} // namespace
+
+extern "C" {
+
+size_t gdn_linear_workspace_bytes(const gdn_linear_problem* p, int op) {
+  if (check_linear(p) != GDN_OK) return 0;
+  if (op != GDN_OP_FWD && op != GDN_OP_BWD) {
+    fail(GDN_EINVAL, "unknown op %d", op);
+    return 0;
+  }
+  LinearLayout L;
+  return linear_layout(p, op, &L) == GDN_OK ? L.total : 0;
+}
+
+int gdn_linear_fwd(const gdn_linear_problem* p, const void* q, const void* k, const void* v, const float* g,
+                   const int32_t* cu_seqlens, const float* h0, void* o, float* ht, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+  CHECK(check_linear(p));
+  LinearLayout L;
+  CHECK(linear_layout(p, GDN_OP_FWD, &L));
+  LinearCall c;
+  CHECK(linear_call(&c, L, p, q, k, v, g, cu_seqlens));
+  if ((h0 != nullptr) != (p->has_h0 != 0)) return fail(GDN_EINVAL, "h0 must be given iff has_h0");
+  if ((ht != nullptr) != (p->want_ht != 0)) return fail(GDN_EINVAL, "ht must be given iff want_ht");
+  if (h0) CHECK(check_ptr(h0, "h0"));
+  if (ht) CHECK(check_ptr(ht, "ht"));
+  CHECK(check_tok(o, "o", p->n_tokens));
+  CHECK(check_linear_workspace(L, workspace, workspace_bytes));
+  char* w = (char*)workspace;
+  gdn::LinearArgs a = c.base;
+  a.a = c.q;
+  a.b = c.k;
+  a.c = c.v;
+  a.init = h0;
+  a.states = (float*)(w + L.S);
+  a.decay = (float*)(w + L.Sdecay);
+  if (L.seg) {
+    LAUNCH("gdn_linear_states", gdn::launch_linear_states(a, false, p->dtype, stream));
+    LAUNCH("gdn_linear_scan", gdn::launch_linear_scan(a, false, stream));
+  }
+  a.p_scale = a.in_scale = p->scale;
+  a.fin = ht;
+  a.out = o;
+  LAUNCH("gdn_linear_walk", gdn::launch_linear_walk(a, false, p->dtype, stream));
+  g_err.clear();
+  return GDN_OK;
+}
+
+int gdn_linear_bwd(const gdn_linear_problem* p, const void* q, const void* k, const void* v, const float* g,
+                   const int32_t* cu_seqlens, const float* h0, const void* dO, const float* dht, void* dq, void* dk,
+                   void* dv, float* dg, float* dh0, void* workspace, size_t workspace_bytes, void* stream) {
+  CHECK(check_linear(p));
+  LinearLayout L;
+  CHECK(linear_layout(p, GDN_OP_BWD, &L));
+  LinearCall c;
+  CHECK(linear_call(&c, L, p, q, k, v, g, cu_seqlens));
+  const int64_t T = p->n_tokens;
+  if ((h0 != nullptr) != (p->has_h0 != 0)) return fail(GDN_EINVAL, "h0 must be given iff has_h0");
+  if ((dh0 != nullptr) != (p->has_h0 != 0)) return fail(GDN_EINVAL, "dh0 must be given iff has_h0");
+  if (h0) CHECK(check_ptr(h0, "h0"));
+  if (dh0) CHECK(check_ptr(dh0, "dh0"));
+  if (dht) CHECK(check_ptr(dht, "dht"));
+  if (dg) CHECK(check_ptr(dg, "dg"));
+  CHECK(check_tok(dO, "dO", T));
+  CHECK(check_tok(dq, "dq", T));
+  CHECK(check_tok(dk, "dk", T));
+  CHECK(check_tok(dv, "dv", T));
+  CHECK(check_linear_workspace(L, workspace, workspace_bytes));
+  char* w = (char*)workspace;
+  const int dt = p->dtype;
+  const gdn::LinearSide d_out = {dO, (int64_t)p->h_v * p->d, 0};
+  float* part = p->h_v != p->h_qk ? (float*)(w + L.part) : nullptr;
+  gdn::LinearArgs f = c.base, r = c.base; // forward and in reverse
+  f.init = h0;
+  f.states = (float*)(w + L.S);
+  f.decay = (float*)(w + L.Sdecay);
+  r.init = dht;
+  r.states = (float*)(w + L.D);
+  r.decay = (float*)(w + L.Ddecay);
+  r.w_scale = p->scale;
+  if (L.seg) {
+    f.b = c.k;
+    f.c = c.v;
+    LAUNCH("gdn_linear_states", gdn::launch_linear_states(f, false, dt, stream));
+    r.b = c.q;
+    r.c = d_out;
+    LAUNCH("gdn_linear_states", gdn::launch_linear_states(r, true, dt, stream));
+    LAUNCH("gdn_linear_scan", gdn::launch_linear_scan(f, false, stream));
+    LAUNCH("gdn_linear_scan", gdn::launch_linear_scan(r, true, stream));
+  }
+  // dq
+  gdn::LinearArgs a = f;
+  a.a = d_out;
+  a.b = c.v;
+  a.c = c.k;
+  a.flip = 1;
+  a.p_scale = a.in_scale = p->scale;
+  a.out = dq;
+  a.part = part;
+  if (dg) {
+    a.dot = c.q;
+    a.dots = (float*)(w + L.qdots);
+  }
+  LAUNCH("gdn_linear_walk", gdn::launch_linear_walk(a, false, dt, stream));
+  if (part) LAUNCH("gdn_linear_group_sum", gdn::launch_linear_group_sum(a, dt, stream));
+  // dk
+  a = r;
+  a.a = c.v;
+  a.b = d_out;
+  a.c = c.q;
+  a.flip = 1;
+  a.p_scale = p->scale;
+  a.out = dk;
+  a.part = part;
+  if (dg) {
+    a.dot = c.k;
+    a.dots = (float*)(w + L.kdots);
+  }
+  LAUNCH("gdn_linear_walk", gdn::launch_linear_walk(a, true, dt, stream));
+  if (part) LAUNCH("gdn_linear_group_sum", gdn::launch_linear_group_sum(a, dt, stream));
+  // dv and dh0
+  a = r;
+  a.a = c.k;
+  a.b = c.q;
+  a.c = d_out;
+  a.p_scale = p->scale;
+  a.out = dv;
+  a.fin = dh0;
+  LAUNCH("gdn_linear_walk", gdn::launch_linear_walk(a, true, dt, stream));
+  if (dg) {
+    gdn::LinearDgArgs d;
+    std::memset(&d, 0, sizeof d);
+    d.a = c.base;
+    d.S = (const float*)(w + L.S);
+    d.D = (const float*)(w + L.D);
+    d.h0 = h0;
+    d.dh0 = dh0;
+    d.dht = dht;
+    d.qdots = (const float*)(w + L.qdots);
+    d.kdots = (const float*)(w + L.kdots);
+    d.sums = (double*)(w + L.sums);
+    d.dg = dg;
+    LAUNCH("gdn_linear_dg", gdn::launch_linear_dg(d, stream));
+  }
+  g_err.clear();
+  return GDN_OK;
+}
+
+int gdn_linear_step(const gdn_linear_step_problem* p, const void* q, const void* k, const void* v, const float* g,
+                    const int32_t* cu_seqlens, const int32_t* slot_in, const int32_t* slot_out, const int32_t* slot_tok,
+                    float* states, void* o, void* stream) {
+  if (!p) return fail(GDN_EINVAL, "linear step problem descriptor is NULL");
+  if (p->h_qk < 1 || p->h_v < 1) return fail(GDN_EINVAL, "head counts must be >= 1");
+  if (p->h_v % p->h_qk != 0) return fail(GDN_EINVAL, "h_v (%d) must be a multiple of h_qk (%d)", p->h_v, p->h_qk);
+  if (p->d != 64 && p->d != 128) return fail(GDN_EUNSUPPORTED, "d must be 64 or 128 (got %d)", p->d);
+  if (p->dtype != GDN_DTYPE_BF16 && p->dtype != GDN_DTYPE_F32)
+    return fail(GDN_EUNSUPPORTED, "unsupported dtype %d", p->dtype);
+  if (p->decay != GDN_DECAY_TOKEN && p->decay != GDN_DECAY_HEAD) return fail(GDN_EINVAL, "decay must be token (0) or head (1)");
+  if (!std::isfinite(p->scale)) return fail(GDN_EINVAL, "scale must be finite");
+  CHECK(check_steps(p->n_seqs, p->n_tokens, p->n_slots, p->reserved0, p->cu_seqlens_host));
+  if ((int64_t)p->n_seqs * p->h_v > (int64_t)0x0fffffff) return fail(GDN_EINVAL, "too many sequences x heads");
+  if (p->h_v > 65536) return fail(GDN_EINVAL, "h_v must be at most 65536 (got %d)", p->h_v);
+  gdn::LinearStepArgs a;
+  std::memset(&a, 0, sizeof a);
+  CHECK(token_stride(p->q_stride, (int64_t)p->h_qk * p->d, p->dtype, "q_stride", &a.qs));
+  CHECK(token_stride(p->k_stride, (int64_t)p->h_qk * p->d, p->dtype, "k_stride", &a.ks));
+  CHECK(token_stride(p->v_stride, (int64_t)p->h_v * p->d, p->dtype, "v_stride", &a.vs));
+  if (std::max(std::max(a.qs, a.ks), a.vs) > (int64_t)1 << 24) return fail(GDN_EINVAL, "token strides must be at most 2^24 elements");
+  const int64_t T = p->n_tokens;
+  CHECK(check_tok(q, "q", T));
+  CHECK(check_tok(k, "k", T));
+  CHECK(check_tok(v, "v", T));
+  CHECK(check_decays(g, p->decay, T));
+  CHECK(check_tok(o, "o", T));
+  CHECK(check_ptr(states, "states"));
+  CHECK(check_step_arrays(p->cu_seqlens_host, cu_seqlens, slot_in, slot_out, slot_tok));
+  a.T = (int)T;
+  a.N = p->n_seqs;
+  a.HV = p->h_v;
+  a.g_mul = ((uint64_t)1 << 32) / (p->h_v / p->h_qk) + 1;
+  a.D = p->d;
+  a.n_slots = p->n_slots;
+  a.gs = p->decay == GDN_DECAY_TOKEN ? p->h_v : 0;
+  a.scale = p->scale;
+  a.longest = 1;
+  a.live = p->n_seqs;
+  if (p->cu_seqlens_host) {
+    a.live = 0;
+    for (int n = 0; n < p->n_seqs; ++n) {
+      const int len = p->cu_seqlens_host[n + 1] - p->cu_seqlens_host[n];
+      a.longest = std::max(a.longest, len);
+      a.live += len > 0;
+    }
+  }
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.g = g;
+  a.cu = cu_seqlens;
+  a.slot_in = slot_in;
+  a.slot_out = slot_out;
+  a.slot_tok = slot_tok;
+  a.states = states;
+  a.o = o;
+  LAUNCH("gdn_linear_step", gdn::launch_linear_step(a, p->dtype, stream));
+  g_err.clear();
+  return GDN_OK;
+}
+
+} // extern "C"
+
+// ---------------------------------------------------------------------------------------------
+// RMS norm of rows; a serving step's maps
+
+namespace {
+
+int check_norm(const gdn_rms_norm_problem* p) {
+  if (!p) return fail(GDN_EINVAL, "rms norm problem descriptor is NULL");
+  if (p->n_rows < 0 || p->n_rows > STEP_MOST) return fail(GDN_EINVAL, "n_rows must be 0..%lld", (long long)STEP_MOST);
+  if (p->d < 8 || p->d > 16384 || p->d % 8 != 0)
+    return fail(GDN_EUNSUPPORTED, "d must be a multiple of 8, 8..16384 (got %d)", p->d);
+  if (p->dtype != GDN_DTYPE_BF16 && p->dtype != GDN_DTYPE_F32)
+    return fail(GDN_EUNSUPPORTED, "unsupported dtype %d", p->dtype);
+  if (p->out != GDN_OUT_IO && p->out != GDN_OUT_E4M3) return fail(GDN_EINVAL, "out must be io (0) or e4m3 (1)");
+  if (p->group != 0 && p->group != 32 && p->group != 64 && p->group != 128)
+    return fail(GDN_EINVAL, "group must be 0 (a row), 32, 64 or 128 (got %d)", p->group);
+  if (p->group != 0 && p->out != GDN_OUT_E4M3) return fail(GDN_EINVAL, "a group needs out = e4m3");
+  if (p->group != 0 && p->d % p->group != 0) return fail(GDN_EINVAL, "d (%d) must be a multiple of group (%d)", p->d, p->group);
+  if (!(p->eps >= 0.f) || !std::isfinite(p->eps)) return fail(GDN_EINVAL, "eps must be >= 0");
+  if (p->reserved0 != 0) return fail(GDN_EINVAL, "reserved0 must be 0");
+  return GDN_OK;
+}
+
+int norm_args(gdn::NormArgs& a, const gdn_rms_norm_problem* p, const float* weight) {
+  std::memset(&a, 0, sizeof a);
+  CHECK(check_norm(p));
+  if (weight) CHECK(check_ptr(weight, "weight"));
+  a.rows = p->n_rows;
+  a.D = p->d;
+  a.e4m3 = p->out == GDN_OUT_E4M3;
+  a.group = p->group ? p->group : p->d;
+  a.eps = p->eps;
+  a.w = weight;
+  CHECK(token_stride(p->x_stride, p->d, p->dtype, "x_stride", &a.xs));
+  CHECK(token_stride(p->residual_stride, p->d, p->dtype, "residual_stride", &a.rs));
+  return GDN_OK;
+}
+
+} // namespace
+
+extern "C" {
+
+size_t gdn_rms_norm_workspace_bytes(const gdn_rms_norm_problem* p) {
+  gdn::NormArgs a;
+  if (norm_args(a, p, nullptr) != GDN_OK) return 0;
+  return align_up((size_t)std::max(gdn::norm_blocks(a), 1) * a.D * 4);
+}
+
+int gdn_rms_norm_fwd(const gdn_rms_norm_problem* p, const void* x, const float* weight, const void* residual, void* y,
+                     float* scales, void* residual_out, void* stream) {
+  gdn::NormArgs a;
+  CHECK(norm_args(a, p, weight));
+  CHECK(check_tok(x, "x", p->n_rows));
+  CHECK(check_tok(y, "y", p->n_rows));
+  if (a.e4m3) CHECK(check_tok(scales, "scales", p->n_rows));
+  else if (scales) return fail(GDN_EINVAL, "scales are of out = e4m3");
+  if (p->n_rows > 0 && (residual != nullptr) != (residual_out != nullptr))
+    return fail(GDN_EINVAL, "residual and residual_out must be given together");
+  if (residual) CHECK(check_ptr(residual, "residual"));
+  if (residual_out) CHECK(check_ptr(residual_out, "residual_out"));
+  a.x = x;
+  a.res = residual;
+  a.y = y;
+  a.ys = a.os = p->d;
+  a.scales = scales;
+  a.out = residual_out;
+  LAUNCH("gdn_rms_norm_fwd", gdn::launch_norm_fwd(a, p->dtype, stream));
+  g_err.clear();
+  return GDN_OK;
+}
+
+int gdn_rms_norm_bwd(const gdn_rms_norm_problem* p, const void* x, const float* weight, const void* dy,
+                     const void* d_residual, void* dx, float* dweight, void* workspace, size_t workspace_bytes, void* stream) {
+  gdn::NormArgs a;
+  CHECK(norm_args(a, p, weight));
+  if (a.e4m3) return fail(GDN_EUNSUPPORTED, "the backward is of out = io");
+  CHECK(check_tok(x, "x", p->n_rows));
+  CHECK(check_tok(dy, "dy", p->n_rows));
+  CHECK(check_tok(dx, "dx", p->n_rows));
+  if (d_residual) CHECK(check_ptr(d_residual, "d_residual"));
+  if (dweight) {
+    if (!weight) return fail(GDN_EINVAL, "dweight is given without weight");
+    CHECK(check_ptr(dweight, "dweight"));
+    CHECK(check_ptr(workspace, "workspace"));
+    const size_t need = align_up((size_t)std::max(gdn::norm_blocks(a), 1) * a.D * 4);
+    if (workspace_bytes < need) return fail(GDN_EWORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+  }
+  a.x = x;
+  a.dy = dy;
+  a.ys = a.os = p->d;
+  a.res = d_residual;
+  a.out = dx;
+  a.dw = dweight;
+  a.part = (float*)workspace;
+  LAUNCH("gdn_rms_norm_bwd", gdn::launch_norm_bwd(a, p->dtype, stream));
+  g_err.clear();
+  return GDN_OK;
+}
+
+int gdn_step_maps(const gdn_step_maps_problem* p, const int32_t* lengths, const int32_t* contexts, int32_t* block_table,
+                  const int32_t* free_list, const int32_t* free_count, const gdn_step_maps_out* out, void* stream) {
+  if (!p) return fail(GDN_EINVAL, "step maps problem descriptor is NULL");
+  if (!out) return fail(GDN_EINVAL, "step maps outputs are NULL");
+  if (p->n_seqs < 1 || p->n_seqs > 4096) return fail(GDN_EINVAL, "n_seqs must be 1..4096 (got %d)", p->n_seqs);
+  if (p->n_tokens < 0 || p->n_tokens > STEP_MOST) return fail(GDN_EINVAL, "n_tokens must be 0..%lld", (long long)STEP_MOST);
+  if (p->block < 1) return fail(GDN_EINVAL, "block must be >= 1 (got %d)", p->block);
+  if (p->max_blocks < 1) return fail(GDN_EINVAL, "max_blocks must be >= 1 (got %d)", p->max_blocks);
+  if (p->n_free < 0) return fail(GDN_EINVAL, "n_free must be >= 0 (got %d)", p->n_free);
+  if (p->reserved0 != 0) return fail(GDN_EINVAL, "reserved0 must be 0");
+  CHECK(check_ptr(lengths, "lengths"));
+  CHECK(check_ptr(contexts, "contexts"));
+  CHECK(check_ptr(block_table, "block_table"));
+  CHECK(check_tok(free_list, "free_list", p->n_free));
+  CHECK(check_ptr(free_count, "free_count"));
+  const void* given[] = {out->cu_seqlens, out->positions, out->token_slots, out->granted, out->slot_in,
+                         out->slot_out,   out->slot_tok,  out->contexts,    out->free_count};
+  for (const void* x : given)
+    if (x && !aligned16(x)) return fail(GDN_EINVAL, "an output is not 16-byte aligned");
+  gdn::MapsArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.N = p->n_seqs;
+  a.T = (int)p->n_tokens;
+  a.block = p->block;
+  a.max_blocks = p->max_blocks;
+  a.n_free = p->n_free;
+  a.lengths = lengths;
+  a.contexts = contexts;
+  a.table = block_table;
+  a.free_list = free_list;
+  a.free_count = free_count;
+  a.cu = out->cu_seqlens;
+  a.positions = out->positions;
+  a.token_slots = out->token_slots;
+  a.granted = out->granted;
+  a.slot_in = out->slot_in;
+  a.slot_out = out->slot_out;
+  a.slot_tok = out->slot_tok;
+  a.contexts_out = out->contexts;
+  a.free_count_out = out->free_count;
+  LAUNCH("gdn_step_maps", gdn::launch_maps(a, stream));
+  g_err.clear();
+  return GDN_OK;
+}
+
+} // extern "C"

@@ -1,4 +1,4 @@
-// Python side of the serving steps and of the q/k norms and rotation: checks the tensors, allocates
+// Python side of the serving steps, the norms with rotation and residual, linear attention and a step's maps: checks the tensors, allocates
 // the outputs and calls the C ABI (include/gdn.h). These calls are short (a decoding step takes a few
 // microseconds on the GPU), so their argument marshalling is native: a step's host time is 4 to 6 us
 // instead of 10 to 16 us with the same checks written in Python.
@@ -15,7 +15,9 @@
 
 #include <cstdarg>
 #include <cstdio>
+#include <cstring>
 #include <exception>
+#include <optional>
 
 #include "gdn.h"
 
@@ -31,7 +33,16 @@ struct Entries {
   decltype(&gdn_qk_rope_bwd) rope_bwd;
   decltype(&gdn_qk_rope_workspace_bytes) rope_workspace;
   decltype(&gdn_last_error) last_error;
+  decltype(&gdn_linear_fwd) linear_fwd;
+  decltype(&gdn_linear_bwd) linear_bwd;
+  decltype(&gdn_linear_workspace_bytes) linear_workspace;
+  decltype(&gdn_linear_step) linear_step;
+  decltype(&gdn_rms_norm_fwd) norm_fwd;
+  decltype(&gdn_rms_norm_bwd) norm_bwd;
+  decltype(&gdn_rms_norm_workspace_bytes) norm_workspace;
+  decltype(&gdn_step_maps) step_maps;
 } g_lib;
+constexpr int ENTRIES = sizeof(Entries) / sizeof(void*);
 PyObject* g_error = nullptr; // the package's GdnError
 
 struct Raised {}; // a Python exception is set
@@ -145,7 +156,7 @@ class Buffers {
     int64_t from; // bytes
   };
   at::Device dev_;
-  Want wants_[5];
+  Want wants_[10];
   int n_ = 0;
   int64_t total_ = 0;
 };
@@ -341,14 +352,235 @@ PyObject* rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// init(GdnError, addresses of recurrent, conv_step, rope_fwd, rope_bwd, rope_workspace, last_error)
+// The problem's workspace: `given`, or one of the size that `bytes` names, among the call's buffers.
+struct Workspace {
+  Tensor t;
+  size_t bytes = 0;
+  template <typename F>
+  Workspace(PyObject* given, const at::Device& dev, Buffers& made, F needed) {
+    if (given != Py_None) {
+      t = tensor(given, "workspace");
+      bytes = (size_t)t.numel();
+      expect(t, "workspace", {t.numel()}, at::kByte, dev);
+      return;
+    }
+    bytes = needed();
+    if (!bytes) raise(GDN_EINVAL, g_lib.last_error());
+    made.want(t, {(int64_t)bytes}, at::kByte);
+  }
+};
+
+// What both directions of linear attention read, with the strides put into the problem.
+struct LinearInputs {
+  void *q, *k, *v;
+  const float *g, *h0;
+  const int32_t* cu;
+  LinearInputs(gdn_linear_problem& p, PyObject* const* a, const at::Device& dev) {
+    const at::ScalarType io = io_type(p.dtype);
+    const int64_t T = p.n_tokens, N = p.n_seqs;
+    const int64_t qs[] = {T, p.h_qk, p.d}, vs[] = {T, p.h_v, p.d}, ss[] = {N, p.h_v, p.d, p.d}, gs[] = {T, p.h_v};
+    q = expect(tensor(a[0], "q"), "q", qs, io, dev, &p.q_stride);
+    k = expect(tensor(a[1], "k"), "k", qs, io, dev, &p.k_stride);
+    v = expect(tensor(a[2], "v"), "v", vs, io, dev, &p.v_stride);
+    const at::IntArrayRef shape = p.decay == GDN_DECAY_HEAD ? at::IntArrayRef(gs + 1, 1) : at::IntArrayRef(gs);
+    g = (float*)expect(tensor(a[3], "g"), "g", shape, at::kFloat, dev);
+    cu = (int32_t*)expect(tensor(a[4], "cu_seqlens"), "cu_seqlens", {N + 1}, at::kInt, dev);
+    h0 = optional<float>(a[5], "h0", ss, at::kFloat, dev);
+    if ((h0 != nullptr) != (p.has_h0 != 0)) refuse("h0 must be given iff has_h0");
+  }
+};
+
+// linear_fwd(problem, q, k, v, g, cu_seqlens, h0, o, ht, workspace) -> (o, ht)
+PyObject* linear_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    count(n, 10);
+    gdn_linear_problem p = problem<gdn_linear_problem>(a[0]);
+    const at::Device dev = gpu_of(tensor(a[3], "v"), "v");
+    const c10::DeviceGuard guard(dev);
+    const LinearInputs in(p, a + 1, dev);
+    const int64_t vs[] = {p.n_tokens, p.h_v, p.d}, ss[] = {p.n_seqs, p.h_v, p.d, p.d};
+    Tensor o, ht;
+    Buffers made(dev);
+    made.want(o, a[7], "o", vs, io_type(p.dtype));
+    if (p.want_ht) made.want(ht, a[8], "ht", ss, at::kFloat);
+    else if (a[8] != Py_None) refuse("ht is given but want_ht is not set");
+    Workspace ws(a[9], dev, made, [&] { return g_lib.linear_workspace(&p, GDN_OP_FWD); });
+    made.allocate();
+    void* op = expect(o, "o", vs, io_type(p.dtype), dev);
+    float* htp = p.want_ht ? (float*)expect(ht, "ht", ss, at::kFloat, dev) : nullptr;
+    check(g_lib.linear_fwd(&p, in.q, in.k, in.v, in.g, in.cu, in.h0, op, htp, ws.t.data_ptr(), ws.bytes, stream_of(dev)));
+    return Py_BuildValue("NN", THPVariable_Wrap(o), wrap_or_none(ht));
+  });
+}
+
+// linear_bwd(problem, q, k, v, g, cu_seqlens, h0, dO, dht, want_dg, dq, dk, dv, dg, dh0, workspace) -> (dq, dk, dv, dg, dh0)
+PyObject* linear_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    count(n, 16);
+    gdn_linear_problem p = problem<gdn_linear_problem>(a[0]);
+    const at::Device dev = gpu_of(tensor(a[3], "v"), "v");
+    const c10::DeviceGuard guard(dev);
+    const LinearInputs in(p, a + 1, dev);
+    const at::ScalarType io = io_type(p.dtype);
+    const int64_t qs[] = {p.n_tokens, p.h_qk, p.d}, vs[] = {p.n_tokens, p.h_v, p.d}, ss[] = {p.n_seqs, p.h_v, p.d, p.d};
+    const int64_t gs[] = {p.n_tokens, p.h_v};
+    const at::IntArrayRef gshape = p.decay == GDN_DECAY_HEAD ? at::IntArrayRef(gs + 1, 1) : at::IntArrayRef(gs);
+    void* dop = expect(tensor(a[7], "dO"), "dO", vs, io, dev);
+    const float* dht = optional<float>(a[8], "dht", ss, at::kFloat, dev);
+    const bool with_g = a[9] == Py_True;
+    if (!with_g && a[13] != Py_None) refuse("dg is given but not wanted");
+    if (!p.has_h0 && a[14] != Py_None) refuse("dh0 is given but has_h0 is not set");
+    Tensor dq, dk, dv, dg, dh0;
+    Buffers made(dev);
+    made.want(dq, a[10], "dq", qs, io);
+    made.want(dk, a[11], "dk", qs, io);
+    made.want(dv, a[12], "dv", vs, io);
+    if (with_g) made.want(dg, a[13], "dg", gshape, at::kFloat);
+    if (p.has_h0) made.want(dh0, a[14], "dh0", ss, at::kFloat);
+    Workspace ws(a[15], dev, made, [&] { return g_lib.linear_workspace(&p, GDN_OP_BWD); });
+    made.allocate();
+    void* dqp = expect(dq, "dq", qs, io, dev);
+    void* dkp = expect(dk, "dk", qs, io, dev);
+    void* dvp = expect(dv, "dv", vs, io, dev);
+    float* dgp = with_g ? (float*)expect(dg, "dg", gshape, at::kFloat, dev) : nullptr;
+    float* dh0p = p.has_h0 ? (float*)expect(dh0, "dh0", ss, at::kFloat, dev) : nullptr;
+    check(g_lib.linear_bwd(&p, in.q, in.k, in.v, in.g, in.cu, in.h0, dop, dht, dqp, dkp, dvp, dgp, dh0p, ws.t.data_ptr(),
+                           ws.bytes, stream_of(dev)));
+    return Py_BuildValue("NNNNN", THPVariable_Wrap(dq), THPVariable_Wrap(dk), THPVariable_Wrap(dv), wrap_or_none(dg),
+                         wrap_or_none(dh0));
+  });
+}
+
+// linear_step(problem, q, k, v, g, states, slot_in, slot_out, slot_tok, cu_seqlens, o) -> o
+PyObject* linear_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    count(n, 11);
+    gdn_linear_step_problem p = problem<gdn_linear_step_problem>(a[0]);
+    const Tensor& v = tensor(a[3], "v");
+    const at::Device dev = gpu_of(v, "v");
+    const c10::DeviceGuard guard(dev);
+    const at::ScalarType io = io_type(p.dtype);
+    const int64_t T = p.n_tokens, N = p.n_seqs;
+    const int64_t qs[] = {T, p.h_qk, p.d}, vs[] = {T, p.h_v, p.d}, gs[] = {T, p.h_v}, ss[] = {p.n_slots, p.h_v, p.d, p.d};
+    const at::IntArrayRef gshape = p.decay == GDN_DECAY_HEAD ? at::IntArrayRef(gs + 1, 1) : at::IntArrayRef(gs);
+    void* vp = expect(v, "v", vs, io, dev, &p.v_stride);
+    void* qp = expect(tensor(a[1], "q"), "q", qs, io, dev, &p.q_stride);
+    void* kp = expect(tensor(a[2], "k"), "k", qs, io, dev, &p.k_stride);
+    void* gp = expect(tensor(a[4], "g"), "g", gshape, at::kFloat, dev);
+    void* sp = expect(tensor(a[5], "states"), "states", ss, at::kFloat, dev);
+    void* in = expect(tensor(a[6], "slot_in"), "slot_in", {N}, at::kInt, dev);
+    void* out = expect(tensor(a[7], "slot_out"), "slot_out", {N}, at::kInt, dev);
+    const int32_t* tok = optional<int32_t>(a[8], "slot_tok", {T}, at::kInt, dev);
+    const int32_t* cu = optional<int32_t>(a[9], "cu_seqlens", {N + 1}, at::kInt, dev);
+    const Tensor o = a[10] == Py_None ? empty(vs, io, dev) : tensor(a[10], "o");
+    void* op = expect(o, "o", vs, io, dev);
+    check(g_lib.linear_step(&p, qp, kp, vp, (float*)gp, cu, (int32_t*)in, (int32_t*)out, tok, (float*)sp, op, stream_of(dev)));
+    return THPVariable_Wrap(o);
+  });
+}
+
+// norm_fwd(problem, x, weight, residual, y, scales, residual_out) -> (y, scales, residual_out)
+PyObject* norm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    count(n, 7);
+    gdn_rms_norm_problem p = problem<gdn_rms_norm_problem>(a[0]);
+    const Tensor& x = tensor(a[1], "x");
+    const at::Device dev = gpu_of(x, "x");
+    const c10::DeviceGuard guard(dev);
+    const at::ScalarType io = io_type(p.dtype), yt = p.out == GDN_OUT_E4M3 ? at::kFloat8_e4m3fn : io;
+    if (p.d < 1 || p.group < 0 || p.n_rows < 0) refuse("d must be >= 1, group and n_rows >= 0");
+    const int64_t xs[] = {p.n_rows, p.d}, ss[] = {p.n_rows, p.group ? p.d / p.group : 1};
+    void* xp = expect(x, "x", xs, io, dev, &p.x_stride);
+    const float* w = optional<float>(a[2], "weight", {p.d}, at::kFloat, dev);
+    void* res = a[3] == Py_None ? nullptr : expect(tensor(a[3], "residual"), "residual", xs, io, dev, &p.residual_stride);
+    const bool with_res = a[3] != Py_None, scaled = p.out == GDN_OUT_E4M3;
+    if (!scaled && a[5] != Py_None) refuse("scales are given but out is not e4m3");
+    if (!with_res && a[6] != Py_None) refuse("residual_out is given without residual");
+    Tensor y, scales, out;
+    Buffers made(dev);
+    made.want(y, a[4], "y", xs, yt);
+    if (scaled) made.want(scales, a[5], "scales", ss, at::kFloat);
+    if (with_res) made.want(out, a[6], "residual_out", xs, io);
+    made.allocate();
+    void* yp = expect(y, "y", xs, yt, dev);
+    float* sp = scaled ? (float*)expect(scales, "scales", ss, at::kFloat, dev) : nullptr;
+    void* op = with_res ? expect(out, "residual_out", xs, io, dev) : nullptr;
+    check(g_lib.norm_fwd(&p, xp, w, res, yp, sp, op, stream_of(dev)));
+    return Py_BuildValue("NNN", THPVariable_Wrap(y), wrap_or_none(scales), wrap_or_none(out));
+  });
+}
+
+// norm_bwd(problem, x, dy, weight, d_residual, dx, dweight, workspace) -> (dx, dweight)
+PyObject* norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    count(n, 8);
+    gdn_rms_norm_problem p = problem<gdn_rms_norm_problem>(a[0]);
+    const Tensor& x = tensor(a[1], "x");
+    const at::Device dev = gpu_of(x, "x");
+    const c10::DeviceGuard guard(dev);
+    const at::ScalarType io = io_type(p.dtype);
+    if (p.d < 1 || p.n_rows < 0) refuse("d must be >= 1 and n_rows >= 0");
+    const int64_t xs[] = {p.n_rows, p.d};
+    void* xp = expect(x, "x", xs, io, dev, &p.x_stride);
+    void* dyp = expect(tensor(a[2], "dy"), "dy", xs, io, dev);
+    const float* w = optional<float>(a[3], "weight", {p.d}, at::kFloat, dev);
+    void* res = a[4] == Py_None ? nullptr : expect(tensor(a[4], "d_residual"), "d_residual", xs, io, dev, &p.residual_stride);
+    if (!w && a[6] != Py_None) refuse("dweight is given without weight");
+    Tensor dx, dw;
+    Buffers made(dev);
+    made.want(dx, a[5], "dx", xs, io);
+    if (w) made.want(dw, a[6], "dweight", {p.d}, at::kFloat);
+    std::optional<Workspace> ws; // the weight's
+    if (w) ws.emplace(a[7], dev, made, [&] { return g_lib.norm_workspace(&p); });
+    made.allocate();
+    void* dxp = expect(dx, "dx", xs, io, dev);
+    float* dwp = w ? (float*)expect(dw, "dweight", {p.d}, at::kFloat, dev) : nullptr;
+    check(g_lib.norm_bwd(&p, xp, w, dyp, res, dxp, dwp, ws ? ws->t.data_ptr() : nullptr, ws ? ws->bytes : 0, stream_of(dev)));
+    return Py_BuildValue("NN", THPVariable_Wrap(dx), wrap_or_none(dw));
+  });
+}
+
+// step_maps(problem, lengths, contexts, block_table, free_list, free_count, cu_seqlens, positions, token_slots, granted,
+//           slot_in, slot_out, slot_tok, contexts_out, free_count_out) -> the nine outputs
+PyObject* step_maps(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    count(n, 15);
+    const gdn_step_maps_problem p = problem<gdn_step_maps_problem>(a[0]);
+    const Tensor& lengths = tensor(a[1], "lengths");
+    const at::Device dev = gpu_of(lengths, "lengths");
+    const c10::DeviceGuard guard(dev);
+    if (p.n_seqs < 0 || p.n_tokens < 0 || p.max_blocks < 0 || p.n_free < 0) refuse("sizes must be >= 0");
+    const int64_t N = p.n_seqs, T = p.n_tokens;
+    void* lp = expect(lengths, "lengths", {N}, at::kInt, dev);
+    void* cp = expect(tensor(a[2], "contexts"), "contexts", {N}, at::kInt, dev);
+    void* tp = expect(tensor(a[3], "block_table"), "block_table", {N, p.max_blocks}, at::kInt, dev);
+    void* fp = expect(tensor(a[4], "free_list"), "free_list", {p.n_free}, at::kInt, dev);
+    void* np = expect(tensor(a[5], "free_count"), "free_count", {1}, at::kInt, dev);
+    const char* names[] = {"cu_seqlens", "positions", "token_slots", "granted", "slot_in", "slot_out", "slot_tok", "contexts_out", "free_count_out"};
+    const int64_t sizes[] = {N + 1, T, T, N, N, N, T, N, 1};
+    Tensor out[9];
+    void* at[9];
+    Buffers made(dev);
+    for (int i = 0; i < 9; ++i) made.want(out[i], a[6 + i], names[i], {sizes[i]}, i == 2 ? at::kLong : at::kInt);
+    made.allocate();
+    for (int i = 0; i < 9; ++i) at[i] = expect(out[i], names[i], {sizes[i]}, i == 2 ? at::kLong : at::kInt, dev);
+    const gdn_step_maps_out o = {(int32_t*)at[0], (int32_t*)at[1], (int64_t*)at[2], (int32_t*)at[3], (int32_t*)at[4],
+                                 (int32_t*)at[5], (int32_t*)at[6], (int32_t*)at[7], (int32_t*)at[8]};
+    check(g_lib.step_maps(&p, (int32_t*)lp, (int32_t*)cp, (int32_t*)tp, (int32_t*)fp, (int32_t*)np, &o, stream_of(dev)));
+    PyObject* r = PyTuple_New(9);
+    for (int i = 0; r && i < 9; ++i) PyTuple_SET_ITEM(r, i, THPVariable_Wrap(out[i]));
+    return r;
+  });
+}
+
+// init(GdnError, addresses of the entry points in the order of Entries)
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 7) {
-    PyErr_SetString(PyExc_TypeError, "init takes 7 arguments");
+  if (n != 1 + ENTRIES) {
+    PyErr_Format(PyExc_TypeError, "init takes %d arguments", 1 + ENTRIES);
     return nullptr;
   }
-  void* f[6];
-  for (int i = 0; i < 6; ++i) {
+  void* f[ENTRIES];
+  for (int i = 0; i < ENTRIES; ++i) {
     f[i] = PyLong_AsVoidPtr(a[i + 1]);
     if (!f[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "NULL entry point");
@@ -358,8 +590,8 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Py_INCREF(a[0]);
   Py_XDECREF(g_error);
   g_error = a[0];
-  g_lib = {(decltype(g_lib.recurrent))f[0], (decltype(g_lib.conv_step))f[1], (decltype(g_lib.rope_fwd))f[2],
-           (decltype(g_lib.rope_bwd))f[3],  (decltype(g_lib.rope_workspace))f[4], (decltype(g_lib.last_error))f[5]};
+  static_assert(sizeof f == sizeof g_lib, "one address an entry");
+  std::memcpy(&g_lib, f, sizeof g_lib);
   Py_RETURN_NONE;
 }
 
@@ -369,6 +601,12 @@ PyMethodDef methods[] = {
     {"conv_step", (PyCFunction)(void (*)(void))conv_step, METH_FASTCALL, nullptr},
     {"rope_fwd", (PyCFunction)(void (*)(void))rope_fwd, METH_FASTCALL, nullptr},
     {"rope_bwd", (PyCFunction)(void (*)(void))rope_bwd, METH_FASTCALL, nullptr},
+    {"linear_fwd", (PyCFunction)(void (*)(void))linear_fwd, METH_FASTCALL, nullptr},
+    {"linear_bwd", (PyCFunction)(void (*)(void))linear_bwd, METH_FASTCALL, nullptr},
+    {"linear_step", (PyCFunction)(void (*)(void))linear_step, METH_FASTCALL, nullptr},
+    {"norm_fwd", (PyCFunction)(void (*)(void))norm_fwd, METH_FASTCALL, nullptr},
+    {"norm_bwd", (PyCFunction)(void (*)(void))norm_bwd, METH_FASTCALL, nullptr},
+    {"step_maps", (PyCFunction)(void (*)(void))step_maps, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

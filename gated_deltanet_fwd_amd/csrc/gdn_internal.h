@@ -230,4 +230,91 @@ struct RopeArgs {
 void rope_shape(RopeArgs& a, bool bwd);
 int launch_rope(const RopeArgs& a, bool bwd, int dtype, void* stream);
 
+// Linear attention (gdn_linear.hip): one product y = (a, b, c; W), forward or in reverse.
+struct LinearSide {
+  const void* p;
+  int64_t stride; // elements between its tokens
+  int shared;     // 1: [T, H, d], a head for each group of value heads; 0: [T, HV, d]
+};
+struct LinearArgs {
+  LinearSide a, b, c;
+  LinearSide dot;  // with dots: whose rows' products with y are wanted
+  int T, N, H, HV, G, D;
+  int seg, slots;  // tokens of a segment, a multiple of 64 (0: whole documents), and how many slots that makes
+  int gs;          // elements of g between tokens (HV, or 0: one decay a head)
+  int flip;        // 1: `init` and `states` hold the state with its rows and columns exchanged
+  float p_scale, in_scale, w_scale; // factors of a.b, of a W, and of what is added to W
+  const float* g;
+  const int32_t* cu;
+  const float* init; // [N, HV, d, d] states that documents start from (NULL: 0), forward h0, in reverse dht
+  float* fin;        // [N, HV, d, d] states that they end with, or NULL
+  float* states;     // [slots, HV, d, d] states that segments start from
+  float* decay;      // [slots, HV] factor of a state over a segment
+  void* out;         // y: [T, HV, d], or with `part` the sums over groups [T, H, d]
+  float* part;       // [T, HV, d] y in f32, before those sums; NULL: y goes to out
+  float* dots;       // [HV, T], or NULL
+};
+struct LinearDgArgs {
+  LinearArgs a;                // sizes, g, cu, slots
+  const float *S, *D;          // scanned states and their gradients, [slots, HV, d, d]
+  const float *h0, *dh0, *dht; // NULL where not given
+  const float *qdots, *kdots;  // [HV, T]
+  double* sums;                // [slots, HV] (one decay a head)
+  float* dg;                   // [T, HV], or [HV]
+};
+int launch_linear_states(const LinearArgs& a, bool rev, int dtype, void* stream);
+int launch_linear_scan(const LinearArgs& a, bool rev, void* stream);
+int launch_linear_walk(const LinearArgs& a, bool rev, int dtype, void* stream);
+int launch_linear_group_sum(const LinearArgs& a, int dtype, void* stream);
+int launch_linear_dg(const LinearDgArgs& d, void* stream);
+
+// Its serving step (gdn_linear_step.hip). `longest` and `live` by the host's lengths.
+struct LinearStepArgs {
+  int64_t qs, ks, vs;
+  uint64_t g_mul; // as in RecurrentArgs
+  int T, N, HV, D, n_slots, gs, longest, live;
+  float scale;
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* g;
+  const int32_t* cu;
+  const int32_t* slot_in;
+  const int32_t* slot_out;
+  const int32_t* slot_tok;
+  float* states;
+  void* o;
+};
+int launch_linear_step(const LinearStepArgs& a, int dtype, void* stream);
+
+// RMS norm of rows with the residual's addition (gdn_norm.hip).
+struct NormArgs {
+  int64_t rows;
+  int D, group, e4m3; // values of a scale (e4m3)
+  float eps;
+  int64_t xs, rs, ys, os; // elements between the rows of x, residual, y (dy) and residual_out (dx)
+  const void* x;
+  const void* res; // forward: the residual; backward: the gradient of residual_out; NULL: none
+  const float* w;  // NULL: ones
+  const void* dy;
+  void* y;         // forward
+  float* scales;   // forward, e4m3: [rows, D / group]
+  void* out;       // forward: residual_out; backward: dx
+  float* dw;
+  float* part;     // [norm_blocks][D]
+};
+int norm_blocks(const NormArgs& a); // workgroups of the backward, whose weight gradients are summed
+int launch_norm_fwd(const NormArgs& a, int dtype, void* stream);
+int launch_norm_bwd(const NormArgs& a, int dtype, void* stream);
+
+// What a serving step reads, from the requests' lengths (gdn_maps.hip).
+struct MapsArgs {
+  int N, T, block, max_blocks, n_free;
+  const int32_t *lengths, *contexts, *free_list, *free_count;
+  int32_t *table, *contexts_out, *free_count_out;
+  int32_t *cu, *positions, *granted, *slot_in, *slot_out, *slot_tok;
+  int64_t* token_slots;
+};
+int launch_maps(const MapsArgs& a, void* stream);
+
 } // namespace gdn

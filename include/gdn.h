@@ -395,6 +395,175 @@ int gdn_conv_step(const gdn_conv_step_problem* p, const void* x, const float* we
                   const int32_t* cu_seqlens, const int32_t* slot_in, const int32_t* slot_out,
                   const int32_t* slot_tok, void* windows, void* const* y, void* stream);
 
+/* ---- Linear attention with a decay for each head ---------------------------------------------
+ * The layer without the delta rule: per document n and value head h, with q/k head j = h / (HV / H),
+ *
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
+ *
+ * S_0 = h0[n,h] (or 0) and ht[n,h] = S_last as in gdn_fwd. The log decays g are one for each token and
+ * head (GDN_DECAY_TOKEN, [T, HV]) or one for each head (GDN_DECAY_HEAD, [HV]). Layouts as at the top of
+ * this file (g may start at any of its values); q, k and v may be parts of one row (their strides in the problem). o and the gradients are
+ * contiguous. States, decays and sums are FP32 (the sums of the log decays 64-bit); for bf16 the decayed
+ * products of a chunk and the state that they meet are rounded once to bf16 for o, dq, dk and dv, which are
+ * rounded to it themselves. ht, dh0 and dg keep FP32's accuracy. All sums have a fixed order: the
+ * same call gives the same bits.
+ *
+ * A document goes in chunks of 64 tokens, and what is not finite in a token reaches, through zeros of
+ * masked products, all tokens of its chunk (forward also earlier ones), then what depends on the state;
+ * other documents never. A log decay of minus infinity drops the state (as any under -10000). Log
+ * decays may be positive while their sums over a chunk stay in FP32's range.
+ *
+ * The launch is planned from the host's lengths; the device's cu_seqlens may hold others (a graph that is
+ * replayed with other lengths, or a shorter batch: T and N stay), as long as it rises from 0 or more to
+ * at most T. Values that do not are cut to that range, and the rows of such documents are then not
+ * specified. Rows of o and of gradients that no document covers are not written. */
+#define GDN_DECAY_TOKEN 0
+#define GDN_DECAY_HEAD 1
+
+typedef struct gdn_linear_problem {
+  int32_t n_seqs;                 /* N documents, 1 .. 65535 (of zero tokens or more) */
+  int32_t h_qk;                   /* H q/k heads */
+  int32_t h_v;                    /* HV value heads, a multiple of H; HV d at most 2^22 */
+  int32_t d;                      /* head dim, 64 or 128 */
+  int64_t n_tokens;               /* T = cu_seqlens[N], at most 2^31 - 2^20 */
+  int32_t dtype;                  /* GDN_DTYPE_* of q, k, v, o and their gradients */
+  int32_t decay;                  /* GDN_DECAY_* */
+  int32_t has_h0;                 /* 1: h0 is given (and gdn_linear_bwd writes dh0) */
+  int32_t want_ht;                /* 1: gdn_linear_fwd writes ht */
+  float scale;                    /* of the outputs */
+  int32_t reserved0;              /* must be 0 */
+  int64_t q_stride;               /* elements from one token's q to the next (0: H * d), at most */
+  int64_t k_stride;               /* 2^22; the same for k and v (0: HV * d). Rows are 16-byte */
+  int64_t v_stride;               /* aligned */
+  const int32_t* cu_seqlens_host; /* host copy of cu_seqlens, read during each call only */
+} gdn_linear_problem;
+
+/* Bytes of device workspace a call of `op` (GDN_OP_FWD, GDN_OP_BWD) needs: the states that long documents'
+ * segments start from, and in the backward their gradients, row products for dg and, with shared heads,
+ * dq and dk before their sums over a group. 0 if the problem is invalid. */
+size_t gdn_linear_workspace_bytes(const gdn_linear_problem* p, int op);
+
+/* Forward: o, and ht if want_ht. */
+int gdn_linear_fwd(const gdn_linear_problem* p, const void* q, const void* k, const void* v, const float* g,
+                   const int32_t* cu_seqlens, const float* h0, void* o, float* ht, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/* Backward, from the forward's inputs alone (no saved set): dq, dk, dv from dO and optional dht (NULL = 0);
+ * dg (g's layout) if not NULL; dh0 iff has_h0. Without dg the products that it alone needs are left out. */
+int gdn_linear_bwd(const gdn_linear_problem* p, const void* q, const void* k, const void* v, const float* g,
+                   const int32_t* cu_seqlens, const float* h0, const void* dO, const float* dht, void* dq, void* dk,
+                   void* dv, float* dg, float* dh0, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Its serving step on cached states, token by token in FP32: slots, cu_seqlens, slot_tok and the checks on
+ * the device are gdn_recurrent's. For prompts gdn_linear_fwd is faster, whose h0 and ht have the layout of cached
+ * states. */
+typedef struct gdn_linear_step_problem {
+  int32_t n_seqs;                 /* N >= 1 sequences (of zero tokens or more); N and T at most 2^31 - 2^20 */
+  int32_t h_qk;                   /* H q/k heads */
+  int32_t h_v;                    /* HV value heads, a multiple of H */
+  int32_t d;                      /* head dim, 64 or 128 */
+  int64_t n_tokens;               /* T */
+  int32_t dtype;                  /* GDN_DTYPE_* of q, k, v, o */
+  int32_t decay;                  /* GDN_DECAY_* */
+  float scale;                    /* of the outputs */
+  int32_t n_slots;                /* states in the cache, >= 1 */
+  int32_t reserved0;              /* must be 0 */
+  int64_t q_stride;               /* as in gdn_recurrent_problem */
+  int64_t k_stride;
+  int64_t v_stride;
+  const int32_t* cu_seqlens_host; /* host copy of cu_seqlens; NULL: one token a sequence */
+} gdn_linear_step_problem;
+
+int gdn_linear_step(const gdn_linear_step_problem* p, const void* q, const void* k, const void* v, const float* g,
+                    const int32_t* cu_seqlens, const int32_t* slot_in, const int32_t* slot_out, const int32_t* slot_tok,
+                    float* states, void* o, void* stream);
+
+/* ---- RMS norm of rows with the residual's addition --------------------------------------------
+ * What stands before a layer's projections. For each row of d values (weight w, or ones):
+ *
+ *     x' = x + residual                  (FP32; x without a residual)
+ *     residual_out = x'                  (rounded to the io type)
+ *     y  = w x' / sqrt(mean(x'^2) + eps) (of x' before that rounding)
+ *
+ * y is in the io type (GDN_OUT_IO), or in 8 bits (GDN_OUT_E4M3: sign, 4 exponent and 3 mantissa bits, largest
+ * value 448) with an FP32 scale for each row (group = 0) or each `group` values of it: scale = the largest
+ * magnitude / 448 (1 where all are zero, at least 2^-126) and y the nearest of x / scale, ties to even. y and
+ * residual_out may be the inputs' own buffers (of the same row layout): each row is read before it is
+ * written. x' has to stay below the root of FP32's range for its squares. With eps = 0 a row of zeros gives NaN.
+ * What is not finite stays in its row. */
+#define GDN_OUT_IO 0
+#define GDN_OUT_E4M3 1
+
+typedef struct gdn_rms_norm_problem {
+  int64_t n_rows;          /* >= 0 */
+  int32_t d;               /* a multiple of 8, 8 .. 16384 */
+  int32_t dtype;           /* GDN_DTYPE_* of x, residual, y (GDN_OUT_IO) and gradients */
+  int32_t out;             /* GDN_OUT_* */
+  int32_t group;           /* GDN_OUT_E4M3: values that share a scale: 0 (the row), 32, 64 or 128 */
+  float eps;               /* added under the root */
+  int32_t reserved0;       /* must be 0 */
+  int64_t x_stride;        /* elements between the rows of x (0: contiguous) */
+  int64_t residual_stride; /* and of residual (backward: of d_residual). Rows are 16-byte aligned */
+} gdn_rms_norm_problem;
+
+/* Bytes of device workspace gdn_rms_norm_bwd needs (workgroups' sums of dweight). 0 if the problem is invalid. */
+size_t gdn_rms_norm_workspace_bytes(const gdn_rms_norm_problem* p);
+
+/* Forward: y [n_rows, d]; scales f32 [n_rows, d / group] with GDN_OUT_E4M3; residual_out [n_rows, d] iff residual. */
+int gdn_rms_norm_fwd(const gdn_rms_norm_problem* p, const void* x, const float* weight, const void* residual, void* y,
+                     float* scales, void* residual_out, void* stream);
+
+/* Backward of the GDN_OUT_IO form at x' = x (what the forward left in residual_out): dx = the gradient of x'
+ * through y plus d_residual (that of residual_out; NULL: 0), which is the gradient of the forward's x and
+ * residual alike; dweight f32 [d] (NULL: not wanted), summed in a fixed order. dx may be dy or d_residual. */
+int gdn_rms_norm_bwd(const gdn_rms_norm_problem* p, const void* x, const float* weight, const void* dy,
+                     const void* d_residual, void* dx, float* dweight, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- What a serving step reads, from the requests' lengths -------------------------------------
+ * N requests with contexts[n] tokens in the caches and lengths[n] new ones. Caches are cut into blocks of
+ * `block` tokens; block_table[n, b] names the block that holds tokens b block .. of request n. Blocks that new
+ * tokens enter are taken from the end of free_list[0 .. free_count), in the requests' order, and written to the
+ * table (its other entries stay). Made for the step:
+ *
+ *   granted [N]       tokens that the request gets: lengths[n], or 0 from the first request on whose tokens or
+ *                     blocks do not fit any more (n_tokens, free_count); also 0, for that request alone, where
+ *                     lengths[n] or contexts[n] is negative or the table has no room for them
+ *   cu_seqlens [N+1]  running sums of granted, from 0
+ *   positions [T]     the position of each token in its request (0 behind the last)
+ *   token_slots [T]   its row in a cache of blocks, block_table[n, p / block] block + p % block (-1 behind the last)
+ *   slot_in [N]       the block of the request's last token in the caches (-1 with none): the state that it starts from
+ *   slot_out [N]      the block of its last token after the step (slot_in without new tokens): where its state goes
+ *   slot_tok [T]      for each token that ends a block and is not the step's last of its request that block, else -1:
+ *                     states after whole blocks stay behind, as starts for requests that share the tokens so far
+ *   contexts [N]      contexts + granted; free_count [1] what is left (both may be the inputs' own buffers)
+ *
+ * With slots that are blocks, gdn_recurrent, gdn_linear_step and gdn_conv_step read cu_seqlens, slot_in, slot_out and
+ * slot_tok, and gdn_qk_rope positions, as they are. Any output may be NULL. A free_count outside
+ * [0, n_free] is cut to that. The call may be captured; all of its arrays are read at each replay. */
+typedef struct gdn_step_maps_problem {
+  int32_t n_seqs;     /* N requests, 1 .. 4096 */
+  int32_t block;      /* tokens of a block, >= 1 */
+  int64_t n_tokens;   /* T: room for new tokens, 0 .. 2^31 - 2^20 */
+  int32_t max_blocks; /* columns of block_table, >= 1 */
+  int32_t n_free;     /* entries of free_list, >= 0 */
+  int32_t reserved0;  /* must be 0 */
+} gdn_step_maps_problem;
+
+typedef struct gdn_step_maps_out {
+  int32_t* cu_seqlens;
+  int32_t* positions;
+  int64_t* token_slots;
+  int32_t* granted;
+  int32_t* slot_in;
+  int32_t* slot_out;
+  int32_t* slot_tok;
+  int32_t* contexts;
+  int32_t* free_count;
+} gdn_step_maps_out;
+
+int gdn_step_maps(const gdn_step_maps_problem* p, const int32_t* lengths, const int32_t* contexts, int32_t* block_table,
+                  const int32_t* free_list, const int32_t* free_count, const gdn_step_maps_out* out, void* stream);
+
 /* Message of the calling thread's last error ("" if none). */
 const char* gdn_last_error(void);
 
