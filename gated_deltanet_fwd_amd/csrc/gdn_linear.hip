@@ -26,40 +26,116 @@
 
 namespace gdn {
 
-typedef float f32x8 __attribute__((ext_vector_type(8)));
-
 // ------------------------------------------------------------------------------------------------
-// Operands of 16x16 products over 32 k values, in the k-permuted order of gdn_device.h: lane group g has the
+// Tiles: 64 rows of d values in LDS, filled straight from memory (16 bytes a lane, a wave's lanes next to each
+// other), so rows are not padded. Instead the 16-byte unit u of row r lies at u ^ f(r mod 16), where f is chosen
+// so that the lanes that are served together meet all 64 banks, both where they read along rows (16 rows,
+// 8 bytes each for bf16, 16 for f32) and down columns (bf16: 8 rows, 32 bytes each; f32: 4 rows, 64 bytes each).
+//
+// Operands of 16x16 products over 32 k values come in the k-permuted order of gdn_device.h: lane group g has the
 // k values 4 g .. 4 g + 3 and 16 + 4 g .. 16 + 4 g + 3. bf16 rows go to one instruction, f32 rows to eight of
 // 4 k values (element e of every lane to the e-th), so both share all of the indexing.
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) char lds_char;
+
+template <typename T>
+__device__ __forceinline__ T lds_read(int at) {
+  return *(__attribute__((address_space(3))) const T*)(lds_char*)(uintptr_t)at;
+}
+template <typename T>
+__device__ __forceinline__ void lds_write(int at, const T& x) {
+  *(__attribute__((address_space(3))) T*)(lds_char*)(uintptr_t)at = x;
+}
+
+template <typename T, int D>
+struct Tile {
+  static constexpr bool HALF = sizeof(T) == 2;
+  static constexpr int ROW = D * sizeof(T), BYTES = CH * ROW; // of a row, of a tile
+  static constexpr int UNITS = ROW / 16, TOGETHER = 64 / UNITS, PIECES = 16 / TOGETHER; // rows a load, loads of a wave's 16 rows
+  static __device__ __forceinline__ constexpr int f(int r) {
+    return !HALF ? r & 15 : D == 128 ? (r & 7) << 1 | (r >> 3 & 1) : (r >> 1 & 3) << 1 | (r >> 3 & 1);
+  }
+};
+
 template <typename T>
 struct Op;
 template <>
 struct Op<bf16> {
   typedef bf16x8 frag;
-  static constexpr int PADDED = 8; // elements of row padding in LDS
   // The terms that hold an FP32 value: 3 bf16 hold all of its 24 bits.
   static constexpr int EXACT = 3;
-  static __device__ __forceinline__ frag along(const bf16* tile, int stride, int row, int k0) { return lds_kp(tile, stride, row, k0); }
-  static __device__ __forceinline__ frag down(const bf16* tile, int stride, int k0, int m0) { return lds_tr_kp(tile, stride, k0, m0); }
+  // lane constants: of a read along row l16 (of 16), down the column of lane l16 (of 16) from row 4 g
+  template <int D>
+  static __device__ __forceinline__ int along_lane() {
+    typedef Tile<bf16, D> S;
+    const int l = threadIdx.x & 63, g = l >> 4, r = l & 15;
+    return r * S::ROW + (((g >> 1) ^ S::f(r)) << 4) + (g & 1) * 8;
+  }
+  template <int D> // rows 16 row16 .., k values 32 kk ..
+  static __device__ __forceinline__ frag along(int tile, int lane, int row16, int kk) {
+    const int at = tile + row16 * 16 * Tile<bf16, D>::ROW;
+    const bf16x4 a = lds_read<bf16x4>(at + (lane ^ (kk << 6))), b = lds_read<bf16x4>(at + (lane ^ (kk << 6 | 32)));
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+  // Columns `first` + `step` (l16 / 4) + l16 mod 4, both multiples of 4. The transposing read hands lane i of 16 element
+  // i mod 4 of the 8-byte blocks that lanes i / 4, + 4, .. address (see lds_tr8).
+  struct Down {
+    int at;
+  };
+  template <int D>
+  static __device__ __forceinline__ Down down_lane(int first, int step) {
+    typedef Tile<bf16, D> S;
+    const int l = threadIdx.x & 63, g = l >> 4, j = l & 15, r = 4 * g + (j >> 2), col = first + step * (j & 3);
+    return {r * S::ROW + (((col >> 3) ^ S::f(r)) << 4) + (col & 4) * 2};
+  }
+  template <int D> // k values: rows 32 ks ..; columns moved by 16 m
+  static __device__ __forceinline__ frag down(int tile, const Down& lane, int ks, int m) {
+    constexpr int ROW = Tile<bf16, D>::ROW;
+    typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
+    const int at = tile + (lane.at ^ (m << 5)) + 32 * ks * ROW;
+    const bf16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(lds_char*)(uintptr_t)at);
+    const bf16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(lds_char*)(uintptr_t)(at + 16 * ROW));
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
   static __device__ __forceinline__ f32x4 mul(const frag& a, const frag& b, const f32x4& c) { return mfma(a, b, c); }
 };
 template <>
 struct Op<float> {
   typedef f32x8 frag;
-  static constexpr int PADDED = 4, EXACT = 1;
-  static __device__ __forceinline__ frag along(const float* tile, int stride, int row, int k0) {
-    const float* p = tile + row * stride + k0 + 4 * ((threadIdx.x & 63) >> 4);
-    const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 16);
+  static constexpr int EXACT = 1;
+  template <int D>
+  static __device__ __forceinline__ int along_lane() {
+    typedef Tile<float, D> S;
+    const int l = threadIdx.x & 63, g = l >> 4, r = l & 15;
+    return r * S::ROW + ((g ^ S::f(r)) << 4);
+  }
+  template <int D>
+  static __device__ __forceinline__ frag along(int tile, int lane, int row16, int kk) {
+    const int at = tile + row16 * 16 * Tile<float, D>::ROW;
+    const f32x4 a = lds_read<f32x4>(at + (lane ^ (kk << 7))), b = lds_read<f32x4>(at + (lane ^ (kk << 7 | 64)));
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
   }
-  static __device__ __forceinline__ frag down(const float* tile, int stride, int k0, int m0) {
-    const float* p = tile + (k0 + 4 * ((threadIdx.x & 63) >> 4)) * stride + m0 + (threadIdx.x & 15);
+  struct Down {
+    int at[4];
+  };
+  template <int D>
+  static __device__ __forceinline__ Down down_lane(int first, int step) {
+    typedef Tile<float, D> S;
+    const int l = threadIdx.x & 63, g = l >> 4, j = l & 15, col = first + step * (j >> 2);
+    Down d;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d.at[e] = (4 * g + e) * S::ROW + (((col >> 2) ^ S::f(4 * g + e)) << 4) + (j & 3) * 4;
+    return d;
+  }
+  template <int D>
+  static __device__ __forceinline__ frag down(int tile, const Down& lane, int ks, int m) {
+    constexpr int ROW = Tile<float, D>::ROW;
     frag r;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      r[e] = p[e * stride];
-      r[4 + e] = p[(16 + e) * stride];
+      const int at = tile + (lane.at[e] ^ (m << 6)) + 32 * ks * ROW;
+      r[e] = lds_read<float>(at);
+      r[4 + e] = lds_read<float>(at + 16 * ROW);
     }
     return r;
   }
@@ -71,39 +147,37 @@ struct Op<float> {
 };
 
 // FP32 values as NT operands whose sum they are: of bf16 each term takes the 8 leading bits of what the terms
-// before it left.
+// before it left (x - x's leading bits by a product with -1: exact, and one instruction from the packed pair).
 template <typename T, int NT>
 struct Terms {
   typename Op<T>::frag f[NT];
+  __device__ __forceinline__ Terms() {}
   __device__ __forceinline__ explicit Terms(const f32x8& x) {
     if constexpr (sizeof(T) == 4) {
       f[0] = x;
     } else {
+      typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+      // (-1, 0) and (0, -1); as a constant that the compiler knows it would become an inline one, which the
+      // instruction reads as a 32-bit -1
+      unsigned low = 0xbf80, high = 0xbf800000;
+      asm("" : "+s"(low), "+s"(high));
+      const bf16x2 first = __builtin_bit_cast(bf16x2, low), second = __builtin_bit_cast(bf16x2, high);
       f32x8 left = x;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[n][e] = (bf16)left[e];
-        if (n + 1 < NT) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) left[e] -= (float)f[n][e];
+        for (int e = 0; e < 8; e += 2) {
+          const bf16x2 h = {(__bf16)left[e], (__bf16)left[e + 1]};
+          f[n][e] = h[0];
+          f[n][e + 1] = h[1];
+          if (n + 1 < NT) {
+            left[e] = __builtin_amdgcn_fdot2_f32_bf16(h, first, left[e], false);
+            left[e + 1] = __builtin_amdgcn_fdot2_f32_bf16(h, second, left[e + 1], false);
+          }
         }
-      }
     }
   }
 };
-template <typename T, int NT>
-__device__ __forceinline__ f32x4 mul_terms(const Terms<T, NT>& a, const typename Op<T>::frag& b, f32x4 c) {
-#pragma unroll
-  for (int n = NT - 1; n >= 0; --n) c = Op<T>::mul(a.f[n], b, c);
-  return c;
-}
-template <typename T, int NT>
-__device__ __forceinline__ f32x4 mul_terms(const typename Op<T>::frag& a, const Terms<T, NT>& b, f32x4 c) {
-#pragma unroll
-  for (int n = NT - 1; n >= 0; --n) c = Op<T>::mul(a, b.f[n], c);
-  return c;
-}
 __device__ __forceinline__ f32x8 join(const f32x4& a, const f32x4& b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
 template <typename T>
 __device__ __forceinline__ f32x8 widen(const typename Op<T>::frag& x) {
@@ -122,6 +196,7 @@ struct Segment {
   int doc, i, t0, t1; // its document, its place there, its tokens
   bool live, first, last;
 };
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 __device__ __forceinline__ int cut_to(int x, int T) { return min(max(x, 0), T); }
 __device__ __forceinline__ int doc_slot(const LinearArgs& a, int n) { return a.seg == 0 ? n : cut_to(a.cu[n], a.T) / a.seg + n; }
 __device__ __forceinline__ Segment find_segment(const LinearArgs& a, int slot) {
@@ -130,13 +205,13 @@ __device__ __forceinline__ Segment find_segment(const LinearArgs& a, int slot) {
   else
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (doc_slot(a, mid) <= slot) lo = mid;
+      if (uniform(doc_slot(a, mid)) <= slot) lo = mid;
       else hi = mid - 1;
     }
   Segment s;
   s.doc = lo;
-  const int from = cut_to(a.cu[lo], a.T), to = max(cut_to(a.cu[lo + 1], a.T), from);
-  s.i = a.seg == 0 ? 0 : slot - doc_slot(a, lo);
+  const int from = uniform(cut_to(a.cu[lo], a.T)), to = max(uniform(cut_to(a.cu[lo + 1], a.T)), from);
+  s.i = a.seg == 0 ? 0 : slot - uniform(doc_slot(a, lo));
   const int64_t t0 = from + (int64_t)s.i * a.seg;
   s.live = s.i == 0 || (s.i > 0 && t0 < to);
   s.t0 = (int)(t0 < to ? t0 : to);
@@ -161,7 +236,7 @@ static unsigned place_blocks(const LinearArgs& a) { return (unsigned)(((int64_t)
 // Decays of one chunk, from the 64 log decays in a wave's lanes. The sums are kept in 64 bits (as two 32-bit
 // floats, in powers of two): differences of 32-bit sums of strong decays would lose what they differ by.
 // A log decay under -10000 is taken as that: its exponential is 0 either way, and infinities have no differences.
-struct Decays {
+struct alignas(16) Decays {
   float hi[CH], lo[CH]; // sum up to and with each token
   float in[CH];         // factor of the state that enters, for each row
   float w[CH];          // factor of each row in the state that leaves
@@ -189,70 +264,131 @@ __device__ __forceinline__ float log_decay(const LinearArgs& a, int h, int t, in
   return t < t1 ? a.g[(int64_t)t * a.gs + h] : 0.f;
 }
 
-// 64 rows of an operand: through a buffer that ends with the segment, so that rows behind it are zeros
+// 64 rows of an operand from memory to a tile: wave w loads rows 16 w .. of it, through a buffer that ends with
+// the segment, so that rows behind it arrive as zeros. The loads are written in assembly, without output
+// registers: the compiler, which cannot tell one tile from another, would wait for them before every read of any
+// tile. They are waited for by wait_loads before the barrier that hands the tile over.
 template <typename T, int D>
-struct Rows {
-  static constexpr int PER = 16 / sizeof(T), PIECES = CH * D / PER / NTHREADS, STRIDE = D + Op<T>::PADDED;
-  i32x4_t r[PIECES];
-  __device__ __forceinline__ void load(const LinearSide& x, const LinearArgs& a, int h, int t, int t1) {
-    const int n = max(min(t1 - t, CH), 0);
-    const T* p = (const T*)x.p + (int64_t)t * x.stride + (int64_t)(x.shared ? h / a.G : h) * D;
-    const __amdgpu_buffer_rsrc_t from = make_rsrc(p, n > 0 ? ((n - 1) * (int)x.stride + D) * (int)sizeof(T) : 0);
-#pragma unroll
-    for (int i = 0; i < PIECES; ++i) {
-      const int at = threadIdx.x + i * NTHREADS, row = at / (D / PER), col = at % (D / PER) * PER;
-      r[i] = buf_load16(from, row < n ? (row * (int)x.stride + col) * (int)sizeof(T) : 0x7ffffff0);
-    }
+struct Feed {
+  typedef Tile<T, D> S;
+  const T* base; // of the head
+  int stride, unit, lane, wave; // the lane's place in a row and its row, in bytes
+  __device__ __forceinline__ Feed(const LinearSide& x, const LinearArgs& a, int h, int w)
+      : base((const T*)x.p + (int64_t)(x.shared ? h / a.G : h) * D), stride((int)x.stride), wave(w) {
+    const int l = threadIdx.x & 63, q = l / S::UNITS, u = l % S::UNITS;
+    unit = (u ^ S::f(q)) << 4;
+    lane = q * stride * (int)sizeof(T);
   }
-  __device__ __forceinline__ void store(T* tile) const {
+  __device__ __forceinline__ void load(int tile, int t, int t1) const {
+    const int n = max(min(t1 - t, CH), 0);
+    const uint64_t p = (uint64_t)(base + (int64_t)t * stride);
+    i32x4_t from = {uniform((int)p), uniform((int)(p >> 32) & 0xffff), uniform(n > 0 ? ((n - 1) * stride + D) * (int)sizeof(T) : 0),
+                    0x00020000}; // make_rsrc's words
+    asm volatile("s_nop 4" : "+s"(from)); // before a buffer access reads scalars that a vector instruction wrote
+    const int step = S::TOGETHER * stride * (int)sizeof(T);
+    int row = wave * S::PIECES * step, to = uniform(tile + wave * 16 * S::ROW);
 #pragma unroll
-    for (int i = 0; i < PIECES; ++i) {
-      const int at = threadIdx.x + i * NTHREADS, row = at / (D / PER), col = at % (D / PER) * PER;
-      *reinterpret_cast<i32x4_t*>(tile + row * STRIDE + col) = r[i];
+    for (int i = 0; i < S::PIECES; ++i, row += step, to += 1024) {
+      const int off = (unit ^ (S::f(i * S::TOGETHER) << 4)) + lane + row;
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" : : "s"(to), "v"(off), "s"(from) : "m0", "memory");
     }
   }
 };
+// Waits until all but the newest N of a wave's memory accesses are done.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
 
-// W += b^T diag(w) c over one chunk, for a wave's columns: W[kt][ct] the 16x16 tile of rows 16 kt.. and columns
-// col0 + 16 ct... w c is the one operand that is no input; it goes in as EXACT terms, since the states are
-// results in FP32 and everything after them is made from them.
-template <typename T, int D, int CT>
-__device__ __forceinline__ void add_to_state(f32x4 (&W)[D / 16][CT], const typename Op<T>::frag (&cf)[2][CT], const T* tb,
-                                             const Decays& d) {
-  constexpr int LD = Rows<T, D>::STRIDE, NT = Op<T>::EXACT;
+// Column of lane l16 in a wave's tile ct of CT: neighbouring tiles share 4 CT neighbouring columns, so that a lane's
+// part of a row of y is one piece.
+template <int CT>
+__device__ __forceinline__ int column(int col0, int ct, int l16) {
+  return col0 + 4 * CT * (l16 >> 2) + 4 * ct + (l16 & 3);
+}
+
+// A value that the compiler takes for a new one: what is derived from it is computed where it is used, and not
+// kept in registers from before a loop.
+__device__ __forceinline__ int fresh(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+// The states between the kernels lie as the registers hold them: four rows of a column together, a wave's lanes next to
+// each other. Element i of that order is row kept_row(i), column kept_col(i).
+template <int D>
+__device__ __forceinline__ int kept_at(int wave, int kt, int ct, int lane) {
+  return (((wave * (D / 16) + kt) * (D / 64) + ct) * 64 + lane) * 4;
+}
+template <int D>
+__device__ __forceinline__ int kept_row(int i) {
+  return 16 * (i / 256 / (D / 64) % (D / 16)) + 4 * (i / 64 % 4) + i % 4;
+}
+template <int D>
+__device__ __forceinline__ int kept_col(int i) {
+  return column<D / 64>(i / 256 / (D / 64) / (D / 16) * (D / 4), i / 256 % (D / 64), i / 4 % 16);
+}
+// And where the element of a row and column lies.
+template <int D>
+__device__ __forceinline__ int kept_of(int row, int col) {
+  constexpr int CT = D / 64;
+  const int in = col % (16 * CT), l16 = in / (4 * CT) * 4 + in % 4;
+  return kept_at<D>(col / (16 * CT), row / 16, in / 4 % CT, row % 16 / 4 * 16 + l16) + row % 4;
+}
+
+// W = decay W + b^T diag(w) c over one chunk, for a wave's columns: W[kt][ct] the tile of rows 16 kt .. and the
+// columns of tile ct, cf its c. w c is the one operand that is no input; it goes in as NT terms. (A tile's terms one
+// after the other would wait for each other: a round over the tiles for each.)
+template <typename T, int D, int CT, int NT>
+__device__ __forceinline__ void add_to_state(f32x4 (&W)[D / 16][CT], const typename Op<T>::frag (&cf)[2][CT], int tb,
+                                             const typename Op<T>::Down& lane, const Decays& d) {
   const int g = (threadIdx.x & 63) >> 4;
   const float all = d.all;
 #pragma unroll
-  for (int kt = 0; kt < D / 16; ++kt)
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) W[kt][ct] *= all;
-#pragma unroll
   for (int ks = 0; ks < 2; ++ks) {
     const f32x8 w = join(*reinterpret_cast<const f32x4*>(&d.w[32 * ks + 4 * g]), *reinterpret_cast<const f32x4*>(&d.w[32 * ks + 16 + 4 * g]));
+    Terms<T, NT> cw[CT];
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-      const Terms<T, NT> cw(widen<T>(cf[ks][ct]) * w);
+    for (int ct = 0; ct < CT; ++ct) cw[ct] = Terms<T, NT>(widen<T>(cf[ks][ct]) * w);
 #pragma unroll
-      for (int kt = 0; kt < D / 16; ++kt) W[kt][ct] = mul_terms<T, NT>(Op<T>::down(tb, LD, 32 * ks, 16 * kt), cw, W[kt][ct]);
+    for (int k4 = 0; k4 < D / 16; k4 += 4) {
+      typename Op<T>::frag bf[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        bf[j] = Op<T>::template down<D>(tb, lane, ks, k4 + j);
+        if (ks == 0)
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) W[k4 + j][ct] *= all;
+      }
+#pragma unroll
+      for (int n = NT - 1; n >= 0; --n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) W[k4 + j][ct] = Op<T>::mul(bf[j], cw[ct].f[n], W[k4 + j][ct]);
     }
   }
 }
 
+// LDS of the kernels: tiles at the start, then what they name
+extern __shared__ __attribute__((aligned(1024))) char linear_lds[];
+__device__ __forceinline__ int lds_start() { return (int)(uintptr_t)(lds_char*)linear_lds; }
+
 // ------------------------------------------------------------------------------------------------
 // What each segment adds to a state, and its decay. The last segment of a document (the first, in reverse)
-// is left out: no other starts from it.
+// is left out: no other starts from it. w c goes in as EXACT terms: the states are results in FP32, and
+// everything after them is made from them.
 template <typename T, int D, bool REV>
 __global__ __launch_bounds__(NTHREADS, sizeof(T) == 2 ? 2 : 1) void k_linear_states(LinearArgs a) {
-  constexpr int CT = D / 64, LD = Rows<T, D>::STRIDE;
-  extern __shared__ __attribute__((aligned(16))) char lds[];
-  T* tb = (T*)lds;
-  T* tc = tb + CH * LD;
-  Decays* dec = (Decays*)(tc + CH * LD);
+  typedef Tile<T, D> S;
+  constexpr int CT = D / 64, NT = Op<T>::EXACT;
+  Decays* dec = (Decays*)(linear_lds + 4 * S::BYTES); // of two chunks
   int slot, h;
   if (!place(a, &slot, &h)) return;
   const Segment s = find_segment(a, slot);
   if (!s.live || (REV ? s.first : s.last)) return;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15, col0 = wave * 16 * CT;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+  const int col0 = wave * 16 * CT, tiles = lds_start();
   f32x4 W[D / 16][CT];
 #pragma unroll
   for (int kt = 0; kt < D / 16; ++kt)
@@ -260,40 +396,47 @@ __global__ __launch_bounds__(NTHREADS, sizeof(T) == 2 ? 2 : 1) void k_linear_sta
     for (int ct = 0; ct < CT; ++ct) W[kt][ct] = zero4();
   const int chunks = (s.t1 - s.t0 + CH - 1) / CH;
   const auto at = [&](int i) { return s.t0 + (REV ? chunks - 1 - i : i) * CH; };
-  Rows<T, D> rb, rc;
+  const Feed<T, D> fb(a.b, a, h, wave), fc(a.c, a, h, wave);
+  const typename Op<T>::Down b_lane = Op<T>::template down_lane<D>(0, 4);
+  typename Op<T>::Down c_lane[CT];
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) c_lane[ct] = Op<T>::template down_lane<D>(col0 + 4 * ct, 4 * CT);
   float gl = 0.f;
   double sum = 0.0; // of the log decays, in wave 0
-  rb.load(a.b, a, h, at(0), s.t1);
-  rc.load(a.c, a, h, at(0), s.t1);
-  if (wave == 0) gl = log_decay(a, h, at(0) + lane, s.t1);
+  const auto decays = [&](int i) { // of chunk i, and the log decays of the next
+    chunk_decays<REV>(dec[i & 1], gl, 1.f, a.w_scale);
+    sum += (double)(gl < -1e4f ? -1e4f : gl);
+    gl = i + 1 < chunks ? log_decay(a, h, at(i + 1) + lane, s.t1) : 0.f;
+  };
+  if (wave == 0) {
+    gl = log_decay(a, h, at(0) + lane, s.t1);
+    decays(0);
+  }
+  fb.load(tiles, at(0), s.t1);
+  fc.load(tiles + S::BYTES, at(0), s.t1);
   for (int i = 0; i < chunks; ++i) {
-    rb.store(tb);
-    rc.store(tc);
-    if (wave == 0) {
-      chunk_decays<REV>(*dec, gl, 1.f, a.w_scale);
-      sum += (double)(gl < -1e4f ? -1e4f : gl);
-    }
+    wait_loads<0>();
     __syncthreads();
+    const int tb = tiles + (i & 1) * 2 * S::BYTES, tc = tb + S::BYTES;
     if (i + 1 < chunks) {
-      rb.load(a.b, a, h, at(i + 1), s.t1);
-      rc.load(a.c, a, h, at(i + 1), s.t1);
-      if (wave == 0) gl = log_decay(a, h, at(i + 1) + lane, s.t1);
+      const int next = tiles + (~i & 1) * 2 * S::BYTES;
+      fb.load(next, at(i + 1), s.t1);
+      fc.load(next + S::BYTES, at(i + 1), s.t1);
     }
+    const Decays& d = dec[i & 1];
     typename Op<T>::frag cf[2][CT];
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) cf[ks][ct] = Op<T>::down(tc, LD, 32 * ks, col0 + 16 * ct);
-    add_to_state<T, D, CT>(W, cf, tb, *dec);
-    __syncthreads();
+      for (int ct = 0; ct < CT; ++ct) cf[ks][ct] = Op<T>::template down<D>(tc, c_lane[ct], ks, 0);
+    add_to_state<T, D, CT, NT>(W, cf, tb, b_lane, d);
+    if (wave == 0 && i + 1 < chunks) decays(i + 1);
   }
   float* to = a.states + ((int64_t)slot * a.HV + h) * D * D;
 #pragma unroll
   for (int kt = 0; kt < D / 16; ++kt)
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) to[(16 * kt + 4 * g + e) * D + col0 + 16 * ct + l16] = W[kt][ct][e];
+    for (int ct = 0; ct < CT; ++ct) *reinterpret_cast<f32x4*>(to + kept_at<D>(wave, kt, ct, lane)) = W[kt][ct];
   if (wave == 0) {
 #pragma unroll
     for (int by = 32; by > 0; by >>= 1) sum += __shfl_xor(sum, by);
@@ -303,18 +446,20 @@ __global__ __launch_bounds__(NTHREADS, sizeof(T) == 2 ? 2 : 1) void k_linear_sta
 
 // The states that segments start from, in place of what they add: forward from `init` (h0) at the first segment,
 // reverse from `init` (dht) at the last.
-template <bool REV>
+template <int D, bool REV>
 __global__ __launch_bounds__(256) void k_linear_scan(LinearArgs a) {
-  const int n = blockIdx.z, h = blockIdx.y, size = a.D * a.D;
-  const int e = (blockIdx.x * 256 + threadIdx.x) * 4;
-  if (e >= size) return;
+  constexpr int SIZE = D * D, AHEAD = 4;
+  const int n = blockIdx.z, h = blockIdx.y, e = (blockIdx.x * 256 + threadIdx.x) * 4;
   const int from = cut_to(a.cu[n], a.T), to = max(cut_to(a.cu[n + 1], a.T), from);
   const int count = (to - from + a.seg - 1) / a.seg, base = doc_slot(a, n);
   const auto slot = [&](int i) { return base + (REV ? count - 1 - i : i); };
-  const auto at = [&](int i) { return a.states + ((int64_t)slot(i) * a.HV + h) * size + e; };
+  const auto at = [&](int i) { return a.states + ((int64_t)slot(i) * a.HV + h) * SIZE + e; };
   f32x4 W = zero4();
-  if (a.init) W = *reinterpret_cast<const f32x4*>(a.init + ((int64_t)n * a.HV + h) * size + e);
-  constexpr int AHEAD = 4;
+  if (a.init && count > 1) {
+    const float* p = a.init + ((int64_t)n * a.HV + h) * SIZE + kept_col<D>(e);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) W[j] = p[(kept_row<D>(e) + j) * D];
+  }
   for (int i = 0; i < count; i += AHEAD) {
     f32x4 add[AHEAD];
     float dec[AHEAD];
@@ -338,101 +483,115 @@ __global__ __launch_bounds__(256) void k_linear_scan(LinearArgs a) {
 // ------------------------------------------------------------------------------------------------
 // The walk. A wave owns 16 CT columns of the state W (and of c and y) and keeps them in registers for the
 // whole segment; a chunk takes
-//   y^T  = W^T a^T, each column times its row's factor       (W's registers are the operand as they are)
 //   P    = decays * a b^T, its 16x16 tiles shared out to the waves, through LDS
-//   y^T += c^T P^T                                            (written out: 4 neighbouring columns a lane)
+//   y^T  = W^T a^T, each column times its row's factor       (W's registers are the operand as they are)
+//   -- barrier: P is whole; a's and c's tiles are free, c is in registers
+//   y^T += c^T P^T                                            (written out: 4 CT neighbouring columns a lane)
 //   W    = decay W + b^T diag(w) c
+//   -- barrier: the next tiles are there
+// Four tiles in LDS: the next a goes where the last b was, at the chunk's start; the next b and c to where a and c
+// were, after the first barrier. So each load has at least half a chunk to arrive, and two workgroups share a CU.
+//
 // P and W's operand are rounded once, to the io type: their products are summed in FP32 and the result is
-// rounded to that type itself. With `dots` (the decays' gradient, an FP32 result that is a difference of
-// sums) both go in as EXACT terms instead.
-template <typename T, int D, bool REV, bool DOTS>
-__global__ __launch_bounds__(NTHREADS, sizeof(T) == 2 ? 2 : 1) void k_linear_walk(LinearArgs a) {
-  constexpr int CT = D / 64, LD = Rows<T, D>::STRIDE, NT = DOTS ? Op<T>::EXACT : 1;
+// rounded to that type itself. With DOTS (the decays' gradient, an FP32 result that is a difference of
+// sums) both go in as EXACT terms instead. w c goes into W as EXACT terms where W is a result (DOTS, or the state that a
+// document ends with), and as 2 where it is not: that leaves 2^-17 of each term, nothing beside W's own rounding.
+template <typename T, int D>
+struct WalkLds {
+  static constexpr int P = 4 * Tile<T, D>::BYTES, P_TILE = 256;      // P: 10 tiles of 256 values
+  static constexpr int dec(int p_size) { return P + 10 * P_TILE * p_size; } // Decays of two chunks
+  static constexpr int red(int p_size) { return dec(p_size) + 2 * (int)sizeof(Decays); } // DOTS: [4 waves][64 rows]
+  static constexpr int bytes(bool dots) { return red(dots ? 4 : sizeof(T)) + (dots ? 4 * CH * 4 : 0); }
+};
+
+template <typename T, int D, bool REV, bool DOTS, int NTW, typename F>
+__device__ __forceinline__ void walk_chunks(const LinearArgs& a, const Segment& s, int h, f32x4 (&W)[D / 16][D / 64], const F& load_state) {
+  typedef Tile<T, D> S;
+  typedef Op<T> O;
+  typedef typename O::frag frag;
+  typedef WalkLds<T, D> L;
+  constexpr int CT = D / 64, NT = DOTS ? O::EXACT : 1;
   typedef typename std::conditional<DOTS, float, T>::type PT; // type of P in LDS
-  constexpr int LP = CH + Op<PT>::PADDED;
-  typedef typename Op<T>::frag frag;
-  extern __shared__ __attribute__((aligned(16))) char lds[];
-  T* ta = (T*)lds;
-  T* tb = ta + CH * LD;
-  T* tc = tb + CH * LD;
-  PT* tp = (PT*)(tc + CH * LD);
-  Decays* dec = (Decays*)(tp + CH * LP);
-  float* red = (float*)(dec + 1); // DOTS: [4 waves][64 rows]
-  int slot, h;
-  if (!place(a, &slot, &h)) return;
-  const Segment s = find_segment(a, slot);
-  if (!s.live) return;
+  typedef PT p4 __attribute__((ext_vector_type(4)));
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
-  const int col0 = wave * 16 * CT;
-  const int64_t doc_state = ((int64_t)s.doc * a.HV + h) * D * D;
-
-  // the state: rows 16 kt + 4 g + e, column col0 + 16 ct + l16; `flip`: stored with rows and columns exchanged
-  f32x4 W[D / 16][CT];
-  const bool begins = REV ? s.last : s.first;
-  const float* from = begins ? (a.init ? a.init + doc_state : nullptr) : a.states + ((int64_t)slot * a.HV + h) * D * D;
-#pragma unroll
-  for (int kt = 0; kt < D / 16; ++kt)
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-      const int row = 16 * kt + 4 * g, col = col0 + 16 * ct + l16;
-      W[kt][ct] = zero4();
-      if (from) {
-        if (a.flip) W[kt][ct] = *reinterpret_cast<const f32x4*>(from + col * D + row);
-        else
-#pragma unroll
-          for (int e = 0; e < 4; ++e) W[kt][ct][e] = from[(row + e) * D + col];
-      }
-    }
-
-  // the tiles of P beside the diagonal that products read but no wave writes
-  for (int i = threadIdx.x; i < CH * CH; i += NTHREADS) tp[(i / CH) * LP + i % CH] = (PT)0.f;
+  const int col0 = wave * 16 * CT, lds = lds_start();
+  Decays* dec = (Decays*)(linear_lds + L::dec(sizeof(PT)));
+  float* red = (float*)(linear_lds + L::red(sizeof(PT)));
+  int ta = lds, tb = lds + S::BYTES, spare = lds + 2 * S::BYTES;
+  const int tc = lds + 3 * S::BYTES;
+  const int p_lane = lds + L::P + lane * 4 * (int)sizeof(PT); // a lane reads of each tile what the same lane wrote
 
   const int chunks = (s.t1 - s.t0 + CH - 1) / CH;
   const auto at = [&](int i) { return s.t0 + (REV ? chunks - 1 - i : i) * CH; };
-  Rows<T, D> ra, rb, rc;
+  const Feed<T, D> fa(a.a, a, h, wave), fb(a.b, a, h, wave), fc(a.c, a, h, wave);
+  const int along = O::template along_lane<D>();
+  const typename O::Down b_lane = O::template down_lane<D>(0, 4);
+  typename O::Down c_lane[CT];
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) c_lane[ct] = O::template down_lane<D>(col0 + 4 * ct, 4 * CT);
   float gl = 0.f;
-  if (chunks > 0) {
-    ra.load(a.a, a, h, at(0), s.t1);
-    rb.load(a.b, a, h, at(0), s.t1);
-    rc.load(a.c, a, h, at(0), s.t1);
-    if (wave == 3) gl = log_decay(a, h, at(0) + lane, s.t1);
+  const auto decays = [&](int i) { // of chunk i, and the log decays of the next
+    chunk_decays<REV>(dec[i & 1], gl, a.in_scale, a.w_scale);
+    gl = i + 1 < chunks ? log_decay(a, h, at(i + 1) + lane, s.t1) : 0.f;
+  };
+  fa.load(ta, at(0), s.t1);
+  fb.load(tb, at(0), s.t1);
+  fc.load(tc, at(0), s.t1);
+  if (wave == 0) {
+    gl = log_decay(a, h, at(0) + lane, s.t1);
+    decays(0);
   }
+  load_state();
+  wait_loads<0>();
   for (int i = 0; i < chunks; ++i) {
     const int t = at(i), n = min(s.t1 - t, CH);
-    Decays& d = *dec;
-    ra.store(ta);
-    rb.store(tb);
-    rc.store(tc);
-    if (wave == 3) chunk_decays<REV>(d, gl, a.in_scale, a.w_scale);
+    const Decays& d = dec[i & 1];
     __syncthreads();
-    if (i + 1 < chunks) {
-      ra.load(a.a, a, h, at(i + 1), s.t1);
-      rb.load(a.b, a, h, at(i + 1), s.t1);
-      rc.load(a.c, a, h, at(i + 1), s.t1);
-      if (wave == 3) gl = log_decay(a, h, at(i + 1) + lane, s.t1);
-    }
-    // P^T: rows s, column t; tiles (tb, sb) with sb <= tb, (sb, tb) exchanged in reverse
-#pragma unroll 1
-    for (int e = wave; e < 10; e += 4) {
-      const int x = e < 1 ? 0 : e < 3 ? 1 : e < 6 ? 2 : 3, y = e - x * (x + 1) / 2;
-      const int bt = REV ? y : x, bs = REV ? x : y;
-      f32x4 p = zero4();
+    const bool more = i + 1 < chunks;
+    if (more) fa.load(spare, at(i + 1), s.t1);
+    // P^T (rows s, column t) in tiles (x, z), z <= x: forward of rows x and columns z, in reverse the other way round.
+    // Waves 0 and 1 take two of x = 3, wave 2 those of x = 2, wave 3 those of x = 1 and 0.
+    {
+      const int al = fresh(along), tx = REV ? tb : ta, tz = REV ? ta : tb;
+      const int x = wave < 2 ? 3 : 4 - wave, z = wave == 1 ? 2 : 0;
+      const auto finish = [&](const f32x4& p, int x, int z) {
+        const int tt = 16 * (REV ? z : x) + l16, ss = 16 * (REV ? x : z) + 4 * g;
+        const float th = d.hi[tt], tl = d.lo[tt];
+        const f32x4 sh = *reinterpret_cast<const f32x4*>(&d.hi[ss]), sl = *reinterpret_cast<const f32x4*>(&d.lo[ss]);
+        p4 v;
 #pragma unroll
-      for (int kk = 0; kk < D / 32; ++kk)
-        p = Op<T>::mul(Op<T>::along(tb, LD, 16 * bs + l16, 32 * kk), Op<T>::along(ta, LD, 16 * bt + l16, 32 * kk), p);
-      const int tt = 16 * bt + l16, ss = 16 * bs + 4 * g;
-      const float th = d.hi[tt], tl = d.lo[tt];
-      const f32x4 sh = *reinterpret_cast<const f32x4*>(&d.hi[ss]), sl = *reinterpret_cast<const f32x4*>(&d.lo[ss]);
-      float v[4];
+        for (int j = 0; j < 4; ++j) {
+          const float x2 = REV ? (sh[j] - th) + (sl[j] - tl) : (th - sh[j]) + (tl - sl[j]);
+          const bool keep = REV ? ss + j >= tt : ss + j <= tt;
+          v[j] = (PT)(keep ? a.p_scale * p[j] * __builtin_amdgcn_exp2f(x2) : 0.f);
+        }
+        lds_write<p4>(p_lane + (x * (x + 1) / 2 + z) * L::P_TILE * (int)sizeof(PT), v);
+      };
+      const auto tile = [&](const frag& fx, const frag& fz, const f32x4& p) { return REV ? O::mul(fx, fz, p) : O::mul(fz, fx, p); };
+      f32x4 p0 = zero4(), p1 = zero4();
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float x2 = REV ? (sh[j] - th) + (sl[j] - tl) : (th - sh[j]) + (tl - sl[j]);
-        const bool keep = REV ? ss + j >= tt : ss + j <= tt;
-        v[j] = keep ? a.p_scale * p[j] * __builtin_amdgcn_exp2f(x2) : 0.f;
+      for (int kk = 0; kk < D / 32; ++kk) {
+        const frag fx = O::template along<D>(tx, al, x, kk);
+        p0 = tile(fx, O::template along<D>(tz, al, z, kk), p0);
+        p1 = tile(fx, O::template along<D>(tz, al, z + 1, kk), p1);
       }
-      IO<PT>::store4(tp + tt * LP + ss, v);
+      finish(p0, x, z);
+      finish(p1, x, z + 1);
+      if (wave >= 2) {
+        const int m = wave == 2 ? 2 : 0;
+        f32x4 p2 = zero4();
+#pragma unroll
+        for (int kk = 0; kk < D / 32; ++kk) p2 = tile(O::template along<D>(tx, al, m, kk), O::template along<D>(tz, al, m, kk), p2);
+        finish(p2, m, m);
+      }
     }
+    frag cf[2][CT];
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) cf[ks][ct] = O::template down<D>(tc, c_lane[ct], ks, 0);
     // y^T = W^T a^T
+    const int al = fresh(along);
     f32x4 y[CT][4];
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct)
@@ -442,12 +601,14 @@ __global__ __launch_bounds__(NTHREADS, sizeof(T) == 2 ? 2 : 1) void k_linear_wal
     for (int kk = 0; kk < D / 32; ++kk) {
       frag af[4];
 #pragma unroll
-      for (int bt = 0; bt < 4; ++bt) af[bt] = Op<T>::along(ta, LD, 16 * bt + l16, 32 * kk);
+      for (int bt = 0; bt < 4; ++bt) af[bt] = O::template along<D>(ta, al, bt, kk);
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) {
         const Terms<T, NT> w(join(W[2 * kk][ct], W[2 * kk + 1][ct]));
 #pragma unroll
-        for (int bt = 0; bt < 4; ++bt) y[ct][bt] = mul_terms<T, NT>(w, af[bt], y[ct][bt]);
+        for (int m = NT - 1; m >= 0; --m)
+#pragma unroll
+          for (int bt = 0; bt < 4; ++bt) y[ct][bt] = O::mul(w.f[m], af[bt], y[ct][bt]);
       }
     }
 #pragma unroll
@@ -456,74 +617,140 @@ __global__ __launch_bounds__(NTHREADS, sizeof(T) == 2 ? 2 : 1) void k_linear_wal
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) y[ct][bt] *= f;
     }
-    frag cf[2][CT];
+    __syncthreads(); // P
+    if (more) {
+      fb.load(ta, at(i + 1), s.t1);
+      fc.load(tc, at(i + 1), s.t1);
+      if (wave == 0) decays(i + 1); // it has fewer tiles of P
+    }
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) cf[ks][ct] = Op<T>::down(tc, LD, 32 * ks, col0 + 16 * ct);
-    __syncthreads(); // P
-#pragma unroll
-    for (int bt = 0; bt < 4; ++bt)
-#pragma unroll
-      for (int ks = REV ? bt / 2 : 0; ks < (REV ? 2 : bt / 2 + 1); ++ks) {
+      for (int bt = 0; bt < 4; ++bt) {
+        if (REV ? ks < bt / 2 : ks > bt / 2) continue;
+        const auto part = [&](int bs) -> p4 { // beside the diagonal: nothing
+          if (REV ? bs < bt : bs > bt) return p4{(PT)0.f, (PT)0.f, (PT)0.f, (PT)0.f};
+          const int x = REV ? bs : bt, z = REV ? bt : bs;
+          return lds_read<p4>(p_lane + (x * (x + 1) / 2 + z) * L::P_TILE * (int)sizeof(PT));
+        };
+        const auto p8 = __builtin_shufflevector(part(2 * ks), part(2 * ks + 1), 0, 1, 2, 3, 4, 5, 6, 7);
         if constexpr (DOTS) {
-          const float* p = (const float*)tp + (16 * bt + l16) * LP + 32 * ks + 4 * g;
-          const Terms<T, NT> pf(join(*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 16)));
+          const Terms<T, NT> pf(p8);
 #pragma unroll
-          for (int ct = 0; ct < CT; ++ct) y[ct][bt] = mul_terms<T, NT>(cf[ks][ct], pf, y[ct][bt]);
+          for (int m = NT - 1; m >= 0; --m)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) y[ct][bt] = O::mul(cf[ks][ct], pf.f[m], y[ct][bt]);
         } else {
-          const frag pf = Op<T>::along((const T*)tp, LP, 16 * bt + l16, 32 * ks);
 #pragma unroll
-          for (int ct = 0; ct < CT; ++ct) y[ct][bt] = Op<T>::mul(cf[ks][ct], pf, y[ct][bt]);
+          for (int ct = 0; ct < CT; ++ct) y[ct][bt] = O::mul(cf[ks][ct], p8, y[ct][bt]);
         }
       }
-    add_to_state<T, D, CT>(W, cf, tb, d);
+    add_to_state<T, D, CT, NTW>(W, cf, tb, b_lane, d);
 
-    // y: lane (g, l16): row 16 bt + l16, columns col0 + 16 ct + 4 g .. + 3
-    const auto write = [&](auto* out) {
-      typedef typename std::remove_reference<decltype(*out)>::type O;
-      const int os = a.HV * D;
-      const __amdgpu_buffer_rsrc_t to = make_rsrc(out + (int64_t)t * os + (int64_t)h * D, ((n - 1) * os + D) * (int)sizeof(O));
-#pragma unroll
-      for (int bt = 0; bt < 4; ++bt)
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-          const int row = 16 * bt + l16;
-          const float v[4] = {y[ct][bt][0], y[ct][bt][1], y[ct][bt][2], y[ct][bt][3]};
-          if (row < n) IO<O>::bstore4(to, row * os + col0 + 16 * ct + 4 * g, v);
-        }
-    };
-    if (a.part) write(a.part);
-    else write((T*)a.out);
     if constexpr (DOTS) {
 #pragma unroll
       for (int bt = 0; bt < 4; ++bt) {
         const int row = 16 * bt + l16;
-        const T* x = (const T*)a.dot.p + (int64_t)(t + min(row, n - 1)) * a.dot.stride + (int64_t)(a.dot.shared ? h / a.G : h) * D + col0 + 4 * g;
+        const T* x = (const T*)a.dot.p + (int64_t)(t + min(row, n - 1)) * a.dot.stride + (int64_t)(a.dot.shared ? h / a.G : h) * D + col0 + 4 * CT * g;
         float sum = 0.f;
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sum = __builtin_fmaf((float)x[16 * ct + e], y[ct][bt][e], sum);
+          for (int e = 0; e < 4; ++e) sum = __builtin_fmaf((float)x[4 * ct + e], y[ct][bt][e], sum);
         sum = col_sum4(sum);
         if (g == 0) red[wave * CH + row] = sum;
       }
     }
-    __syncthreads();
+    // y: lane (g, l16): row 16 bt + l16, columns col0 + 4 CT g ..; rows past the end lie past the buffer's, which drops them
+    const auto write = [&](auto* out) {
+      typedef typename std::remove_reference<decltype(*out)>::type Y;
+      const int os = a.HV * D;
+      const __amdgpu_buffer_rsrc_t to = make_rsrc(out + (int64_t)t * os + (int64_t)h * D, ((n - 1) * os + D) * (int)sizeof(Y));
+      int off = (l16 * os + col0 + 4 * CT * g) * (int)sizeof(Y);
+#pragma unroll
+      for (int bt = 0; bt < 4; ++bt, off += 16 * os * (int)sizeof(Y)) {
+        if constexpr (CT == 2 && sizeof(Y) == 2) {
+          bf16x8 v;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = (bf16)y[e >> 2][bt][e & 3];
+          buf_store16(v, to, off);
+        } else {
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) {
+            const float v[4] = {y[ct][bt][0], y[ct][bt][1], y[ct][bt][2], y[ct][bt][3]};
+            IO<Y>::bstore4(to, off / (int)sizeof(Y) + 4 * ct, v);
+          }
+        }
+      }
+    };
+    if (a.part) {
+      write(a.part);
+      wait_loads<4 * CT>(); // the next tiles, not these stores
+    } else {
+      write((T*)a.out);
+      wait_loads<CT == 2 && sizeof(T) == 2 ? 4 : 4 * CT>();
+    }
     if constexpr (DOTS) {
+      __syncthreads();
       if ((int)threadIdx.x < n)
         a.dots[(int64_t)h * a.T + t + threadIdx.x] =
             (red[threadIdx.x] + red[CH + threadIdx.x]) + (red[2 * CH + threadIdx.x] + red[3 * CH + threadIdx.x]);
     }
+    const int used = tb;
+    tb = ta;
+    ta = spare;
+    spare = used;
   }
-  if ((REV ? s.first : s.last) && a.fin) {
+}
+
+template <typename T, int D, bool REV, bool DOTS>
+__global__ __launch_bounds__(NTHREADS, sizeof(T) == 2 ? 2 : 1) void k_linear_walk(LinearArgs a) {
+  constexpr int CT = D / 64, EXACT = Op<T>::EXACT;
+  int slot, h;
+  if (!place(a, &slot, &h)) return;
+  const Segment s = find_segment(a, slot);
+  if (!s.live) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+  const int col0 = wave * 16 * CT;
+  const int64_t doc_state = ((int64_t)s.doc * a.HV + h) * D * D;
+  const bool begins = REV ? s.last : s.first, ends = (REV ? s.first : s.last) && a.fin;
+
+  // the state: rows 16 kt + 4 g + e, the lane's columns; `flip`: kept with rows and columns exchanged
+  f32x4 W[D / 16][CT];
+  const float* init = begins ? (a.init ? a.init + doc_state : nullptr) : nullptr;
+  const float* kept = begins ? nullptr : a.states + ((int64_t)slot * a.HV + h) * D * D;
+  const auto load_state = [&] {
+#pragma unroll
+    for (int kt = 0; kt < D / 16; ++kt)
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        const int row = 16 * kt + 4 * g, col = column<CT>(col0, ct, l16);
+        W[kt][ct] = zero4();
+        if (kept) {
+          if (!a.flip) W[kt][ct] = *reinterpret_cast<const f32x4*>(kept + kept_at<D>(wave, kt, ct, lane));
+          else
+#pragma unroll
+            for (int e = 0; e < 4; ++e) W[kt][ct][e] = kept[kept_of<D>(col, row + e)];
+        } else if (init) {
+          if (a.flip) W[kt][ct] = *reinterpret_cast<const f32x4*>(init + col * D + row);
+          else
+#pragma unroll
+            for (int e = 0; e < 4; ++e) W[kt][ct][e] = init[(row + e) * D + col];
+        }
+      }
+  };
+  if (s.t0 < s.t1) {
+    if (DOTS || EXACT == 1 || ends) walk_chunks<T, D, REV, DOTS, EXACT>(a, s, h, W, load_state);
+    else if constexpr (!DOTS && EXACT > 1) walk_chunks<T, D, REV, DOTS, 2>(a, s, h, W, load_state);
+  } else load_state();
+  if (ends) {
     float* to = a.fin + doc_state;
 #pragma unroll
     for (int kt = 0; kt < D / 16; ++kt)
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) to[(16 * kt + 4 * g + e) * D + col0 + 16 * ct + l16] = W[kt][ct][e];
+        for (int e = 0; e < 4; ++e) to[(16 * kt + 4 * g + e) * D + column<CT>(col0, ct, l16)] = W[kt][ct][e];
   }
 }
 
@@ -642,7 +869,7 @@ static int ask_lds(const void* kernel, unsigned lds, std::atomic<uint64_t>& aske
 
 template <typename T, int D, bool REV>
 static int states_t(const LinearArgs& a, hipStream_t s) {
-  constexpr unsigned lds = 2 * CH * Rows<T, D>::STRIDE * sizeof(T) + sizeof(Decays);
+  constexpr unsigned lds = 4 * Tile<T, D>::BYTES + 2 * sizeof(Decays);
   static std::atomic<uint64_t> asked{0};
   if (const int e = ask_lds(reinterpret_cast<const void*>(&k_linear_states<T, D, REV>), lds, asked)) return e;
   hipLaunchKernelGGL((k_linear_states<T, D, REV>), dim3(place_blocks(a)), dim3(NTHREADS), lds, s, a);
@@ -654,9 +881,7 @@ static int states_td(const LinearArgs& a, bool rev, hipStream_t s) {
 }
 template <typename T, int D, bool REV, bool DOTS>
 static int walk_t(const LinearArgs& a, hipStream_t s) {
-  constexpr unsigned lds = 3 * CH * Rows<T, D>::STRIDE * sizeof(T) +
-                           (DOTS ? CH * (CH + Op<float>::PADDED) * 4 : CH * (CH + Op<T>::PADDED) * (unsigned)sizeof(T)) +
-                           sizeof(Decays) + (DOTS ? 4 * CH * 4 : 0);
+  constexpr unsigned lds = WalkLds<T, D>::bytes(DOTS);
   static std::atomic<uint64_t> asked{0};
   if (const int e = ask_lds(reinterpret_cast<const void*>(&k_linear_walk<T, D, REV, DOTS>), lds, asked)) return e;
   hipLaunchKernelGGL((k_linear_walk<T, D, REV, DOTS>), dim3(place_blocks(a)), dim3(NTHREADS), lds, s, a);
@@ -676,9 +901,14 @@ int launch_linear_states(const LinearArgs& a, bool rev, int dtype, void* stream)
 
 int launch_linear_scan(const LinearArgs& a, bool rev, void* stream) {
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  const dim3 grid((unsigned)((a.D * a.D + 1023) / 1024), (unsigned)a.HV, (unsigned)a.N);
-  if (rev) hipLaunchKernelGGL(k_linear_scan<true>, grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL(k_linear_scan<false>, grid, dim3(256), 0, s, a);
+  const dim3 grid((unsigned)(a.D * a.D / 1024), (unsigned)a.HV, (unsigned)a.N);
+  if (a.D == 128) {
+    if (rev) hipLaunchKernelGGL((k_linear_scan<128, true>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_linear_scan<128, false>), grid, dim3(256), 0, s, a);
+  } else {
+    if (rev) hipLaunchKernelGGL((k_linear_scan<64, true>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_linear_scan<64, false>), grid, dim3(256), 0, s, a);
+  }
   return (int)hipGetLastError();
 }
 
