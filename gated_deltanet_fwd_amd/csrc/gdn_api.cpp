@@ -1451,7 +1451,7 @@ int linear_segment(const gdn_linear_problem* p) {
 
 struct LinearLayout {
   int seg, slots;
-  size_t S, D, Sdecay, Ddecay, qdots, kdots, sums, part, total;
+  size_t S, D, Sdecay, Ddecay, worth, qdots, kdots, sums, part[2], total;
 };
 
 int linear_layout(const gdn_linear_problem* p, int op, LinearLayout* L) {
@@ -1475,11 +1475,13 @@ int linear_layout(const gdn_linear_problem* p, int op, LinearLayout* L) {
     if (L->seg) {
       L->D = take(states);
       L->Ddecay = take((size_t)slots * p->h_v * 4);
+      L->worth = take(states / 1024 * 2);
     }
     L->qdots = take(rows);
     L->kdots = take(rows);
     L->sums = take((size_t)slots * p->h_v * 8);
-    if (p->h_v != p->h_qk) L->part = take(rows * p->d);
+    for (size_t& part : L->part)
+      if (p->h_v != p->h_qk) part = take(rows * p->d);
   }
   L->total = std::max(off, kAlign);
   return GDN_OK;
@@ -1567,13 +1569,15 @@ int gdn_linear_fwd(const gdn_linear_problem* p, const void* q, const void* k, co
   a.states = (float*)(w + L.S);
   a.decay = (float*)(w + L.Sdecay);
   if (L.seg) {
-    LAUNCH("gdn_linear_states", gdn::launch_linear_states(a, false, p->dtype, stream));
-    LAUNCH("gdn_linear_scan", gdn::launch_linear_scan(a, false, stream));
+    gdn::LinearJobs j;
+    j.job[0] = a;
+    LAUNCH("gdn_linear_states", gdn::launch_linear_states(j, 1, p->dtype, stream));
+    LAUNCH("gdn_linear_scan", gdn::launch_linear_scan(a, false, nullptr, nullptr, stream));
   }
   a.p_scale = a.in_scale = p->scale;
   a.fin = ht;
   a.out = o;
-  LAUNCH("gdn_linear_walk", gdn::launch_linear_walk(a, false, p->dtype, stream));
+  LAUNCH("gdn_linear_walk", gdn::launch_linear_walk(a, p->dtype, stream));
   g_err.clear();
   return GDN_OK;
 }
@@ -1601,7 +1605,7 @@ int gdn_linear_bwd(const gdn_linear_problem* p, const void* q, const void* k, co
   char* w = (char*)workspace;
   const int dt = p->dtype;
   const gdn::LinearSide d_out = {dO, (int64_t)p->h_v * p->d, 0};
-  float* part = p->h_v != p->h_qk ? (float*)(w + L.part) : nullptr;
+  const bool shared = p->h_v != p->h_qk;
   gdn::LinearArgs f = c.base, r = c.base; // forward and in reverse
   f.init = h0;
   f.states = (float*)(w + L.S);
@@ -1610,61 +1614,48 @@ int gdn_linear_bwd(const gdn_linear_problem* p, const void* q, const void* k, co
   r.states = (float*)(w + L.D);
   r.decay = (float*)(w + L.Ddecay);
   r.w_scale = p->scale;
+  gdn::LinearJobs j;
   if (L.seg) {
-    f.b = c.k;
-    f.c = c.v;
-    LAUNCH("gdn_linear_states", gdn::launch_linear_states(f, false, dt, stream));
-    r.b = c.q;
-    r.c = d_out;
-    LAUNCH("gdn_linear_states", gdn::launch_linear_states(r, true, dt, stream));
-    LAUNCH("gdn_linear_scan", gdn::launch_linear_scan(f, false, stream));
-    LAUNCH("gdn_linear_scan", gdn::launch_linear_scan(r, true, stream));
+    j.job[0] = f;
+    j.job[0].b = c.k;
+    j.job[0].c = c.v;
+    j.job[1] = r;
+    j.job[1].b = c.q;
+    j.job[1].c = d_out;
+    LAUNCH("gdn_linear_states", gdn::launch_linear_states(j, 2, dt, stream));
+    LAUNCH("gdn_linear_scan", gdn::launch_linear_scan(f, false, nullptr, nullptr, stream));
+    LAUNCH("gdn_linear_scan", gdn::launch_linear_scan(r, true, f.states, dg ? (double*)(w + L.worth) : nullptr, stream));
   }
-  // dq
-  gdn::LinearArgs a = f;
-  a.a = d_out;
-  a.b = c.v;
-  a.c = c.k;
-  a.flip = 1;
-  a.p_scale = a.in_scale = p->scale;
-  a.out = dq;
-  a.part = part;
-  if (dg) {
-    a.dot = c.q;
-    a.dots = (float*)(w + L.qdots);
+  const auto product = [&](gdn::LinearArgs& a, const gdn::LinearArgs& base, const gdn::LinearSide& x, const gdn::LinearSide& y,
+                           const gdn::LinearSide& z, void* out) {
+    a = base;
+    a.a = x;
+    a.b = y;
+    a.c = z;
+    a.p_scale = p->scale;
+    a.out = out;
+  };
+  product(j.job[0], f, d_out, c.v, c.k, dq);
+  j.job[0].in_scale = p->scale;
+  product(j.job[1], r, c.v, d_out, c.q, dk);
+  product(j.job[2], r, c.k, c.q, d_out, dv);
+  j.job[2].fin = dh0;
+  for (int i = 0; i < 2; ++i) {
+    gdn::LinearArgs& a = j.job[i];
+    a.flip = 1;
+    if (shared) a.part = (float*)(w + L.part[i]);
+    if (dg) {
+      a.dot = i == 0 ? c.q : c.k;
+      a.dots = (float*)(w + (i == 0 ? L.qdots : L.kdots));
+    }
   }
-  LAUNCH("gdn_linear_walk", gdn::launch_linear_walk(a, false, dt, stream));
-  if (part) LAUNCH("gdn_linear_group_sum", gdn::launch_linear_group_sum(a, dt, stream));
-  // dk
-  a = r;
-  a.a = c.v;
-  a.b = d_out;
-  a.c = c.q;
-  a.flip = 1;
-  a.p_scale = p->scale;
-  a.out = dk;
-  a.part = part;
-  if (dg) {
-    a.dot = c.k;
-    a.dots = (float*)(w + L.kdots);
-  }
-  LAUNCH("gdn_linear_walk", gdn::launch_linear_walk(a, true, dt, stream));
-  if (part) LAUNCH("gdn_linear_group_sum", gdn::launch_linear_group_sum(a, dt, stream));
-  // dv and dh0
-  a = r;
-  a.a = c.k;
-  a.b = c.q;
-  a.c = d_out;
-  a.p_scale = p->scale;
-  a.out = dv;
-  a.fin = dh0;
-  LAUNCH("gdn_linear_walk", gdn::launch_linear_walk(a, true, dt, stream));
+  LAUNCH("gdn_linear_walks", gdn::launch_linear_walks(j, dt, stream));
+  if (shared) LAUNCH("gdn_linear_group_sum", gdn::launch_linear_group_sum(j, dt, stream));
   if (dg) {
     gdn::LinearDgArgs d;
     std::memset(&d, 0, sizeof d);
     d.a = c.base;
-    d.S = (const float*)(w + L.S);
-    d.D = (const float*)(w + L.D);
+    d.worth = (const double*)(w + L.worth);
     d.h0 = h0;
     d.dh0 = dh0;
     d.dht = dht;
@@ -1865,6 +1856,12 @@ int gdn_step_maps(const gdn_step_maps_problem* p, const int32_t* lengths, const 
   a.block = p->block;
   a.max_blocks = p->max_blocks;
   a.n_free = p->n_free;
+  // with k the smallest power of two's exponent that reaches block, 2^(31 + k) / block rounded up has 32 bits, and is off
+  // by less than 2^k / 2^(31 + k) of a whole for each unit of x
+  int k = 0;
+  while (((int64_t)1 << k) < p->block) ++k;
+  a.block_shift = 31 + k;
+  a.block_mul = (unsigned)((((uint64_t)1 << a.block_shift) + p->block - 1) / p->block);
   a.lengths = lengths;
   a.contexts = contexts;
   a.table = block_table;

@@ -254,18 +254,22 @@ struct LinearArgs {
   float* part;       // [T, HV, d] y in f32, before those sums; NULL: y goes to out
   float* dots;       // [HV, T], or NULL
 };
+struct LinearJobs { // products that one launch makes: forward and reverse states; dq, dk and dv
+  LinearArgs job[3];
+};
 struct LinearDgArgs {
   LinearArgs a;                // sizes, g, cu, slots
-  const float *S, *D;          // scanned states and their gradients, [slots, HV, d, d]
+  const double* worth;         // [slots, HV, d d / 1024] parts of <S, D> behind each segment but the last of a document
   const float *h0, *dh0, *dht; // NULL where not given
   const float *qdots, *kdots;  // [HV, T]
   double* sums;                // [slots, HV] (one decay a head)
   float* dg;                   // [T, HV], or [HV]
 };
-int launch_linear_states(const LinearArgs& a, bool rev, int dtype, void* stream);
-int launch_linear_scan(const LinearArgs& a, bool rev, void* stream);
-int launch_linear_walk(const LinearArgs& a, bool rev, int dtype, void* stream);
-int launch_linear_group_sum(const LinearArgs& a, int dtype, void* stream);
+int launch_linear_states(const LinearJobs& j, int n, int dtype, void* stream); // n = 1: forward; 2: and reverse
+int launch_linear_scan(const LinearArgs& a, bool rev, const float* other, double* worth, void* stream);
+int launch_linear_walk(const LinearArgs& a, int dtype, void* stream);
+int launch_linear_walks(const LinearJobs& j, int dtype, void* stream);
+int launch_linear_group_sum(const LinearJobs& j, int dtype, void* stream);
 int launch_linear_dg(const LinearDgArgs& d, void* stream);
 
 // Its serving step (gdn_linear_step.hip). `longest` and `live` by the host's lengths.
@@ -310,6 +314,9 @@ int launch_norm_bwd(const NormArgs& a, int dtype, void* stream);
 // What a serving step reads, from the requests' lengths (gdn_maps.hip).
 struct MapsArgs {
   int N, T, block, max_blocks, n_free;
+  unsigned block_mul; // x / block = x block_mul >> block_shift, for x below 2^31
+  int block_shift;
+  int fill; // set by the launch: tokens are filled
   const int32_t *lengths, *contexts, *free_list, *free_count;
   int32_t *table, *contexts_out, *free_count_out;
   int32_t *cu, *positions, *granted, *slot_in, *slot_out, *slot_tok;

@@ -223,8 +223,8 @@ __device__ __forceinline__ Segment find_segment(const LinearArgs& a, int slot) {
 
 // Workgroup -> (slot, value head). Workgroups go to the 8 XCDs in turn; the heads of one group, which read the
 // same shared rows, are placed 8 apart and so on one XCD.
-__device__ __forceinline__ bool place(const LinearArgs& a, int* slot, int* h) {
-  const int b = blockIdx.x, per = 8 * a.G;
+__device__ __forceinline__ bool place(const LinearArgs& a, int b, int* slot, int* h) {
+  const int per = 8 * a.G;
   const int sg = b / per, rem = b - sg * per;
   const int group = sg * 8 + (rem & 7);
   *slot = group / a.H;
@@ -379,12 +379,12 @@ __device__ __forceinline__ int lds_start() { return (int)(uintptr_t)(lds_char*)l
 // is left out: no other starts from it. w c goes in as EXACT terms: the states are results in FP32, and
 // everything after them is made from them.
 template <typename T, int D, bool REV>
-__global__ __launch_bounds__(NTHREADS, sizeof(T) == 2 ? 2 : 1) void k_linear_states(LinearArgs a) {
+__device__ __forceinline__ void segment_state(const LinearArgs& a, int block) {
   typedef Tile<T, D> S;
   constexpr int CT = D / 64, NT = Op<T>::EXACT;
   Decays* dec = (Decays*)(linear_lds + 4 * S::BYTES); // of two chunks
   int slot, h;
-  if (!place(a, &slot, &h)) return;
+  if (!place(a, block, &slot, &h)) return;
   const Segment s = find_segment(a, slot);
   if (!s.live || (REV ? s.first : s.last)) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
@@ -444,16 +444,34 @@ __global__ __launch_bounds__(NTHREADS, sizeof(T) == 2 ? 2 : 1) void k_linear_sta
   }
 }
 
+// Forward and, behind it in the same launch (`blocks` workgroups each), reverse.
+template <typename T, int D>
+__global__ __launch_bounds__(NTHREADS, sizeof(T) == 2 ? 2 : 1) void k_linear_states(LinearJobs j, int blocks) {
+  if ((int)blockIdx.x < blocks) segment_state<T, D, false>(j.job[0], blockIdx.x);
+  else segment_state<T, D, true>(j.job[1], blockIdx.x - blocks);
+}
+
+__device__ __forceinline__ double block_sum(double x, double* tmp) { // over 256 threads
+#pragma unroll
+  for (int by = 32; by > 0; by >>= 1) x += __shfl_xor(x, by);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = x;
+  __syncthreads();
+  return (tmp[0] + tmp[1]) + (tmp[2] + tmp[3]);
+}
+
 // The states that segments start from, in place of what they add: forward from `init` (h0) at the first segment,
-// reverse from `init` (dht) at the last.
+// reverse from `init` (dht) at the last. In reverse, with `worth`: also this workgroup's part of <S, D> at the borders
+// between segments, where S (`other`, from the forward scan) meets its gradient; see k_linear_dg.
 template <int D, bool REV>
-__global__ __launch_bounds__(256) void k_linear_scan(LinearArgs a) {
-  constexpr int SIZE = D * D, AHEAD = 4;
+__global__ __launch_bounds__(256) void k_linear_scan(LinearArgs a, const float* other, double* worth) {
+  constexpr int SIZE = D * D, PARTS = SIZE / 1024, AHEAD = 4;
+  __shared__ double tmp[4];
   const int n = blockIdx.z, h = blockIdx.y, e = (blockIdx.x * 256 + threadIdx.x) * 4;
   const int from = cut_to(a.cu[n], a.T), to = max(cut_to(a.cu[n + 1], a.T), from);
   const int count = (to - from + a.seg - 1) / a.seg, base = doc_slot(a, n);
   const auto slot = [&](int i) { return base + (REV ? count - 1 - i : i); };
-  const auto at = [&](int i) { return a.states + ((int64_t)slot(i) * a.HV + h) * SIZE + e; };
+  const auto index = [&](int slot) { return ((int64_t)slot * a.HV + h) * SIZE + e; };
   f32x4 W = zero4();
   if (a.init && count > 1) {
     const float* p = a.init + ((int64_t)n * a.HV + h) * SIZE + kept_col<D>(e);
@@ -461,20 +479,28 @@ __global__ __launch_bounds__(256) void k_linear_scan(LinearArgs a) {
     for (int j = 0; j < 4; ++j) W[j] = p[(kept_row<D>(e) + j) * D];
   }
   for (int i = 0; i < count; i += AHEAD) {
-    f32x4 add[AHEAD];
+    f32x4 add[AHEAD], meets[AHEAD];
     float dec[AHEAD];
 #pragma unroll
     for (int j = 0; j < AHEAD; ++j) {
-      add[j] = zero4();
+      add[j] = meets[j] = zero4();
       dec[j] = 0.f;
       if (i + j < count - 1) {
-        add[j] = *reinterpret_cast<const f32x4*>(at(i + j));
+        add[j] = *reinterpret_cast<const f32x4*>(a.states + index(slot(i + j)));
         dec[j] = a.decay[(int64_t)slot(i + j) * a.HV + h];
       }
+      if (REV && worth && i + j < count && i + j > 0) meets[j] = *reinterpret_cast<const f32x4*>(other + index(slot(i + j) + 1));
     }
 #pragma unroll
     for (int j = 0; j < AHEAD; ++j) {
-      if (i + j < count && i + j > 0) *reinterpret_cast<f32x4*>(at(i + j)) = W;
+      if (i + j < count && i + j > 0) {
+        *reinterpret_cast<f32x4*>(a.states + index(slot(i + j))) = W;
+        if (REV && worth) {
+          const f32x4 S = meets[j];
+          const double x = block_sum(((double)S[0] * W[0] + (double)S[1] * W[1]) + ((double)S[2] * W[2] + (double)S[3] * W[3]), tmp);
+          if (threadIdx.x == 0) worth[((int64_t)slot(i + j) * a.HV + h) * PARTS + blockIdx.x] = x;
+        }
+      }
       W = W * dec[j] + add[j];
     }
   }
@@ -704,10 +730,10 @@ __device__ __forceinline__ void walk_chunks(const LinearArgs& a, const Segment& 
 }
 
 template <typename T, int D, bool REV, bool DOTS>
-__global__ __launch_bounds__(NTHREADS, sizeof(T) == 2 ? 2 : 1) void k_linear_walk(LinearArgs a) {
+__device__ __forceinline__ void segment_walk(const LinearArgs& a, int block) {
   constexpr int CT = D / 64, EXACT = Op<T>::EXACT;
   int slot, h;
-  if (!place(a, &slot, &h)) return;
+  if (!place(a, block, &slot, &h)) return;
   const Segment s = find_segment(a, slot);
   if (!s.live) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
@@ -754,10 +780,24 @@ __global__ __launch_bounds__(NTHREADS, sizeof(T) == 2 ? 2 : 1) void k_linear_wal
   }
 }
 
+template <typename T, int D>
+__global__ __launch_bounds__(NTHREADS, sizeof(T) == 2 ? 2 : 1) void k_linear_walk(LinearArgs a) {
+  segment_walk<T, D, false, false>(a, blockIdx.x);
+}
+// The backward's three in one launch, `blocks` workgroups each: dq, dk, dv.
+template <typename T, int D, bool DOTS>
+__global__ __launch_bounds__(NTHREADS, sizeof(T) == 2 ? 2 : 1) void k_linear_walks(LinearJobs j, int blocks) {
+  const int b = blockIdx.x;
+  if (b < blocks) segment_walk<T, D, false, DOTS>(j.job[0], b);
+  else if (b < 2 * blocks) segment_walk<T, D, true, DOTS>(j.job[1], b - blocks);
+  else segment_walk<T, D, true, false>(j.job[2], b - 2 * blocks);
+}
+
 // ------------------------------------------------------------------------------------------------
-// Sum over the value heads of a group, in their order: part f32 [T, HV, D] -> out [T, H, D]
+// Sums over the value heads of a group, in their order: part f32 [T, HV, D] -> out [T, H, D], for dq and dk
 template <typename T>
-__global__ __launch_bounds__(256) void k_linear_group_sum(LinearArgs a) {
+__global__ __launch_bounds__(256) void k_linear_group_sum(LinearJobs jobs) {
+  const LinearArgs& a = jobs.job[blockIdx.y];
   const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, n = (int64_t)a.T * a.H * a.D;
   if (i >= n) return;
   const int64_t head = i / a.D, col = i - head * a.D;
@@ -769,52 +809,48 @@ __global__ __launch_bounds__(256) void k_linear_group_sum(LinearArgs a) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// The decays' gradient. Summed over a whole document the differences q.dq - k.dk would lose what is left of
-// them, so each segment starts again from its border, where the gradient is <S, D> of the state there and its
-// own gradient, both at hand: dg_t = <S_end, D_end> + sum_{s >= t} (q_s.dq_s - k_s.dk_s). A document's last segment has no
-// S_end: without dht its D_end is 0; with it the sum runs from the segment's start instead, where S_0 = 0 or
-// both S_0 and D_0 are at hand: dg_t = <S_0, D_0> - sum_{s < t} (q_s.dq_s - k_s.dk_s).
-__device__ __forceinline__ double block_sum(double x, double* tmp) {
-#pragma unroll
-  for (int by = 32; by > 0; by >>= 1) x += __shfl_xor(x, by);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = x;
-  __syncthreads();
-  return (tmp[0] + tmp[1]) + (tmp[2] + tmp[3]);
-}
+// The decays' gradient. The differences q.dq - k.dk cancel to a large part, and summed over a whole document their
+// roundings would outgrow what is left. So each segment is summed by itself, between borders where the gradient is known
+// apart from those sums: it is <S, D> of the state there and its own gradient, which the scan in reverse has summed. With
+// n tokens, sums from the end and E = <S, D> at the end, dg_t = E + sum_{s >= t} (q_s.dq_s - k_s.dk_s), and at the first
+// token that has to be <S, D> at the start: what it misses is spread evenly over the tokens, which leaves a
+// third of the roundings. At a document's start S is h0 or 0; at its end D is 0, or with dht S is not at hand, and
+// the sum runs from the start alone.
 __global__ __launch_bounds__(256) void k_linear_dg(LinearDgArgs d) {
   const LinearArgs& a = d.a;
   __shared__ double tmp[4], carry[4];
-  const int slot = blockIdx.x, h = blockIdx.y, size = a.D * a.D;
+  const int slot = blockIdx.x, h = blockIdx.y, size = a.D * a.D, parts = size / 1024;
   const Segment s = find_segment(a, slot);
-  const auto state = [&](const float* base, int64_t at) { return base + (at * a.HV + h) * size; };
-  const float *x = nullptr, *y = nullptr; // S and D at the border
-  bool from_end = true;
-  if (s.live) {
-    if (!s.last) {
-      x = state(d.S, slot + 1);
-      y = state(d.D, slot);
-    } else if (d.dht) {
-      from_end = false;
-      if (s.i > 0) {
-        x = state(d.S, slot);
-        y = state(d.D, slot - 1);
-      } else if (d.h0) {
-        x = state(d.h0, s.doc);
-        y = state(d.dh0, s.doc);
-      }
-    }
-  }
-  double f = 0.0;
-  if (x)
-    for (int e = threadIdx.x * 4; e < size; e += 1024) {
-      const f32x4 u = *reinterpret_cast<const f32x4*>(x + e), v = *reinterpret_cast<const f32x4*>(y + e);
-      f += ((double)u[0] * v[0] + (double)u[1] * v[1]) + ((double)u[2] * v[2] + (double)u[3] * v[3]);
-    }
-  f = block_sum(f, tmp);
-  double all = 0.0; // one decay a head: the sum of dg over the segment
   const int n = s.live ? s.t1 - s.t0 : 0;
   const float *qd = d.qdots + (int64_t)h * a.T + s.t0, *kd = d.kdots + (int64_t)h * a.T + s.t0;
+  const auto border = [&](int slot) { // behind that segment
+    double x = 0.0;
+    if ((int)threadIdx.x < parts) x = d.worth[((int64_t)slot * a.HV + h) * parts + threadIdx.x];
+    return block_sum(x, tmp);
+  };
+  double start = 0.0, end = 0.0, all = 0.0;
+  bool from_end = true;
+  if (n > 0) {
+    if (!s.first) start = border(slot - 1);
+    else if (d.h0) {
+      const int64_t at = ((int64_t)s.doc * a.HV + h) * size;
+      double x = 0.0;
+      for (int e = threadIdx.x * 4; e < size; e += 1024) {
+        const f32x4 u = *reinterpret_cast<const f32x4*>(d.h0 + at + e), v = *reinterpret_cast<const f32x4*>(d.dh0 + at + e);
+        x += ((double)u[0] * v[0] + (double)u[1] * v[1]) + ((double)u[2] * v[2] + (double)u[3] * v[3]);
+      }
+      start = block_sum(x, tmp);
+    }
+    if (!s.last) end = border(slot);
+    from_end = !(s.last && d.dht);
+  }
+  double spread = 0.0; // what each token takes of what is missed
+  if (from_end && n > 0) {
+    double x = 0.0;
+    for (int t = threadIdx.x; t < n; t += 256) x += (double)qd[t] - (double)kd[t];
+    spread = (start - (end + block_sum(x, tmp))) / n;
+  }
+  double f = from_end ? end : start;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   for (int c = 0; c < n; c += 256) { // from the border inwards
     const int j = c + (int)threadIdx.x, t = from_end ? n - 1 - j : j;
@@ -830,7 +866,7 @@ __global__ __launch_bounds__(256) void k_linear_dg(LinearDgArgs d) {
       before += w < wave ? carry[w] : 0.0;
       turn += carry[w];
     }
-    const double v = from_end ? f + before + p : f - before - (p - own);
+    const double v = from_end ? f + before + p + spread * (j + 1) : f - before - (p - own);
     if (j < n) {
       if (a.gs) d.dg[(int64_t)(s.t0 + t) * a.HV + h] = (float)v;
       all += v;
@@ -838,7 +874,7 @@ __global__ __launch_bounds__(256) void k_linear_dg(LinearDgArgs d) {
     f += from_end ? turn : -turn;
     __syncthreads();
   }
-  if (a.gs == 0) {
+  if (a.gs == 0) { // one decay a head: the sum of dg over the segment
     all = block_sum(all, tmp);
     if (threadIdx.x == 0) d.sums[(int64_t)slot * a.HV + h] = all;
   }
@@ -867,63 +903,77 @@ static int ask_lds(const void* kernel, unsigned lds, std::atomic<uint64_t>& aske
   return 0;
 }
 
-template <typename T, int D, bool REV>
-static int states_t(const LinearArgs& a, hipStream_t s) {
+template <typename T, int D>
+static int states_t(const LinearJobs& j, int n, hipStream_t s) {
   constexpr unsigned lds = 4 * Tile<T, D>::BYTES + 2 * sizeof(Decays);
   static std::atomic<uint64_t> asked{0};
-  if (const int e = ask_lds(reinterpret_cast<const void*>(&k_linear_states<T, D, REV>), lds, asked)) return e;
-  hipLaunchKernelGGL((k_linear_states<T, D, REV>), dim3(place_blocks(a)), dim3(NTHREADS), lds, s, a);
+  if (const int e = ask_lds(reinterpret_cast<const void*>(&k_linear_states<T, D>), lds, asked)) return e;
+  const unsigned blocks = place_blocks(j.job[0]);
+  hipLaunchKernelGGL((k_linear_states<T, D>), dim3(blocks * n), dim3(NTHREADS), lds, s, j, (int)blocks);
   return (int)hipGetLastError();
 }
 template <typename T, int D>
-static int states_td(const LinearArgs& a, bool rev, hipStream_t s) {
-  return rev ? states_t<T, D, true>(a, s) : states_t<T, D, false>(a, s);
-}
-template <typename T, int D, bool REV, bool DOTS>
 static int walk_t(const LinearArgs& a, hipStream_t s) {
+  constexpr unsigned lds = WalkLds<T, D>::bytes(false);
+  static std::atomic<uint64_t> asked{0};
+  if (const int e = ask_lds(reinterpret_cast<const void*>(&k_linear_walk<T, D>), lds, asked)) return e;
+  hipLaunchKernelGGL((k_linear_walk<T, D>), dim3(place_blocks(a)), dim3(NTHREADS), lds, s, a);
+  return (int)hipGetLastError();
+}
+template <typename T, int D, bool DOTS>
+static int walks_t(const LinearJobs& j, hipStream_t s) {
   constexpr unsigned lds = WalkLds<T, D>::bytes(DOTS);
   static std::atomic<uint64_t> asked{0};
-  if (const int e = ask_lds(reinterpret_cast<const void*>(&k_linear_walk<T, D, REV, DOTS>), lds, asked)) return e;
-  hipLaunchKernelGGL((k_linear_walk<T, D, REV, DOTS>), dim3(place_blocks(a)), dim3(NTHREADS), lds, s, a);
+  if (const int e = ask_lds(reinterpret_cast<const void*>(&k_linear_walks<T, D, DOTS>), lds, asked)) return e;
+  const unsigned blocks = place_blocks(j.job[0]);
+  hipLaunchKernelGGL((k_linear_walks<T, D, DOTS>), dim3(3 * blocks), dim3(NTHREADS), lds, s, j, (int)blocks);
   return (int)hipGetLastError();
 }
 template <typename T, int D>
-static int walk_td(const LinearArgs& a, bool rev, hipStream_t s) {
-  if (rev) return a.dots ? walk_t<T, D, true, true>(a, s) : walk_t<T, D, true, false>(a, s);
-  return a.dots ? walk_t<T, D, false, true>(a, s) : walk_t<T, D, false, false>(a, s);
+static int walks_td(const LinearJobs& j, hipStream_t s) {
+  return j.job[0].dots ? walks_t<T, D, true>(j, s) : walks_t<T, D, false>(j, s);
 }
 
-int launch_linear_states(const LinearArgs& a, bool rev, int dtype, void* stream) {
+int launch_linear_states(const LinearJobs& j, int n, int dtype, void* stream) {
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  if (dtype == 0) return a.D == 128 ? states_td<bf16, 128>(a, rev, s) : states_td<bf16, 64>(a, rev, s);
-  return a.D == 128 ? states_td<float, 128>(a, rev, s) : states_td<float, 64>(a, rev, s);
+  const bool wide = j.job[0].D == 128;
+  if (dtype == 0) return wide ? states_t<bf16, 128>(j, n, s) : states_t<bf16, 64>(j, n, s);
+  return wide ? states_t<float, 128>(j, n, s) : states_t<float, 64>(j, n, s);
 }
 
-int launch_linear_scan(const LinearArgs& a, bool rev, void* stream) {
+int launch_linear_scan(const LinearArgs& a, bool rev, const float* other, double* worth, void* stream) {
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const dim3 grid((unsigned)(a.D * a.D / 1024), (unsigned)a.HV, (unsigned)a.N);
   if (a.D == 128) {
-    if (rev) hipLaunchKernelGGL((k_linear_scan<128, true>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((k_linear_scan<128, false>), grid, dim3(256), 0, s, a);
+    if (rev) hipLaunchKernelGGL((k_linear_scan<128, true>), grid, dim3(256), 0, s, a, other, worth);
+    else hipLaunchKernelGGL((k_linear_scan<128, false>), grid, dim3(256), 0, s, a, other, worth);
   } else {
-    if (rev) hipLaunchKernelGGL((k_linear_scan<64, true>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((k_linear_scan<64, false>), grid, dim3(256), 0, s, a);
+    if (rev) hipLaunchKernelGGL((k_linear_scan<64, true>), grid, dim3(256), 0, s, a, other, worth);
+    else hipLaunchKernelGGL((k_linear_scan<64, false>), grid, dim3(256), 0, s, a, other, worth);
   }
   return (int)hipGetLastError();
 }
 
-int launch_linear_walk(const LinearArgs& a, bool rev, int dtype, void* stream) {
+int launch_linear_walk(const LinearArgs& a, int dtype, void* stream) {
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  if (dtype == 0) return a.D == 128 ? walk_td<bf16, 128>(a, rev, s) : walk_td<bf16, 64>(a, rev, s);
-  return a.D == 128 ? walk_td<float, 128>(a, rev, s) : walk_td<float, 64>(a, rev, s);
+  if (dtype == 0) return a.D == 128 ? walk_t<bf16, 128>(a, s) : walk_t<bf16, 64>(a, s);
+  return a.D == 128 ? walk_t<float, 128>(a, s) : walk_t<float, 64>(a, s);
 }
 
-int launch_linear_group_sum(const LinearArgs& a, int dtype, void* stream) {
+int launch_linear_walks(const LinearJobs& j, int dtype, void* stream) {
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  const int64_t n = (int64_t)a.T * a.H * a.D / 4;
-  const dim3 grid((unsigned)((n + 255) / 256));
-  if (dtype == 0) hipLaunchKernelGGL(k_linear_group_sum<bf16>, grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL(k_linear_group_sum<float>, grid, dim3(256), 0, s, a);
+  const bool wide = j.job[0].D == 128;
+  if (dtype == 0) return wide ? walks_td<bf16, 128>(j, s) : walks_td<bf16, 64>(j, s);
+  return wide ? walks_td<float, 128>(j, s) : walks_td<float, 64>(j, s);
+}
+
+int launch_linear_group_sum(const LinearJobs& j, int dtype, void* stream) {
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const int64_t n = (int64_t)j.job[0].T * j.job[0].H * j.job[0].D / 4;
+  if (n == 0) return 0;
+  const dim3 grid((unsigned)((n + 255) / 256), 2);
+  if (dtype == 0) hipLaunchKernelGGL(k_linear_group_sum<bf16>, grid, dim3(256), 0, s, j);
+  else hipLaunchKernelGGL(k_linear_group_sum<float>, grid, dim3(256), 0, s, j);
   return (int)hipGetLastError();
 }
 

@@ -1,150 +1,161 @@
 // What a serving step reads, made from the requests' lengths (gfx950): sequence starts, positions, block tables and
-// slots. Integers and a few kilobytes: it costs its latency. The whole of it depends on two running sums over the
-// requests (tokens, new blocks), which every workgroup makes for itself in LDS, at once with the others, rather
-// than wait for one that makes them for all.
+// slots. Integers and a few kilobytes: it costs its latency, a chain of a few memory accesses and barriers. The whole
+// of it depends on two running sums over the requests (tokens, new blocks), which every workgroup makes for itself
+// in LDS, at once with the others, rather than wait for one that makes them for all.
 #include "gdn_device.h"
 
 namespace gdn {
 
-constexpr int MAPS_THREADS = 1024, MAPS_SEQS = 4096;
+constexpr int MAPS_SEQS = 4096;
 
-// Inclusive sums over the workgroup's threads of two values.
-struct Two {
-  int64_t x, y;
-};
-__device__ __forceinline__ Two block_scan(Two v, Two* tmp) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-  for (int by = 1; by < 64; by *= 2) {
-    const int64_t x = __shfl_up((long long)v.x, by), y = __shfl_up((long long)v.y, by);
-    if (lane >= by) {
-      v.x += x;
-      v.y += y;
-    }
-  }
-  __syncthreads();
-  if (lane == 63) tmp[wave] = v;
-  __syncthreads();
-  for (int i = 0; i < wave; ++i) {
-    v.x += tmp[i].x;
-    v.y += tmp[i].y;
-  }
-  return v;
+// x + y, at most 2^31 - 1 (for x and y at most that): sums of lengths that nobody can have stay too large to fit
+__device__ __forceinline__ unsigned add_up_to(unsigned x, unsigned y) { return min(x + y, 0x7fffffffu); }
+template <int CTRL, int ROWS>
+__device__ __forceinline__ unsigned scan_step(unsigned x) {
+  return add_up_to(x, (unsigned)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xf, false));
+}
+// Inclusive sums over a wave's lanes (steps as in wave_prefix_sum)
+__device__ __forceinline__ unsigned wave_sums(unsigned x) {
+  x = scan_step<0x111, 0xf>(x);
+  x = scan_step<0x112, 0xf>(x);
+  x = scan_step<0x114, 0xf>(x);
+  x = scan_step<0x118, 0xf>(x);
+  x = scan_step<0x142, 0xa>(x);
+  return scan_step<0x143, 0xc>(x);
 }
 
-// FILL: tokens and the new entries of the table, by all workgroups. UPDATE: what is one value a request, and the
-// buffers that may be the inputs' own, by one workgroup that has read all of its inputs before.
-template <bool FILL, bool UPDATE>
-__global__ __launch_bounds__(MAPS_THREADS) void k_maps(MapsArgs a) {
+// Every workgroup fills tokens and the new entries of the table; workgroup 0 also writes what is one value a
+// request, after all of its inputs are read.
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void k_maps(MapsArgs a) {
+  constexpr int WAVES = THREADS / 64;
   __shared__ int ends[MAPS_SEQS], shift[MAPS_SEQS], taken[MAPS_SEQS]; // tokens so far, position - token, blocks before
-  __shared__ Two tmp[MAPS_THREADS / 64];
-  __shared__ long long most;
-  const int B = a.block, count = min(max(a.free_count[0], 0), a.n_free);
-  const auto blocks = [&](int64_t upto) { return (int)((upto + B - 1) / B); };
-  Two carry = {0, 0};
-  int64_t total = 0; // tokens of the requests that fit
-  int used = 0;      // blocks they take
-  for (int r0 = 0; r0 < a.N; r0 += MAPS_THREADS) {
-    const int r = r0 + threadIdx.x;
-    int64_t len = 0, ctx = 0;
-    int need = 0;
+  __shared__ uint2 sums[WAVES], fitting[WAVES]; // a wave's sums; the sums up to its last request that fits
+  const int B = a.block, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const bool update = blockIdx.x == 0;
+  const unsigned count = min(max(a.free_count[0], 0), a.n_free);
+  const int64_t room = (int64_t)a.max_blocks * B < 0x7fffffff ? (int64_t)a.max_blocks * B : 0x7fffffff; // of a request
+  const auto full = [&](int x) { return (int)(((uint64_t)(unsigned)x * a.block_mul) >> a.block_shift); }; // x / B
+  const auto blocks = [&](int x) { return x == 0 ? 0 : full(x - 1) + 1; };
+  uint2 carry = {0, 0}, total = {0, 0}; // sums over all requests so far, over those that fit (tokens, blocks)
+  for (int r0 = 0; r0 < a.N; r0 += THREADS) {
+    const int r = r0 + (int)threadIdx.x;
+    int len = 0, ctx = 0, given = 0, in = -1;
     bool fine = false;
+    const int32_t* row = a.table;
     if (r < a.N) {
       len = a.lengths[r];
-      ctx = a.contexts[r];
-      fine = ctx >= 0 && ctx <= (int64_t)a.max_blocks * B;
+      given = ctx = a.contexts[r];
+      row += (int64_t)r * a.max_blocks;
+      fine = ctx >= 0 && ctx <= room;
       if (!fine) ctx = 0;
-      if (!fine || len < 0 || ctx + len > (int64_t)a.max_blocks * B || ctx + len > 0x7fffffff) len = 0;
-      need = blocks(ctx + len) - blocks(ctx);
+      if (!fine || len < 0 || ctx + (int64_t)len > room) len = 0;
+      if (update && ctx > 0) in = row[full(ctx - 1)];
     }
-    Two s = block_scan({len, need}, tmp);
-    s.x += carry.x;
-    s.y += carry.y;
-    const bool fits = s.x <= a.T && s.y <= count;
-    // sums rise, so those that fit are the first ones
+    const int held = blocks(ctx), need = blocks(ctx + len) - held;
+    uint2 s = {wave_sums((unsigned)len), wave_sums((unsigned)need)};
+    if (lane == 63) sums[wave] = s;
     __syncthreads();
-    if (threadIdx.x == 0) most = total | ((long long)used << 32);
-    if (threadIdx.x == MAPS_THREADS - 1) tmp[0] = s;
+    uint2 before = carry;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      const uint2 x = sums[w];
+      carry.x = add_up_to(carry.x, x.x);
+      carry.y = add_up_to(carry.y, x.y);
+      if (w + 1 == wave) before = carry;
+    }
+    s.x = add_up_to(s.x, before.x);
+    s.y = add_up_to(s.y, before.y);
+    const bool fits = s.x <= (unsigned)a.T && s.y <= count; // sums rise, so those that fit are the first ones
+    const uint64_t which = __ballot(fits);
+    if (which == 0 ? lane == 0 : lane == 63 - __builtin_clzll(which)) fitting[wave] = which ? s : uint2{0, 0};
     __syncthreads();
-    if (fits) atomicMax(&most, (long long)(s.x | (s.y << 32)));
-    __syncthreads();
-    carry = tmp[0];
-    total = most & 0x7fffffff;
-    used = (int)(most >> 32);
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      const uint2 x = fitting[w];
+      total.x = max(total.x, x.x);
+      total.y = max(total.y, x.y);
+    }
     if (r < a.N) {
       if (!fits) len = 0;
-      const int64_t end = fits ? s.x : total, start = end - len;
-      const int before = (int)(fits ? s.y - need : used);
-      ends[r] = (int)end;
-      shift[r] = (int)(ctx - start);
-      taken[r] = before;
-      if constexpr (UPDATE) {
-        const int32_t* row = a.table + (int64_t)r * a.max_blocks;
-        const int held = blocks(ctx);
-        const int in = ctx > 0 ? row[(ctx - 1) / B] : -1;
-        int out = in;
+      const int end = (int)(fits ? s.x : total.x), first = (int)(fits ? s.y - need : total.y);
+      ends[r] = end;
+      shift[r] = ctx - (end - len);
+      taken[r] = first;
+      if (update) {
+        int out = in; // a new token's block that the request has already is its last one
         if (len > 0) {
-          const int b = (int)((ctx + len - 1) / B);
-          out = b < held ? row[b] : a.free_list[count - 1 - (before + b - held)];
+          const int b = full(ctx + len - 1);
+          if (b >= held) out = a.free_list[count - 1 - (first + b - held)];
         }
-        if (a.cu) a.cu[r + 1] = (int)end;
-        if (a.granted) a.granted[r] = (int)len;
+        if (a.cu) a.cu[r + 1] = end;
+        if (a.granted) a.granted[r] = len;
         if (a.slot_in) a.slot_in[r] = in;
         if (a.slot_out) a.slot_out[r] = out;
-        if (fine && a.contexts_out) a.contexts_out[r] = (int)(ctx + len);
-        else if (a.contexts_out && a.contexts_out != a.contexts) a.contexts_out[r] = a.contexts[r];
+        if (a.contexts_out) a.contexts_out[r] = fine ? ctx + len : given;
       }
     }
-    __syncthreads();
   }
-  if constexpr (UPDATE) {
-    if (threadIdx.x == 0) {
-      if (a.cu) a.cu[0] = 0;
-      if (a.free_count_out) a.free_count_out[0] = count - used;
-    }
+  if (update && threadIdx.x == 0) {
+    if (a.cu) a.cu[0] = 0;
+    if (a.free_count_out) a.free_count_out[0] = (int)(count - total.y);
   }
-  if constexpr (FILL) {
-    for (int t = blockIdx.x * MAPS_THREADS + threadIdx.x; t < a.T; t += gridDim.x * MAPS_THREADS) {
-      int pos = 0, keep = -1;
-      int64_t slot = -1;
-      if (t < total) {
-        int lo = 0, hi = a.N - 1; // the first request that ends behind t
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if (ends[mid] > t) hi = mid;
-          else lo = mid + 1;
-        }
-        const int begin = lo > 0 ? ends[lo - 1] : 0;
-        pos = t + shift[lo];
-        const int b = pos / B, held = blocks(begin + shift[lo]);
-        int32_t* at = a.table + (int64_t)lo * a.max_blocks + b;
-        int id;
-        if (b < held) id = *at;
-        else {
-          id = a.free_list[count - 1 - (taken[lo] + b - held)];
-          if (pos % B == 0) *at = id; // the token that enters a block
-        }
-        slot = (int64_t)id * B + pos % B;
-        if ((pos + 1) % B == 0 && t + 1 < ends[lo]) keep = id;
+  if (!a.fill) return;
+  __syncthreads();
+  for (int64_t t = (int64_t)blockIdx.x * THREADS + threadIdx.x; t < a.T; t += (int64_t)gridDim.x * THREADS) {
+    int pos = 0, keep = -1;
+    int64_t slot = -1;
+    if (t < total.x) {
+      int lo = 0, hi = a.N - 1; // the first request that ends behind t
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (ends[mid] > t) hi = mid;
+        else lo = mid + 1;
       }
-      if (a.positions) a.positions[t] = pos;
-      if (a.token_slots) a.token_slots[t] = slot;
-      if (a.slot_tok) a.slot_tok[t] = keep;
+      const int begin = lo > 0 ? ends[lo - 1] : 0;
+      pos = (int)t + shift[lo];
+      const int b = full(pos), at = pos - b * B, held = blocks(begin + shift[lo]);
+      int32_t* entry = a.table + (int64_t)lo * a.max_blocks + b;
+      int id;
+      if (b < held) id = *entry;
+      else {
+        id = a.free_list[count - 1 - (taken[lo] + b - held)];
+        if (at == 0) *entry = id; // the token that enters a block
+      }
+      slot = (int64_t)id * B + at;
+      if (at == B - 1 && t + 1 < ends[lo]) keep = id;
     }
+    if (a.positions) a.positions[t] = pos;
+    if (a.token_slots) a.token_slots[t] = slot;
+    if (a.slot_tok) a.slot_tok[t] = keep;
   }
 }
 
-int launch_maps(const MapsArgs& a, void* stream) {
+// Up to ALONE tokens one workgroup makes everything (of 256 threads where they are few: a barrier of 4 waves). More
+// tokens take more workgroups, and then contexts and the count, if they are to move on in place, wait for a launch
+// of their own: another workgroup may still be reading them.
+int launch_maps(const MapsArgs& a0, void* stream) {
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  constexpr int ALONE = 4 * MAPS_THREADS; // tokens that one workgroup fills with the rest
+  constexpr int ALONE = 4096;
+  MapsArgs a = a0;
+  a.fill = 1;
   if (a.T <= ALONE) {
-    hipLaunchKernelGGL((k_maps<true, true>), dim3(1), dim3(MAPS_THREADS), 0, s, a);
+    if (a.N <= 256 && a.T <= 1024) hipLaunchKernelGGL(k_maps<256>, dim3(1), dim3(256), 0, s, a);
+    else hipLaunchKernelGGL(k_maps<1024>, dim3(1), dim3(1024), 0, s, a);
     return (int)hipGetLastError();
   }
-  const int groups = (a.T + MAPS_THREADS - 1) / MAPS_THREADS;
-  hipLaunchKernelGGL((k_maps<true, false>), dim3((unsigned)(groups < 256 ? groups : 256)), dim3(MAPS_THREADS), 0, s, a);
+  const bool in_place = a.contexts_out == a.contexts || a.free_count_out == a.free_count;
+  MapsArgs rest = a;
+  if (in_place) {
+    a.contexts_out = a.free_count_out = nullptr;
+    rest.cu = rest.granted = rest.slot_in = rest.slot_out = nullptr;
+    rest.fill = 0;
+  }
+  const int groups = (a.T + 1023) / 1024;
+  hipLaunchKernelGGL(k_maps<1024>, dim3((unsigned)(groups < 512 ? groups : 512)), dim3(1024), 0, s, a);
   if (const int e = (int)hipGetLastError()) return e;
-  hipLaunchKernelGGL((k_maps<false, true>), dim3(1), dim3(MAPS_THREADS), 0, s, a);
+  if (!in_place) return 0;
+  hipLaunchKernelGGL(k_maps<1024>, dim3(1), dim3(1024), 0, s, rest);
   return (int)hipGetLastError();
 }
 

@@ -239,16 +239,28 @@ __global__ __launch_bounds__(LANES > 256 ? LANES : 256) void k_norm_bwd(NormArgs
   }
 }
 
-// dw[c] = sum over the workgroups' parts; 32 columns a workgroup, 8 rows of lanes
-__global__ __launch_bounds__(256) void k_norm_dw(NormArgs a, int blocks) {
-  __shared__ float s[8][33];
+// dw[c] = sum over the workgroups' parts; 32 columns a workgroup, 32 rows of lanes (with 8 of them the sum of
+// 1024 parts of 2048 values took 48 us, a chain of 128 loads)
+__global__ __launch_bounds__(1024) void k_norm_dw(NormArgs a, int blocks) {
+  __shared__ float s[32][33];
   const int x = threadIdx.x % 32, y = threadIdx.x / 32, c = blockIdx.x * 32 + x;
   float sum = 0.f;
-  if (c < a.D)
-    for (int i = y; i < blocks; i += 8) sum += a.part[(int64_t)i * a.D + c];
+  if (c < a.D) {
+    constexpr int AHEAD = 8;
+    for (int i = y; i < blocks; i += 32 * AHEAD) {
+      float v[AHEAD];
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) v[j] = i + 32 * j < blocks ? a.part[(int64_t)(i + 32 * j) * a.D + c] : 0.f;
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) sum += v[j];
+    }
+  }
   s[y][x] = sum;
   __syncthreads();
-  if (y == 0 && c < a.D) a.dw[c] = ((s[0][x] + s[1][x]) + (s[2][x] + s[3][x])) + ((s[4][x] + s[5][x]) + (s[6][x] + s[7][x]));
+  sum = s[x][y]; // of column blockIdx.x 32 + y: a sum over 32 neighbouring lanes
+#pragma unroll
+  for (int by = 1; by < 32; by *= 2) sum += __shfl_xor(sum, by);
+  if (x == 0 && blockIdx.x * 32 + y < (unsigned)a.D) a.dw[blockIdx.x * 32 + y] = sum;
 }
 
 // Lanes a row: a wave takes a row of up to 2048 values, a workgroup a longer one, or any of several hundred where
@@ -288,7 +300,7 @@ int launch_norm_bwd(const NormArgs& a, int dtype, void* stream) {
   if (a.rows > 0)
     if (const int e = dtype == 0 ? norm_any<bf16>(a, true, s) : norm_any<float>(a, true, s)) return e;
   if (!a.dw) return 0;
-  hipLaunchKernelGGL(k_norm_dw, dim3((unsigned)((a.D + 31) / 32)), dim3(256), 0, s, a, norm_blocks(a));
+  hipLaunchKernelGGL(k_norm_dw, dim3((unsigned)((a.D + 31) / 32)), dim3(1024), 0, s, a, norm_blocks(a));
   return (int)hipGetLastError();
 }
 
