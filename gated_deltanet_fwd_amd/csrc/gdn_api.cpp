@@ -1643,7 +1643,7 @@ int gdn_linear_bwd(const gdn_linear_problem* p, const void* q, const void* k, co
   for (int i = 0; i < 2; ++i) {
     gdn::LinearArgs& a = j.job[i];
     a.flip = 1;
-    if (shared) a.part = (float*)(w + L.part[i]);
+    if (shared) a.part = w + L.part[i];
     if (dg) {
       a.dot = i == 0 ? c.q : c.k;
       a.dots = (float*)(w + (i == 0 ? L.qdots : L.kdots));

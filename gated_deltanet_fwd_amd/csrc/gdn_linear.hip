@@ -92,7 +92,7 @@ struct Op<bf16> {
   static __device__ __forceinline__ frag down(int tile, const Down& lane, int ks, int m) {
     constexpr int ROW = Tile<bf16, D>::ROW;
     typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
-    const int at = tile + (lane.at ^ (m << 5)) + 32 * ks * ROW;
+    const int at = ((tile + lane.at) ^ (m << 5)) + 32 * ks * ROW; // (a tile's address has none of the bits exchanged)
     const bf16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(lds_char*)(uintptr_t)at);
     const bf16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(lds_char*)(uintptr_t)(at + 16 * ROW));
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -133,7 +133,7 @@ struct Op<float> {
     frag r;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int at = tile + (lane.at[e] ^ (m << 6)) + 32 * ks * ROW;
+      const int at = ((tile + lane.at[e]) ^ (m << 6)) + 32 * ks * ROW;
       r[e] = lds_read<float>(at);
       r[4 + e] = lds_read<float>(at + 16 * ROW);
     }
@@ -242,17 +242,31 @@ struct alignas(16) Decays {
   float w[CH];          // factor of each row in the state that leaves
   float all;            // factor of the state that enters in the one that leaves
 };
-__device__ __forceinline__ double up(double x, int by, int lane) {
-  const double y = __shfl_up(x, by);
-  return lane >= by ? x + y : x;
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double scan_step(double x) { // lanes without a source add 0
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const unsigned lo = (unsigned)__builtin_amdgcn_update_dpp(0, (int)(unsigned)b, CTRL, ROWS, 0xf, false);
+  const unsigned hi = (unsigned)__builtin_amdgcn_update_dpp(0, (int)(unsigned)(b >> 32), CTRL, ROWS, 0xf, false);
+  return x + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// Inclusive sums over a wave's lanes, by the steps of wave_prefix_sum.
+__device__ __forceinline__ double wave_sums(double x) {
+  x = scan_step<0x111, 0xf>(x);
+  x = scan_step<0x112, 0xf>(x);
+  x = scan_step<0x114, 0xf>(x);
+  x = scan_step<0x118, 0xf>(x);
+  x = scan_step<0x142, 0xa>(x);
+  return scan_step<0x143, 0xc>(x);
+}
+__device__ __forceinline__ double last_lane(double x) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const unsigned lo = (unsigned)__builtin_amdgcn_readlane((int)(unsigned)b, 63), hi = (unsigned)__builtin_amdgcn_readlane((int)(unsigned)(b >> 32), 63);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 template <bool REV>
 __device__ __forceinline__ void chunk_decays(Decays& d, float g, float in_scale, float w_scale) {
   const int lane = threadIdx.x & 63;
-  double s = (double)(g < -1e4f ? -1e4f : g) * 1.4426950408889634;
-#pragma unroll
-  for (int by = 1; by < 64; by *= 2) s = up(s, by, lane);
-  const double total = __shfl(s, 63);
+  const double s = wave_sums((double)(g < -1e4f ? -1e4f : g) * 1.4426950408889634), total = last_lane(s);
   const float begun = __builtin_amdgcn_exp2f((float)s), left = __builtin_amdgcn_exp2f((float)(total - s));
   d.hi[lane] = (float)s;
   d.lo[lane] = (float)(s - (double)(float)s);
@@ -370,9 +384,9 @@ __device__ __forceinline__ void add_to_state(f32x4 (&W)[D / 16][CT], const typen
   }
 }
 
-// LDS of the kernels: tiles at the start, then what they name
+// LDS of the kernels: tiles at the start, then what they name. They have no other, so that it starts at address 0, and
+// what lies at a fixed place in it is an offset in the instructions.
 extern __shared__ __attribute__((aligned(1024))) char linear_lds[];
-__device__ __forceinline__ int lds_start() { return (int)(uintptr_t)(lds_char*)linear_lds; }
 
 // ------------------------------------------------------------------------------------------------
 // What each segment adds to a state, and its decay. The last segment of a document (the first, in reverse)
@@ -388,7 +402,7 @@ __device__ __forceinline__ void segment_state(const LinearArgs& a, int block) {
   const Segment s = find_segment(a, slot);
   if (!s.live || (REV ? s.first : s.last)) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
-  const int col0 = wave * 16 * CT, tiles = lds_start();
+  const int col0 = wave * 16 * CT;
   f32x4 W[D / 16][CT];
 #pragma unroll
   for (int kt = 0; kt < D / 16; ++kt)
@@ -412,25 +426,27 @@ __device__ __forceinline__ void segment_state(const LinearArgs& a, int block) {
     gl = log_decay(a, h, at(0) + lane, s.t1);
     decays(0);
   }
-  fb.load(tiles, at(0), s.t1);
-  fc.load(tiles + S::BYTES, at(0), s.t1);
-  for (int i = 0; i < chunks; ++i) {
+  fb.load(0, at(0), s.t1);
+  fc.load(S::BYTES, at(0), s.t1);
+  const auto step = [&](int i, auto half) { // in tiles 2 half, 2 half + 1
+    constexpr int tb = half * 2 * S::BYTES, tc = tb + S::BYTES, next = (1 - half) * 2 * S::BYTES;
     wait_loads<0>();
     __syncthreads();
-    const int tb = tiles + (i & 1) * 2 * S::BYTES, tc = tb + S::BYTES;
     if (i + 1 < chunks) {
-      const int next = tiles + (~i & 1) * 2 * S::BYTES;
       fb.load(next, at(i + 1), s.t1);
       fc.load(next + S::BYTES, at(i + 1), s.t1);
     }
-    const Decays& d = dec[i & 1];
     typename Op<T>::frag cf[2][CT];
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) cf[ks][ct] = Op<T>::template down<D>(tc, c_lane[ct], ks, 0);
-    add_to_state<T, D, CT, NT>(W, cf, tb, b_lane, d);
+    add_to_state<T, D, CT, NT>(W, cf, tb, b_lane, dec[half]);
     if (wave == 0 && i + 1 < chunks) decays(i + 1);
+  };
+  for (int i = 0; i < chunks; i += 2) {
+    step(i, std::integral_constant<int, 0>());
+    if (i + 1 < chunks) step(i + 1, std::integral_constant<int, 1>());
   }
   float* to = a.states + ((int64_t)slot * a.HV + h) * D * D;
 #pragma unroll
@@ -540,12 +556,12 @@ __device__ __forceinline__ void walk_chunks(const LinearArgs& a, const Segment& 
   typedef typename std::conditional<DOTS, float, T>::type PT; // type of P in LDS
   typedef PT p4 __attribute__((ext_vector_type(4)));
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
-  const int col0 = wave * 16 * CT, lds = lds_start();
+  const int col0 = wave * 16 * CT;
   Decays* dec = (Decays*)(linear_lds + L::dec(sizeof(PT)));
   float* red = (float*)(linear_lds + L::red(sizeof(PT)));
-  int ta = lds, tb = lds + S::BYTES, spare = lds + 2 * S::BYTES;
-  const int tc = lds + 3 * S::BYTES;
-  const int p_lane = lds + L::P + lane * 4 * (int)sizeof(PT); // a lane reads of each tile what the same lane wrote
+  int ta = 0, tb = S::BYTES, spare = 2 * S::BYTES;
+  constexpr int tc = 3 * S::BYTES;
+  const int p_lane = L::P + lane * 4 * (int)sizeof(PT); // a lane reads of each tile what the same lane wrote
 
   const int chunks = (s.t1 - s.t0 + CH - 1) / CH;
   const auto at = [&](int i) { return s.t0 + (REV ? chunks - 1 - i : i) * CH; };
@@ -616,6 +632,7 @@ __device__ __forceinline__ void walk_chunks(const LinearArgs& a, const Segment& 
     for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) cf[ks][ct] = O::template down<D>(tc, c_lane[ct], ks, 0);
+    __builtin_amdgcn_s_setprio(1); // over the other workgroup's waves outside their products: 1 to 3% of the walk
     // y^T = W^T a^T
     const int al = fresh(along);
     f32x4 y[CT][4];
@@ -643,7 +660,9 @@ __device__ __forceinline__ void walk_chunks(const LinearArgs& a, const Segment& 
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) y[ct][bt] *= f;
     }
+    __builtin_amdgcn_s_setprio(0);
     __syncthreads(); // P
+    __builtin_amdgcn_s_setprio(1);
     if (more) {
       fb.load(ta, at(i + 1), s.t1);
       fc.load(tc, at(i + 1), s.t1);
@@ -673,6 +692,7 @@ __device__ __forceinline__ void walk_chunks(const LinearArgs& a, const Segment& 
       }
     add_to_state<T, D, CT, NTW>(W, cf, tb, b_lane, d);
 
+    __builtin_amdgcn_s_setprio(0);
     if constexpr (DOTS) {
 #pragma unroll
       for (int bt = 0; bt < 4; ++bt) {
@@ -709,11 +729,11 @@ __device__ __forceinline__ void walk_chunks(const LinearArgs& a, const Segment& 
         }
       }
     };
-    if (a.part) {
-      write(a.part);
+    if (!DOTS && a.part) {
+      write((float*)a.part);
       wait_loads<4 * CT>(); // the next tiles, not these stores
     } else {
-      write((T*)a.out);
+      write((T*)(a.part ? a.part : a.out));
       wait_loads<CT == 2 && sizeof(T) == 2 ? 4 : 4 * CT>();
     }
     if constexpr (DOTS) {
@@ -794,18 +814,27 @@ __global__ __launch_bounds__(NTHREADS, sizeof(T) == 2 ? 2 : 1) void k_linear_wal
 }
 
 // ------------------------------------------------------------------------------------------------
-// Sums over the value heads of a group, in their order: part f32 [T, HV, D] -> out [T, H, D], for dq and dk
-template <typename T>
+// Sums over the value heads of a group, in their order and in FP32: part [T, HV, D] -> out [T, H, D], for dq and dk. The
+// parts are FP32 where the walk has rounded its operands already. With DOTS it has not, and they are rounded to the io type:
+// one rounding before the result's own, as in the other products (5 bytes less an element moved, of 10: 32,768
+// tokens, 16/48 heads, 128 wide: 2.08 -> 1.77 ms for the whole backward).
+template <typename T, typename P>
 __global__ __launch_bounds__(256) void k_linear_group_sum(LinearJobs jobs) {
   const LinearArgs& a = jobs.job[blockIdx.y];
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, n = (int64_t)a.T * a.H * a.D;
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8, n = (int64_t)a.T * a.H * a.D;
   if (i >= n) return;
   const int64_t head = i / a.D, col = i - head * a.D;
-  const float* p = a.part + head * a.G * a.D + col;
-  f32x4 s = *reinterpret_cast<const f32x4*>(p);
-  for (int j = 1; j < a.G; ++j) s += *reinterpret_cast<const f32x4*>(p + (int64_t)j * a.D);
-  const float v[4] = {s[0], s[1], s[2], s[3]};
-  IO<T>::store4((T*)a.out + i, v);
+  const P* p = (const P*)a.part + head * a.G * a.D + col;
+  float s[8];
+  IO<P>::load8f(p, s);
+  for (int j = 1; j < a.G; ++j) {
+    float x[8];
+    IO<P>::load8f(p + (int64_t)j * a.D, x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] += x[e];
+  }
+  IO<T>::store4((T*)a.out + i, s);
+  IO<T>::store4((T*)a.out + i + 4, s + 4);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -855,9 +884,7 @@ __global__ __launch_bounds__(256) void k_linear_dg(LinearDgArgs d) {
   for (int c = 0; c < n; c += 256) { // from the border inwards
     const int j = c + (int)threadIdx.x, t = from_end ? n - 1 - j : j;
     const double own = j < n ? (double)qd[t] - (double)kd[t] : 0.0;
-    double p = own;
-#pragma unroll
-    for (int by = 1; by < 64; by *= 2) p = up(p, by, lane);
+    const double p = wave_sums(own);
     if (lane == 63) carry[wave] = p;
     __syncthreads();
     double before = 0.0, turn = 0.0;
@@ -969,11 +996,12 @@ int launch_linear_walks(const LinearJobs& j, int dtype, void* stream) {
 
 int launch_linear_group_sum(const LinearJobs& j, int dtype, void* stream) {
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  const int64_t n = (int64_t)j.job[0].T * j.job[0].H * j.job[0].D / 4;
+  const int64_t n = (int64_t)j.job[0].T * j.job[0].H * j.job[0].D / 8;
   if (n == 0) return 0;
   const dim3 grid((unsigned)((n + 255) / 256), 2);
-  if (dtype == 0) hipLaunchKernelGGL(k_linear_group_sum<bf16>, grid, dim3(256), 0, s, j);
-  else hipLaunchKernelGGL(k_linear_group_sum<float>, grid, dim3(256), 0, s, j);
+  if (dtype != 0) hipLaunchKernelGGL((k_linear_group_sum<float, float>), grid, dim3(256), 0, s, j);
+  else if (j.job[0].dots) hipLaunchKernelGGL((k_linear_group_sum<bf16, bf16>), grid, dim3(256), 0, s, j);
+  else hipLaunchKernelGGL((k_linear_group_sum<bf16, float>), grid, dim3(256), 0, s, j);
   return (int)hipGetLastError();
 }
 
