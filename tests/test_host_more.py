@@ -76,7 +76,7 @@ def test_linear_refusals():
 def test_linear_workspace():
     """Short documents need no states in the workspace; long ones do; the backward more than the forward, shared
     heads more again."""
-    short, long = linear([300, 5]), linear([5000])
+    short, long = linear([64, 5]), linear([5000])
     assert G.gdn_linear_workspace_bytes(short, G.OP_FWD) == 256
     f, b = (G.gdn_linear_workspace_bytes(long, op) for op in (G.OP_FWD, G.OP_BWD))
     assert f >= 2 * 4 * 64 * 64 * 4 and b >= 2 * f
