@@ -1491,7 +1491,7 @@ int linear_segment(const gdn_linear_problem* p, int op) {
 
 struct LinearLayout {
   int seg, slots;
-  size_t S, D, Sdecay, Ddecay, worth, qdots, kdots, sums, part[2], total;
+  size_t S, D, Sdecay, Ddecay, worth, qdots, kdots, sums, part[2], unit[2], total;
 };
 
 int linear_layout(const gdn_linear_problem* p, int op, LinearLayout* L) {
@@ -1520,8 +1520,10 @@ int linear_layout(const gdn_linear_problem* p, int op, LinearLayout* L) {
     L->qdots = take(rows);
     L->kdots = take(rows);
     L->sums = take((size_t)slots * p->h_v * 8);
-    for (size_t& part : L->part)
-      if (p->h_v != p->h_qk) part = take(rows * p->d);
+    for (int i = 0; i < 2 && p->h_v != p->h_qk; ++i) {
+      L->part[i] = take(p->dtype == GDN_DTYPE_BF16 ? rows * (p->d / 2) : rows * p->d);
+      if (p->dtype == GDN_DTYPE_BF16) L->unit[i] = take(rows * 4);
+    }
   }
   L->total = std::max(off, kAlign);
   return GDN_OK;
@@ -1683,7 +1685,10 @@ int gdn_linear_bwd(const gdn_linear_problem* p, const void* q, const void* k, co
   for (int i = 0; i < 2; ++i) {
     gdn::LinearArgs& a = j.job[i];
     a.flip = 1;
-    if (shared) a.part = w + L.part[i];
+    if (shared) {
+      a.part = w + L.part[i];
+      a.unit = (float*)(w + L.unit[i]);
+    }
     if (dg) {
       a.dot = i == 0 ? c.q : c.k;
       a.dots = (float*)(w + (i == 0 ? L.qdots : L.kdots));

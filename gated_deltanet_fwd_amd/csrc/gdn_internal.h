@@ -251,7 +251,8 @@ struct LinearArgs {
   float* states;     // [slots, HV, d, d] states that segments start from
   float* decay;      // [slots, HV] factor of a state over a segment
   void* out;         // y: [T, HV, d], or with `part` the sums over groups [T, H, d]
-  void* part;        // [T, HV, d] y before those sums, f32, or with dots in the io type; NULL: y goes to out
+  void* part;        // [T, HV, d] y before those sums, f32 or (for bf16) multiples of `unit` in f16; NULL: y goes to out
+  float* unit;       // [T, HV, 4]
   float* dots;       // [HV, T], or NULL
 };
 struct LinearJobs { // products that one launch makes: forward and reverse states; dq, dk and dv

@@ -546,6 +546,49 @@ struct WalkLds {
   static constexpr int bytes(bool dots) { return red(dots ? 4 : sizeof(T)) + (dots ? 4 * CH * 4 : 0); }
 };
 
+// Parts of dq and dk, to be summed over a group's value heads (k_linear_group_sum): for bf16 in 16 bits, 11 of them
+// significant, as multiples of a power of two that the 16 CT columns of a wave's row share. That is off by at most
+// 2^-12 of the largest of them, an eighth of the sum's own rounding, so that parts that cancel to an eighth still leave
+// it that; bf16 parts would not. (32,768 tokens, 16/48 heads, 128 wide, whole backward: FP32 parts 2090 us, these 1934.)
+// What is not finite makes its columns of the row NaN.
+template <int CT>
+struct PartRow {
+  typedef _Float16 type __attribute__((ext_vector_type(4 * CT)));
+};
+template <int D, int CT>
+__device__ __forceinline__ void write_part(const LinearArgs& a, const f32x4 (&y)[CT][4], int t, int n, int h, int wave) {
+  const int lane = threadIdx.x & 63, g = fresh(lane >> 4), l16 = fresh(lane & 15), os = a.HV * D;
+  const int64_t row = (int64_t)t * a.HV + h;
+  const __amdgpu_buffer_rsrc_t to = make_rsrc((_Float16*)a.part + row * D, ((n - 1) * os + D) * 2);
+  const __amdgpu_buffer_rsrc_t unit = make_rsrc(a.unit + row * 4, ((n - 1) * a.HV * 4 + 4) * 4);
+  int off = (l16 * os + 16 * CT * wave + 4 * CT * g) * 2, uoff = (l16 * a.HV * 4 + wave) * 4;
+#pragma unroll
+  for (int bt = 0; bt < 4; ++bt, off += 32 * os, uoff += 256 * a.HV) {
+    unsigned most = 0; // bits of magnitudes order as they do
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = y[ct][bt][e]; // a cast of the element itself would take the vector's first
+        most = max(most, __builtin_bit_cast(unsigned, x) & 0x7fffffffu);
+      }
+    most = max(most, (unsigned)__shfl_xor((int)most, 16));
+    most = max(most, (unsigned)__shfl_xor((int)most, 32));
+    // 2^(exponent - 14), at least 2^-100, and its inverse, from the exponents' bits
+    const int e = max((int)(most >> 23) - 14, 27);
+    const float by = __builtin_bit_cast(float, (unsigned)(254 - e) << 23);
+    typename PartRow<CT>::type v;
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[4 * ct + j] = (_Float16)(y[ct][bt][j] * by);
+    if constexpr (CT == 2) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4_t, v), to, off, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(i32x2_t, v), to, off, 0, 0);
+    const float u = __builtin_bit_cast(float, most >= 0x7f800000u ? 0x7fc00000u : (unsigned)e << 23);
+    if (g == 0) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(int, u), unit, uoff, 0, 0);
+  }
+}
+
 template <typename T, int D, bool REV, bool DOTS, int NTW, typename F>
 __device__ __forceinline__ void walk_chunks(const LinearArgs& a, const Segment& s, int h, f32x4 (&W)[D / 16][D / 64], const F& load_state) {
   typedef Tile<T, D> S;
@@ -729,11 +772,16 @@ __device__ __forceinline__ void walk_chunks(const LinearArgs& a, const Segment& 
         }
       }
     };
-    if (!DOTS && a.part) {
-      write((float*)a.part);
-      wait_loads<4 * CT>(); // the next tiles, not these stores
+    if (a.part) {
+      if constexpr (sizeof(T) == 4) {
+        write((float*)a.part);
+        wait_loads<4 * CT>(); // the next tiles, not these stores
+      } else {
+        write_part<D, CT>(a, y, t, n, h, wave);
+        wait_loads<8>();
+      }
     } else {
-      write((T*)(a.part ? a.part : a.out));
+      write((T*)a.out);
       wait_loads<CT == 2 && sizeof(T) == 2 ? 4 : 4 * CT>();
     }
     if constexpr (DOTS) {
@@ -814,24 +862,31 @@ __global__ __launch_bounds__(NTHREADS, sizeof(T) == 2 ? 2 : 1) void k_linear_wal
 }
 
 // ------------------------------------------------------------------------------------------------
-// Sums over the value heads of a group, in their order and in FP32: part [T, HV, D] -> out [T, H, D], for dq and dk. The
-// parts are FP32 where the walk has rounded its operands already. With DOTS it has not, and they are rounded to the io type:
-// one rounding before the result's own, as in the other products (5 bytes less an element moved, of 10: 32,768
-// tokens, 16/48 heads, 128 wide: 2.08 -> 1.77 ms for the whole backward).
-template <typename T, typename P>
+// Sums over the value heads of a group, in their order and in FP32: part [T, HV, D] -> out [T, H, D], for dq and dk. It
+// costs moving the parts: 1.1 GB of 16-bit ones at 32,768 tokens, 16/48 heads, 128 wide take 196 us (FP32 ones 355).
+template <typename T, int D>
 __global__ __launch_bounds__(256) void k_linear_group_sum(LinearJobs jobs) {
   const LinearArgs& a = jobs.job[blockIdx.y];
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8, n = (int64_t)a.T * a.H * a.D;
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8, n = (int64_t)a.T * a.H * D;
   if (i >= n) return;
-  const int64_t head = i / a.D, col = i - head * a.D;
-  const P* p = (const P*)a.part + head * a.G * a.D + col;
+  const int64_t head = i / D * a.G;
+  const int col = (int)(i % D);
   float s[8];
-  IO<P>::load8f(p, s);
-  for (int j = 1; j < a.G; ++j) {
-    float x[8];
-    IO<P>::load8f(p + (int64_t)j * a.D, x);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s[e] += x[e];
+  for (int e = 0; e < 8; ++e) s[e] = 0.f;
+  for (int j = 0; j < a.G; ++j) {
+    const int64_t at = (head + j) * D + col;
+    if constexpr (sizeof(T) == 4) {
+      float x[8];
+      IO<float>::load8f((const float*)a.part + at, x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[e] += x[e];
+    } else {
+      const auto x = *reinterpret_cast<const PartRow<2>::type*>((const _Float16*)a.part + at);
+      const float u = a.unit[(head + j) * 4 + col / (D / 4)];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[e] = __builtin_fmaf((float)x[e], u, s[e]);
+    }
   }
   IO<T>::store4((T*)a.out + i, s);
   IO<T>::store4((T*)a.out + i + 4, s + 4);
@@ -999,9 +1054,13 @@ int launch_linear_group_sum(const LinearJobs& j, int dtype, void* stream) {
   const int64_t n = (int64_t)j.job[0].T * j.job[0].H * j.job[0].D / 8;
   if (n == 0) return 0;
   const dim3 grid((unsigned)((n + 255) / 256), 2);
-  if (dtype != 0) hipLaunchKernelGGL((k_linear_group_sum<float, float>), grid, dim3(256), 0, s, j);
-  else if (j.job[0].dots) hipLaunchKernelGGL((k_linear_group_sum<bf16, bf16>), grid, dim3(256), 0, s, j);
-  else hipLaunchKernelGGL((k_linear_group_sum<bf16, float>), grid, dim3(256), 0, s, j);
+  if (j.job[0].D == 128) {
+    if (dtype == 0) hipLaunchKernelGGL((k_linear_group_sum<bf16, 128>), grid, dim3(256), 0, s, j);
+    else hipLaunchKernelGGL((k_linear_group_sum<float, 128>), grid, dim3(256), 0, s, j);
+  } else {
+    if (dtype == 0) hipLaunchKernelGGL((k_linear_group_sum<bf16, 64>), grid, dim3(256), 0, s, j);
+    else hipLaunchKernelGGL((k_linear_group_sum<float, 64>), grid, dim3(256), 0, s, j);
+  }
   return (int)hipGetLastError();
 }
 

@@ -80,7 +80,7 @@ def test_linear_workspace():
     assert G.gdn_linear_workspace_bytes(short, G.OP_FWD) == 256
     f, b = (G.gdn_linear_workspace_bytes(long, op) for op in (G.OP_FWD, G.OP_BWD))
     assert f >= 2 * 4 * 64 * 64 * 4 and b >= 2 * f
-    assert b - G.gdn_linear_workspace_bytes(linear([5000], H=4), G.OP_BWD) == 2 * 5000 * 4 * 64 * 4  # dq and dk
+    assert b - G.gdn_linear_workspace_bytes(linear([5000], H=4), G.OP_BWD) == 2 * 5000 * 4 * (64 * 2 + 16)  # dq and dk: 16 bits each, units
 
 
 @pytest.mark.parametrize("field,value,code,text", [
