@@ -1424,6 +1424,7 @@ int check_linear(const gdn_linear_problem* p) {
   if (p->d != 64 && p->d != 128) return fail(GDN_EUNSUPPORTED, "d must be 64 or 128 (got %d)", p->d);
   if ((int64_t)p->h_v * p->d > LINEAR_ROW)
     return fail(GDN_EINVAL, "h_v * d must be at most 2^22 (got %lld)", (long long)p->h_v * p->d);
+  if (p->h_v > 65535) return fail(GDN_EINVAL, "h_v must be at most 65535 (got %d)", p->h_v);
   if (p->dtype != GDN_DTYPE_BF16 && p->dtype != GDN_DTYPE_F32)
     return fail(GDN_EUNSUPPORTED, "unsupported dtype %d", p->dtype);
   if (p->decay != GDN_DECAY_TOKEN && p->decay != GDN_DECAY_HEAD) return fail(GDN_EINVAL, "decay must be token (0) or head (1)");

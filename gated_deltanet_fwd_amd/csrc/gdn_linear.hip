@@ -231,6 +231,10 @@ __device__ __forceinline__ bool place(const LinearArgs& a, int b, int* slot, int
   *h = (group - *slot * a.H) * a.G + (rem >> 3);
   return *slot < a.slots;
 }
+// Launches of many workgroups have two dimensions: one holds less than 2^32 threads.
+constexpr unsigned MOST_BLOCKS = 1 << 20;
+__device__ __forceinline__ int block_index() { return (int)(blockIdx.y * gridDim.x + blockIdx.x); }
+static dim3 many_blocks(unsigned n) { return n <= MOST_BLOCKS ? dim3(n) : dim3(MOST_BLOCKS, (n + MOST_BLOCKS - 1) / MOST_BLOCKS); }
 static unsigned place_blocks(const LinearArgs& a) { return (unsigned)(((int64_t)a.slots * a.H + 7) / 8 * 8 * a.G); }
 
 // Decays of one chunk, from the 64 log decays in a wave's lanes. The sums are kept in 64 bits (as two 32-bit
@@ -463,8 +467,9 @@ __device__ __forceinline__ void segment_state(const LinearArgs& a, int block) {
 // Forward and, behind it in the same launch (`blocks` workgroups each), reverse.
 template <typename T, int D>
 __global__ __launch_bounds__(NTHREADS, sizeof(T) == 2 ? 2 : 1) void k_linear_states(LinearJobs j, int blocks) {
-  if ((int)blockIdx.x < blocks) segment_state<T, D, false>(j.job[0], blockIdx.x);
-  else segment_state<T, D, true>(j.job[1], blockIdx.x - blocks);
+  const int b = block_index();
+  if (b < blocks) segment_state<T, D, false>(j.job[0], b);
+  else segment_state<T, D, true>(j.job[1], b - blocks);
 }
 
 __device__ __forceinline__ double block_sum(double x, double* tmp) { // over 256 threads
@@ -546,10 +551,10 @@ struct WalkLds {
   static constexpr int bytes(bool dots) { return red(dots ? 4 : sizeof(T)) + (dots ? 4 * CH * 4 : 0); }
 };
 
-// Parts of dq and dk, to be summed over a group's value heads (k_linear_group_sum): for bf16 in 16 bits, 11 of them
-// significant, as multiples of a power of two that the 16 CT columns of a wave's row share. That is off by at most
-// 2^-12 of the largest of them, an eighth of the sum's own rounding, so that parts that cancel to an eighth still leave
-// it that; bf16 parts would not. (32,768 tokens, 16/48 heads, 128 wide, whole backward: FP32 parts 2090 us, these 1934.)
+// Parts of dq and dk, to be summed over a group's value heads (k_linear_group_sum): for bf16 as f16 multiples of a power
+// of two that the 16 CT columns of a wave's row share, so that each keeps 11 bits, down to 2^-28 of the largest. That is
+// off by 2^-12, a sixteenth of the sum's own rounding, and parts that cancel to a tenth still leave it that; bf16 parts
+// would not. (32,768 tokens, 16/48 heads, 128 wide, whole backward: FP32 parts 2090 us, these 1934.)
 // What is not finite makes its columns of the row NaN.
 template <int CT>
 struct PartRow {
@@ -850,26 +855,29 @@ __device__ __forceinline__ void segment_walk(const LinearArgs& a, int block) {
 
 template <typename T, int D>
 __global__ __launch_bounds__(NTHREADS, sizeof(T) == 2 ? 2 : 1) void k_linear_walk(LinearArgs a) {
-  segment_walk<T, D, false, false>(a, blockIdx.x);
+  segment_walk<T, D, false, false>(a, block_index());
 }
 // The backward's three in one launch, `blocks` workgroups each: dq, dk, dv.
 template <typename T, int D, bool DOTS>
 __global__ __launch_bounds__(NTHREADS, sizeof(T) == 2 ? 2 : 1) void k_linear_walks(LinearJobs j, int blocks) {
-  const int b = blockIdx.x;
+  const int b = block_index();
   if (b < blocks) segment_walk<T, D, false, DOTS>(j.job[0], b);
   else if (b < 2 * blocks) segment_walk<T, D, true, DOTS>(j.job[1], b - blocks);
   else segment_walk<T, D, true, false>(j.job[2], b - 2 * blocks);
 }
 
 // ------------------------------------------------------------------------------------------------
-// Sums over the value heads of a group, in their order and in FP32: part [T, HV, D] -> out [T, H, D], for dq and dk. It
-// costs moving the parts: 1.1 GB of 16-bit ones at 32,768 tokens, 16/48 heads, 128 wide take 196 us (FP32 ones 355).
+// Sums over the value heads of a group, in their order and in FP32: part [T, HV, D] -> out [T, H, D], for dq and dk, but
+// for rows of no document, whose parts nobody wrote. It costs moving the parts: 1.1 GB of 16-bit ones at 32,768 tokens,
+// 16/48 heads, 128 wide take 196 us (FP32 ones 355).
 template <typename T, int D>
 __global__ __launch_bounds__(256) void k_linear_group_sum(LinearJobs jobs) {
   const LinearArgs& a = jobs.job[blockIdx.y];
   const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8, n = (int64_t)a.T * a.H * D;
   if (i >= n) return;
-  const int64_t head = i / D * a.G;
+  const int64_t row = i / D; // of [T, H]
+  if (row < (int64_t)cut_to(a.cu[0], a.T) * a.H || row >= (int64_t)cut_to(a.cu[a.N], a.T) * a.H) return;
+  const int64_t head = row * a.G;
   const int col = (int)(i % D);
   float s[8];
 #pragma unroll
@@ -991,7 +999,7 @@ static int states_t(const LinearJobs& j, int n, hipStream_t s) {
   static std::atomic<uint64_t> asked{0};
   if (const int e = ask_lds(reinterpret_cast<const void*>(&k_linear_states<T, D>), lds, asked)) return e;
   const unsigned blocks = place_blocks(j.job[0]);
-  hipLaunchKernelGGL((k_linear_states<T, D>), dim3(blocks * n), dim3(NTHREADS), lds, s, j, (int)blocks);
+  hipLaunchKernelGGL((k_linear_states<T, D>), many_blocks(blocks * n), dim3(NTHREADS), lds, s, j, (int)blocks);
   return (int)hipGetLastError();
 }
 template <typename T, int D>
@@ -999,7 +1007,7 @@ static int walk_t(const LinearArgs& a, hipStream_t s) {
   constexpr unsigned lds = WalkLds<T, D>::bytes(false);
   static std::atomic<uint64_t> asked{0};
   if (const int e = ask_lds(reinterpret_cast<const void*>(&k_linear_walk<T, D>), lds, asked)) return e;
-  hipLaunchKernelGGL((k_linear_walk<T, D>), dim3(place_blocks(a)), dim3(NTHREADS), lds, s, a);
+  hipLaunchKernelGGL((k_linear_walk<T, D>), many_blocks(place_blocks(a)), dim3(NTHREADS), lds, s, a);
   return (int)hipGetLastError();
 }
 template <typename T, int D, bool DOTS>
@@ -1008,7 +1016,7 @@ static int walks_t(const LinearJobs& j, hipStream_t s) {
   static std::atomic<uint64_t> asked{0};
   if (const int e = ask_lds(reinterpret_cast<const void*>(&k_linear_walks<T, D, DOTS>), lds, asked)) return e;
   const unsigned blocks = place_blocks(j.job[0]);
-  hipLaunchKernelGGL((k_linear_walks<T, D, DOTS>), dim3(3 * blocks), dim3(NTHREADS), lds, s, j, (int)blocks);
+  hipLaunchKernelGGL((k_linear_walks<T, D, DOTS>), many_blocks(3 * blocks), dim3(NTHREADS), lds, s, j, (int)blocks);
   return (int)hipGetLastError();
 }
 template <typename T, int D>

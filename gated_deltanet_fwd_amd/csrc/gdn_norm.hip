@@ -74,7 +74,7 @@ __global__ __launch_bounds__(LANES > 256 ? LANES : 256) void k_norm_fwd(NormArgs
   constexpr int PER = LANES < 256 ? 256 / LANES : 1;
   __shared__ float tmp[LANES / 64 < 4 ? 4 : LANES / 64];
   const int lane = threadIdx.x % LANES;
-  const int64_t row = (int64_t)blockIdx.x * PER + threadIdx.x / LANES;
+  const int64_t row = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * PER + threadIdx.x / LANES;
   if (row >= a.rows) return; // (LANES > 64: the whole workgroup)
   const T* x = (const T*)a.x + row * a.xs;
   float v[NP][8], sum = 0.f;
@@ -275,7 +275,9 @@ int norm_blocks(const NormArgs& a) {
 template <typename T, int LANES, int NP>
 static int norm_t(const NormArgs& a, bool bwd, hipStream_t s) {
   constexpr int PER = LANES < 256 ? 256 / LANES : 1, THREADS = LANES > 256 ? LANES : 256;
-  if (!bwd) hipLaunchKernelGGL((k_norm_fwd<T, LANES, NP>), dim3((unsigned)((a.rows + PER - 1) / PER)), dim3(THREADS), 0, s, a);
+  // one dimension of a launch holds less than 2^32 threads
+  const int64_t blocks = (a.rows + PER - 1) / PER, x = blocks < (1 << 20) ? blocks : 1 << 20;
+  if (!bwd) hipLaunchKernelGGL((k_norm_fwd<T, LANES, NP>), dim3((unsigned)x, (unsigned)((blocks + x - 1) / x)), dim3(THREADS), 0, s, a);
   else hipLaunchKernelGGL((k_norm_bwd<T, LANES, NP>), dim3((unsigned)norm_blocks(a)), dim3(THREADS), 0, s, a);
   return (int)hipGetLastError();
 }

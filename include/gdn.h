@@ -402,11 +402,12 @@ int gdn_conv_step(const gdn_conv_step_problem* p, const void* x, const float* we
  *
  * S_0 = h0[n,h] (or 0) and ht[n,h] = S_last as in gdn_fwd. The log decays g are one for each token and
  * head (GDN_DECAY_TOKEN, [T, HV]) or one for each head (GDN_DECAY_HEAD, [HV]). Layouts as at the top of
- * this file (g may start at any of its values); q, k and v may be parts of one row (their strides in the problem). o and the gradients are
- * contiguous. States, decays and sums are FP32 (the sums of the log decays 64-bit); for bf16 the decayed
- * products of a chunk and the state that they meet are rounded once to bf16 for o, dq, dk and dv, which are
- * rounded to it themselves. ht, dh0 and dg keep FP32's accuracy. All sums have a fixed order: the
- * same call gives the same bits.
+ * this file (g may start at any of its values); q, k and v may be parts of one row (their strides in the
+ * problem). o and the gradients are contiguous and no buffers of the inputs. States, decays and sums are FP32
+ * (the sums of the log decays 64-bit); for bf16 the decayed products of a chunk and the state that they meet are
+ * rounded once to bf16 for o, dv and, without dg, dq and dk, which are rounded to it themselves; of a group's
+ * value heads each head's dq and dk are rounded to 11 bits before their sum. ht, dh0 and dg keep FP32's
+ * accuracy. All sums have a fixed order: the same call gives the same bits.
  *
  * A document goes in chunks of 64 tokens, and what is not finite in a token reaches, through zeros of
  * masked products, all tokens of its chunk (forward also earlier ones), then what depends on the state;
@@ -423,7 +424,7 @@ int gdn_conv_step(const gdn_conv_step_problem* p, const void* x, const float* we
 typedef struct gdn_linear_problem {
   int32_t n_seqs;                 /* N documents, 1 .. 65535 (of zero tokens or more) */
   int32_t h_qk;                   /* H q/k heads */
-  int32_t h_v;                    /* HV value heads, a multiple of H; HV d at most 2^22 */
+  int32_t h_v;                    /* HV value heads, a multiple of H, at most 65535; HV d at most 2^22 */
   int32_t d;                      /* head dim, 64 or 128 */
   int64_t n_tokens;               /* T = cu_seqlens[N], at most 2^31 - 2^20 */
   int32_t dtype;                  /* GDN_DTYPE_* of q, k, v, o and their gradients */
@@ -515,7 +516,7 @@ int gdn_rms_norm_fwd(const gdn_rms_norm_problem* p, const void* x, const float* 
 
 /* Backward of the GDN_OUT_IO form at x' = x (what the forward left in residual_out): dx = the gradient of x'
  * through y plus d_residual (that of residual_out; NULL: 0), which is the gradient of the forward's x and
- * residual alike; dweight f32 [d] (NULL: not wanted), summed in a fixed order. dx may be dy or d_residual. */
+ * residual alike; dweight f32 [d] (NULL: not wanted), summed in a fixed order. dx may be dy or a contiguous d_residual or x. */
 int gdn_rms_norm_bwd(const gdn_rms_norm_problem* p, const void* x, const float* weight, const void* dy,
                      const void* d_residual, void* dx, float* dweight, void* workspace, size_t workspace_bytes, void* stream);
 

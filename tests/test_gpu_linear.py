@@ -186,6 +186,23 @@ def test_rows_of_no_document_stay():
         c.check((f[0][:end], f[1]), {x: (y if x == "dh0" else y[:end]) for x, y in b.items()})
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H", [2, 6])
+def test_gradients_outside_the_documents_stay(dtype, H):
+    """Documents from a later first token to an earlier last one: every row of no document keeps what it held."""
+    for lengths, cu in (([100, 90], [7, 20, 100]), ([3000, 500], [64, 2000, 2700])):
+        c = Case(lengths, H, 6, 64, dtype, seed=14)
+        c.cu = torch.tensor(cu, dtype=torch.int32, device=DEV)
+        o = torch.full_like(c.v.contiguous(), 7.0)
+        grads = dict(dq=torch.full_like(c.q.contiguous(), 7.0), dk=torch.full_like(c.q.contiguous(), 7.0), dv=o.clone(),
+                     dg=torch.full_like(c.g, 7.0))
+        c.fwd(o=o)
+        b = c.bwd(grads=grads)
+        inside = slice(cu[0], cu[-1])
+        for x in (o, b["dq"], b["dk"], b["dv"], b["dg"]):
+            assert (x[:cu[0]] == 7).all() and (x[cu[-1]:] == 7).all() and not (x[inside] == 7).all()
+
+
 def test_lengths_outside_the_tokens_are_cut():
     """cu_seqlens that falls or leaves [0, T] on the device: nothing outside the buffers is touched, later calls are whole."""
     c = Case([300, 200, 600], 1, 2, 64, seed=9)

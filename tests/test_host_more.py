@@ -31,7 +31,7 @@ def lin_bwd(p, dO=PTR, dg=PTR, h0=None, dh0=None, ws=PTR, nbytes=1 << 40):
     ("n_seqs", 0, 1, "n_seqs"), ("n_seqs", 65536, 1, "n_seqs"), ("h_v", 3, 1, "multiple"), ("h_qk", 0, 1, "head counts"),
     ("d", 96, 2, "64 or 128"), ("dtype", 2, 2, "dtype"), ("decay", 2, 1, "decay"), ("scale", float("nan"), 1, "scale"),
     ("scale", float("inf"), 1, "scale"), ("reserved0", 1, 1, "reserved0"), ("n_tokens", 74, 1, "n_tokens"),
-    ("h_v", 2 * 65536, 1, "2^22"), ("q_stride", 120, 1, "q_stride"), ("k_stride", 129, 1, "k_stride"),
+    ("h_v", 2 * 65536, 1, "2^22"), ("h_v", 65536, 1, "65535"), ("q_stride", 120, 1, "q_stride"), ("k_stride", 129, 1, "k_stride"),
     ("v_stride", 255, 1, "v_stride"), ("q_stride", (1 << 22) + 8, 1, "2^22"),
 ])
 def test_linear_problem_refusals(field, value, code, text):
