@@ -4,14 +4,13 @@
 //   S = exp(g) S + k v^T,  o = scale S^T q
 //
 // A wave holds COLS columns of one head's state (a column is a value index; they never mix) in registers from the first
-// token to the last, as k_recurrent_step does. It costs moving the states. They are read and written
-// non-temporally, a row leaves as soon as it is made (nothing of a new state waits for a sum), and few waves share
-// a CU (STEP_LDS bytes of LDS that nobody uses leave two workgroups a CU). Absent states are buffers of no bytes.
+// token to the last, as k_recurrent_step does. It costs moving the states: 256 sequences of 48 heads, 128 wide, one
+// token each, 1.61 GB in 266 us (6.05 TB/s; two workgroups a CU, held apart by LDS, 294 us). States are read and written
+// non-temporally, and a row leaves as soon as it is made (nothing of a new state waits for a sum). Absent states are
+// buffers of no bytes.
 #include "gdn_step.h"
 
 namespace gdn {
-
-constexpr unsigned LINEAR_STEP_LDS = 64 * 1024;
 
 template <typename TI, int D, bool ONE, bool KEEP, int COLS> // one token a sequence; with slot_tok
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(ONE ? 3 : 1, ONE ? 3 : 8))) void k_linear_step(LinearStepArgs a) {
@@ -125,7 +124,11 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(ONE ? 3 : 1
   }
 }
 
-// Columns a wave and waves a workgroup by the number of waves of 32 columns, as in gdn_recurrent.hip.
+// Waves a workgroup and columns a wave by the number of waves of 32 columns (us, states from memory, 48 heads, 128 wide).
+// One wave a workgroup spreads few over all CUs, four keep a CU's waves on neighbouring columns: one token, 192 waves 3.5
+// and 4.5, 1152 waves 9.2 and 10.3, 2112 waves 15.0 and 15.5, 3072 waves 19.7 and 18.9, 49,152 waves 301 and 267. Half the
+// columns halve a token's chain where there are several and few waves: four tokens, 16 waves 4.3 and 4.8, 256 waves
+// 5.9 either way (states in cache 5.1 and 5.5), 768 waves 8.6 and 8.2.
 template <typename TI, int D, bool ONE, bool KEEP>
 static int linear_step_t(const LinearStepArgs& a, hipStream_t s) {
   constexpr int64_t SPREAD = 1280, HALVED = 384;
@@ -137,8 +140,7 @@ static int linear_step_t(const LinearStepArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((k_linear_step<TI, D, ONE, KEEP, COLS>), grid((a.HV * (D / COLS) + GROUP - 1) / GROUP), dim3(64 * GROUP), 0, s, a);
   } else {
     const int group = waves <= SPREAD ? 1 : 4;
-    hipLaunchKernelGGL((k_linear_step<TI, D, ONE, KEEP, 32>), grid((a.HV * (D / 32) + group - 1) / group), dim3(64 * group),
-                       group == 1 ? 0 : LINEAR_STEP_LDS, s, a);
+    hipLaunchKernelGGL((k_linear_step<TI, D, ONE, KEEP, 32>), grid((a.HV * (D / 32) + group - 1) / group), dim3(64 * group), 0, s, a);
   }
   return (int)hipGetLastError();
 }

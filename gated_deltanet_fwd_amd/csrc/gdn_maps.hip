@@ -2,6 +2,8 @@
 // slots. Integers and a few kilobytes: it costs its latency, a chain of a few memory accesses and barriers. The whole
 // of it depends on two running sums over the requests (tokens, new blocks), which every workgroup makes for itself
 // in LDS, at once with the others, rather than wait for one that makes them for all.
+#include <algorithm>
+
 #include "gdn_device.h"
 
 namespace gdn {
@@ -131,32 +133,36 @@ __global__ __launch_bounds__(THREADS) void k_maps(MapsArgs a) {
   }
 }
 
-// Up to ALONE tokens one workgroup makes everything (of 256 threads where they are few: a barrier of 4 waves). More
-// tokens take more workgroups, and then contexts and the count, if they are to move on in place, wait for a launch
-// of their own: another workgroup may still be reading them.
+// A workgroup for every THREADS tokens. Every one sums over all requests, at the price of its barriers' waves: 256 threads
+// up to 512 requests, 1024 for more (us: 256 requests, 16,384 tokens 3.8 and 5.1; 512, 4096 tokens 4.5 and 5.0;
+// 4096 requests 17.8 and 13.7).
+template <int THREADS>
+static int maps_t(const MapsArgs& a, int groups, hipStream_t s) {
+  hipLaunchKernelGGL(k_maps<THREADS>, dim3((unsigned)groups), dim3(THREADS), 0, s, a);
+  return (int)hipGetLastError();
+}
+static int maps_any(const MapsArgs& a, int tokens, hipStream_t s) { // for `tokens` tokens a workgroup each of its threads'
+  const int most = 1024;
+  if (a.N <= 512) return maps_t<256>(a, std::max(1, std::min(most, (int)(((int64_t)tokens + 255) / 256))), s);
+  return maps_t<1024>(a, std::max(1, std::min(most, (int)(((int64_t)tokens + 1023) / 1024))), s);
+}
+
+// Contexts and the count that move on in place may still be read by another workgroup, so few tokens are left to one
+// workgroup, and for more they wait for a launch of their own (us, alone and so: 256 requests, 1024 tokens 5.0 and 7.1; 64,
+// 2048 tokens 5.9 and 6.4; 512, 4096 tokens 8.5 and 7.2; 4096 requests and tokens 17.9 and 23.2, another 1.1 alone for each
+// 1024 tokens). Alone with 256 threads up to 512 tokens (64 requests: 4.2 us, with 1024 threads 4.6; 2048 tokens 9.3, 5.9).
 int launch_maps(const MapsArgs& a0, void* stream) {
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  constexpr int ALONE = 4096;
   MapsArgs a = a0;
   a.fill = 1;
-  if (a.T <= ALONE) {
-    if (a.N <= 256 && a.T <= 1024) hipLaunchKernelGGL(k_maps<256>, dim3(1), dim3(256), 0, s, a);
-    else hipLaunchKernelGGL(k_maps<1024>, dim3(1), dim3(1024), 0, s, a);
-    return (int)hipGetLastError();
-  }
-  const bool in_place = a.contexts_out == a.contexts || a.free_count_out == a.free_count;
+  if (a.contexts_out != a.contexts && a.free_count_out != a.free_count) return maps_any(a, a.T, s);
+  if (a.T <= (a.N <= 512 ? 2048 : 8192)) return a.T <= 512 ? maps_any(a, 1, s) : maps_t<1024>(a, 1, s);
   MapsArgs rest = a;
-  if (in_place) {
-    a.contexts_out = a.free_count_out = nullptr;
-    rest.cu = rest.granted = rest.slot_in = rest.slot_out = nullptr;
-    rest.fill = 0;
-  }
-  const int groups = (a.T + 1023) / 1024;
-  hipLaunchKernelGGL(k_maps<1024>, dim3((unsigned)(groups < 512 ? groups : 512)), dim3(1024), 0, s, a);
-  if (const int e = (int)hipGetLastError()) return e;
-  if (!in_place) return 0;
-  hipLaunchKernelGGL(k_maps<1024>, dim3(1), dim3(1024), 0, s, rest);
-  return (int)hipGetLastError();
+  a.contexts_out = a.free_count_out = nullptr;
+  rest.cu = rest.granted = rest.slot_in = rest.slot_out = nullptr;
+  rest.fill = 0;
+  if (const int e = maps_any(a, a.T, s)) return e;
+  return maps_any(rest, 1, s);
 }
 
 } // namespace gdn

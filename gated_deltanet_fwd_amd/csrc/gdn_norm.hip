@@ -6,6 +6,8 @@
 //
 // It costs moving the rows once. LANES lanes take a row, 8 neighbouring values a lane and pass, and keep it in
 // registers between the sum and its use.
+#include <algorithm>
+
 #include "gdn_device.h"
 
 namespace gdn {
@@ -263,13 +265,17 @@ __global__ __launch_bounds__(1024) void k_norm_dw(NormArgs a, int blocks) {
   if (x == 0 && blockIdx.x * 32 + y < (unsigned)a.D) a.dw[blockIdx.x * 32 + y] = sum;
 }
 
-// Lanes a row: a wave takes a row of up to 2048 values, a workgroup a longer one, or any of several hundred where
-// there are few rows.
-static bool by_wave(const NormArgs& a) { return a.D <= 512 || (a.D <= 2048 && a.rows > 1024); }
+// Lanes a row: a wave takes a short row, a workgroup a long one (us, bf16, forward with residual: 512 wide, 16,384 rows
+// 10.0 by waves, 14.1 by workgroups, 1024 rows 2.9 and 3.1; 1024 wide 17.2 and 19.5, but 3.8 and 3.5 at 1024 rows;
+// 2048 wide, 16,384 rows, 37 and 31. Backward, 1024 wide: 18.5 and 28.2, 5.3 and 5.6 at 128 rows).
+static bool by_wave(const NormArgs& a, bool bwd) { return a.D <= 512 || (a.D <= 1024 && (bwd || a.rows > 1024)); }
 
+// Workgroups of the backward: each leaves a row of sums to be added, and so takes four rows at least unless that would
+// leave CUs idle (2048 wide, 1024 rows: 9.3 us; one row each 11.9), and many where there are many: 1024 of 256
+// threads (2048 wide, 16,384 rows: 31 us, 512 43, 2048 35) or 512 of 1024 (16,384 wide: 257 us, 1024 274).
 int norm_blocks(const NormArgs& a) {
-  const int64_t groups = by_wave(a) ? (a.rows + 3) / 4 : a.rows;
-  return (int)(groups < 1024 ? groups : 1024);
+  const int64_t four = (a.rows + 3) / 4, rows = by_wave(a, true) ? four : std::max(four, std::min<int64_t>(a.rows, 256));
+  return (int)std::min<int64_t>(rows, a.D > 8192 ? 512 : 1024);
 }
 
 template <typename T, int LANES, int NP>
@@ -283,10 +289,7 @@ static int norm_t(const NormArgs& a, bool bwd, hipStream_t s) {
 }
 template <typename T>
 static int norm_any(const NormArgs& a, bool bwd, hipStream_t s) {
-  if (by_wave(a)) {
-    if (a.D <= 512) return norm_t<T, 64, 1>(a, bwd, s);
-    return a.D <= 1024 ? norm_t<T, 64, 2>(a, bwd, s) : norm_t<T, 64, 4>(a, bwd, s);
-  }
+  if (by_wave(a, bwd)) return a.D <= 512 ? norm_t<T, 64, 1>(a, bwd, s) : norm_t<T, 64, 2>(a, bwd, s);
   if (a.D <= 2048) return norm_t<T, 256, 1>(a, bwd, s);
   if (a.D <= 4096) return norm_t<T, 256, 2>(a, bwd, s);
   return a.D <= 8192 ? norm_t<T, 256, 4>(a, bwd, s) : norm_t<T, 1024, 2>(a, bwd, s);
