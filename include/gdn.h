@@ -456,8 +456,8 @@ int gdn_linear_bwd(const gdn_linear_problem* p, const void* q, const void* k, co
                    void* dv, float* dg, float* dh0, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Its serving step on cached states, token by token in FP32: slots, cu_seqlens, slot_tok and the checks on
- * the device are gdn_recurrent's. For prompts gdn_linear_fwd is faster, whose h0 and ht have the layout of cached
- * states. */
+ * the device are gdn_recurrent's. From runs of about 12 tokens on gdn_linear_fwd is faster, whose h0 and ht have
+ * the layout of cached states. */
 typedef struct gdn_linear_step_problem {
   int32_t n_seqs;                 /* N >= 1 sequences (of zero tokens or more); N and T at most 2^31 - 2^20 */
   int32_t h_qk;                   /* H q/k heads */
