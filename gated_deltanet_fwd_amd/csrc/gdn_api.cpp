@@ -1441,16 +1441,18 @@ int check_linear(const gdn_linear_problem* p) {
   return GDN_OK;
 }
 
-// Tokens of a segment (0: whole documents), the cheapest by a model of the call: a CU takes a chunk of a walk after
-// the other (two workgroups on it are as fast as one after the other), the states' pass costs 0.4 of a walk's
-// chunk, a border between segments a step of the scan, a workgroup its start, and states and scan their launches.
-// Microseconds, fitted to 18 shapes with 1 to 40 documents of 30 to 65,536 tokens, 1 to 48 value heads,
-// both widths and types, each measured at up to 17 sizes of a segment: what it picks was 2% slower than the best in the
-// mean, 16% at most.
+// Tokens of a segment (0: whole documents), the cheapest by a model of the call, in microseconds. A pass of `total` chunks in
+// `groups` workgroups of at most `steps` takes their length while each has a CU, and otherwise the CUs' share or a longer
+// length; rounds of workgroups have a price, and with segments there is the pass over the states, a step of the scan for
+// each border and the launches. Fitted to 23 shapes with 1 to 40 documents of 30 to 65,536 tokens, 1 to 48 value
+// heads, both widths and types, forward and backward, each measured at up to 26 sizes of a segment, for the ratio of what it
+// picks to the best alone (the constants are no durations): 1.1% slower in the mean, 11% at most.
 int linear_segment(const gdn_linear_problem* p, int op) {
-  constexpr double CHUNK = 6.0, GRADS = 2.3, STATE = 0.4, TAIL = 0.14, START = 1.2, BORDER = 0.25, LAUNCHES = 13.0, CUS = 256.0;
-  static constexpr int SIZES[] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 16, 20, 24, 32, 40, 64};
-  const int walks = op == GDN_OP_BWD ? 3 : 1, passes = op == GDN_OP_BWD ? 2 : 1;
+  constexpr double CHUNK = 3.473, GRADS = 0.557, STATE = 1.691, BOTH = 1.398, SHARE = 0.786, TAIL = 0.041, WALKS = 0.116,
+                   STATES = 1.566, BORDER = 0.347, LAUNCHES = 3.01, CUS = 256.0;
+  static constexpr int SIZES[] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16, 18, 20, 22, 24, 26, 28, 32, 36, 40, 44, 48, 52, 56, 64};
+  const bool bwd = op == GDN_OP_BWD;
+  const int walks = bwd ? 3 : 1, passes = bwd ? 2 : 1;
   const int32_t* cu = p->cu_seqlens_host;
   int longest = 0;
   int64_t all = 0; // chunks
@@ -1459,29 +1461,29 @@ int linear_segment(const gdn_linear_problem* p, int op) {
     longest = std::max(longest, chunks);
     all += chunks;
   }
-  const double hv = p->h_v, chunk = CHUNK * (op == GDN_OP_BWD ? GRADS : 1.0), total = walks * hv * all / CUS;
-  const auto walk = [&](double steps, double workgroups) {
-    return chunk * std::max(steps, total + TAIL * steps) + START * walks * hv * workgroups / CUS;
+  const double hv = p->h_v;
+  const auto pass = [&](double groups, double total, double steps, double price) {
+    if (groups == 0) return 0.0;
+    return (groups <= CUS ? steps : std::max(BOTH * steps, SHARE * total / CUS + TAIL * steps)) + price * std::max(groups / (2 * CUS), 0.5);
+  };
+  const auto walk = [&](double steps, double segs) {
+    return CHUNK * (bwd ? GRADS : 1.0) * pass(walks * hv * segs, walks * hv * all, steps, WALKS);
   };
   // dg's roundings add up between borders, as the root of a segment: 5e-7 of dg over 512 tokens and 7e-7 over 1024
   // (bf16), 8e-7 and 1.1e-6 (f32), and more where dg is itself a sum over the tokens. So segments end there.
-  const int most = op != GDN_OP_BWD ? INT_MAX : p->dtype == GDN_DTYPE_BF16 && p->decay == GDN_DECAY_TOKEN ? 16 : 8;
+  const int most = !bwd ? INT_MAX : p->dtype == GDN_DTYPE_BF16 && p->decay == GDN_DECAY_TOKEN ? 16 : 8;
   double best = longest <= most ? walk(longest, p->n_seqs) : INFINITY;
   int seg = 0;
   // many documents fill the chip by themselves, or are not worth the host's time for every size
-  const int stride = p->n_seqs > 64 ? 4 : 1;
+  const int stride = p->n_seqs > 32 ? 4 : 1;
   for (int i = stride - 1; i < (int)(sizeof SIZES / sizeof *SIZES); i += stride) {
     const int s = SIZES[i];
     if (s >= longest || s > most) break;
-    int64_t segs = 0, empty = 0;
-    for (int n = 0; n < p->n_seqs; ++n) {
-      const int len = cu[n + 1] - cu[n];
-      segs += (len + s * kChunk - 1) / (s * kChunk);
-      empty += len == 0;
-    }
-    const double states = passes * hv * (segs + empty - p->n_seqs);
-    const double cost = walk(s, segs + empty) + STATE * CHUNK * std::max((double)s, states * s / CUS + TAIL * s) +
-                        START * states / CUS + passes * BORDER * ((longest + s - 1) / s) + LAUNCHES;
+    int64_t segs = 0;
+    for (int n = 0; n < p->n_seqs; ++n) segs += std::max((cu[n + 1] - cu[n] + s * kChunk - 1) / (s * kChunk), 1);
+    const double states = passes * hv * (segs - p->n_seqs);
+    const double cost = walk(s, segs) + STATE * CHUNK * pass(states, states * s, s, STATES) +
+                        passes * BORDER * ((longest + s - 1) / s) + LAUNCHES;
     if (cost < best) {
       best = cost;
       seg = s * kChunk;

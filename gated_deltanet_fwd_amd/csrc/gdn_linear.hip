@@ -548,10 +548,11 @@ __global__ __launch_bounds__(256) void k_linear_scan(LinearArgs a, const float* 
 // document ends with), and as 2 where it is not: that leaves 2^-17 of each term, nothing beside W's own rounding
 // (32,768 tokens, 48 heads, 128 wide, whole forward: one document 490 us, as 3 terms 504; four 495 and 500).
 //
-// Bound by instructions: a chunk takes a wave some 130 matrix, 650 vector and 130 LDS instructions in the forward, each kind
-// 4000 to 5000 cycles of a CU with two workgroups, and two waves a SIMD overlap them in part: 10,000 cycles. The same 32,768
-// tokens: forward 209 GFLOP of matrix instructions in 330 us, the backward's three 957 GFLOP in 1420 us, at the 1.7 GHz to
-// which the card's power limit brings the clock; a library product of 8192^3 reaches 1170 TFLOP/s there.
+// Bound by the chain of a chunk's phases: some 130 matrix, 650 vector and 130 LDS instructions a wave in the forward, each
+// kind 4000 to 5000 cycles of a CU with two workgroups, which two waves a SIMD overlap in part: 10,000 cycles. A third
+// fewer matrix instructions in W's sum (above) gain 0 to 3%, a tenth fewer vector instructions 1.5% (the state's decay kept
+// apart from W, which lost bits of ht and dg). The same 32,768 tokens: forward 209 GFLOP of matrix instructions in 330 us,
+// the backward's three 957 GFLOP in 1420 us, at the 1.7 GHz to which the card's power limit brings the clock.
 template <typename T, int D>
 struct WalkLds {
   static constexpr int P = 4 * Tile<T, D>::BYTES, P_TILE = 256;      // P: 10 tiles of 256 values
