@@ -126,7 +126,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(ONE ? 3 : 1
 
 // Waves a workgroup and columns a wave by the number of waves of 32 columns (us, states from memory, 48 heads, 128 wide).
 // One wave a workgroup spreads few over all CUs, four keep a CU's waves on neighbouring columns: one token, 192 waves 3.5
-// and 4.5, 1152 waves 9.2 and 10.3, 2112 waves 15.0 and 15.5, 3072 waves 19.7 and 18.9, 49,152 waves 301 and 267. Half the
+// and 4.5, 1152 waves 9.2 and 10.3, 2112 waves 15.0 and 15.5, 12,288 waves 74.5 and 67.6, 49,152 waves 301 and 267. Half the
 // columns halve a token's chain where there are several and few waves: four tokens, 16 waves 4.3 and 4.8, 256 waves
 // 5.9 either way (states in cache 5.1 and 5.5), 768 waves 8.6 and 8.2.
 template <typename TI, int D, bool ONE, bool KEEP>
