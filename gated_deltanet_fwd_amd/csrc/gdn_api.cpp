@@ -1615,6 +1615,7 @@ int gdn_linear_fwd(const gdn_linear_problem* p, const void* q, const void* k, co
   a.decay = (float*)(w + L.Sdecay);
   if (L.seg) {
     gdn::LinearJobs j;
+    std::memset(&j, 0, sizeof j);
     j.job[0] = a;
     LAUNCH("gdn_linear_states", gdn::launch_linear_states(j, 1, p->dtype, stream));
     LAUNCH("gdn_linear_scan", gdn::launch_linear_scan(a, false, nullptr, nullptr, stream));
@@ -1660,6 +1661,7 @@ int gdn_linear_bwd(const gdn_linear_problem* p, const void* q, const void* k, co
   r.decay = (float*)(w + L.Ddecay);
   r.w_scale = p->scale;
   gdn::LinearJobs j;
+  std::memset(&j, 0, sizeof j);
   if (L.seg) {
     j.job[0] = f;
     j.job[0].b = c.k;

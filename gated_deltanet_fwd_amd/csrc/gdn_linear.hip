@@ -466,10 +466,12 @@ __device__ __forceinline__ void segment_state(const LinearArgs& a, int block) {
   }
 }
 
-// Forward and, behind it in the same launch (`blocks` workgroups each), reverse.
+// Forward and, with n = 2 behind it in the same launch (`blocks` workgroups each), reverse. A launch of two dimensions has
+// workgroups behind the last job's: these return before a job is chosen, which with n = 1 is the only one there is.
 template <typename T, int D>
-__global__ __launch_bounds__(NTHREADS, sizeof(T) == 2 ? 2 : 1) void k_linear_states(LinearJobs j, int blocks) {
+__global__ __launch_bounds__(NTHREADS, sizeof(T) == 2 ? 2 : 1) void k_linear_states(LinearJobs j, int blocks, int n) {
   const int b = block_index();
+  if (b >= n * blocks) return;
   if (b < blocks) segment_state<T, D, false>(j.job[0], b);
   else segment_state<T, D, true>(j.job[1], b - blocks);
 }
@@ -867,7 +869,8 @@ template <typename T, int D>
 __global__ __launch_bounds__(NTHREADS, sizeof(T) == 2 ? 2 : 1) void k_linear_walk(LinearArgs a) {
   segment_walk<T, D, false, false>(a, block_index());
 }
-// The backward's three in one launch, `blocks` workgroups each: dq, dk, dv.
+// The backward's three in one launch, `blocks` workgroups each: dq, dk, dv. What a launch of two dimensions has behind them
+// (here and in the forward's walk) is refused by place(): its slot is past the last.
 template <typename T, int D, bool DOTS>
 __global__ __launch_bounds__(NTHREADS, sizeof(T) == 2 ? 2 : 1) void k_linear_walks(LinearJobs j, int blocks) {
   const int b = block_index();
@@ -1009,7 +1012,7 @@ static int states_t(const LinearJobs& j, int n, hipStream_t s) {
   static std::atomic<uint64_t> asked{0};
   if (const int e = ask_lds(reinterpret_cast<const void*>(&k_linear_states<T, D>), lds, asked)) return e;
   const unsigned blocks = place_blocks(j.job[0]);
-  hipLaunchKernelGGL((k_linear_states<T, D>), many_blocks(blocks * n), dim3(NTHREADS), lds, s, j, (int)blocks);
+  hipLaunchKernelGGL((k_linear_states<T, D>), many_blocks(blocks * n), dim3(NTHREADS), lds, s, j, (int)blocks, n);
   return (int)hipGetLastError();
 }
 template <typename T, int D>
