@@ -490,8 +490,9 @@ int gdn_linear_step(const gdn_linear_step_problem* p, const void* q, const void*
  * value 448) with an FP32 scale for each row (group = 0) or each `group` values of it: scale = the largest
  * magnitude / 448 (1 where all are zero, at least 2^-126) and y the value nearest to that of the FP32 row over scale,
  * ties to even (for scales of 2^-90 and more; below, of FP32's quotient). y and residual_out may be the inputs'
- * own buffers (of the same row layout): each row is read before it is written. x' has to stay below the root of FP32's range for its squares. With eps = 0 a row of zeros gives NaN.
- * What is not finite stays in its row. */
+ * own buffers (of the same row layout): each row is read before it is written. The squares' sum has to stay in
+ * FP32's range: below its largest number, and with eps = 0 not under its smallest (a row of zeros then gives NaN). What
+ * is not finite stays in its row (and in dweight). */
 #define GDN_OUT_IO 0
 #define GDN_OUT_E4M3 1
 

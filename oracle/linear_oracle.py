@@ -80,3 +80,30 @@ def bwd(cu, q, k, v, g, do, h0=None, dht=None, scale=1.0):
     if by_head:
         r["dg"] = r["dg"].sum(0)
     return r
+
+
+def dg_by_states(cu, q, k, v, g, do, h0=None, dht=None, scale=1.0):
+    """The decays' gradient by its definition, dg_t = e^{g_t} <S_{t-1}, D_t>, with the states S token by token and their
+    gradients D_t = e^{g_{t+1}} D_{t+1} + scale q_t do_t^T (D_T takes dht): for documents too long for a product of
+    all tokens with all. Also [T, HV] |q_t| |dq_t| + |k_t| |dk_t|, of the row products that dg can be summed from, and
+    |S_{t-1}| |D_t| e^{g_t}."""
+    (T, HV, d), group = v.shape, v.shape[1] // q.shape[1]
+    a, head = np.exp(_log_decays(g, T, HV))[..., None, None], np.arange(HV) // group
+    q, k = q[:, head], k[:, head]
+    norm = lambda x, n: np.sqrt((x * x).sum(tuple(range(-n, 0))))  # noqa: E731
+    dg, rows, states = np.zeros((T, HV)), np.zeros((T, HV)), np.zeros((T, HV))
+    for n in range(len(cu) - 1):
+        b, e = cu[n], cu[n + 1]
+        S = np.zeros((e - b + 1, HV, d, d))
+        if h0 is not None:
+            S[0] = h0[n]
+        for t in range(b, e):
+            S[t - b + 1] = a[t] * S[t - b] + k[t][:, :, None] * v[t][:, None, :]
+        D = np.zeros((HV, d, d)) if dht is None else dht[n].copy()
+        for t in range(e - 1, b - 1, -1):
+            D += scale * q[t][:, :, None] * do[t][:, None, :]
+            dq, dk = scale * np.einsum("hkv,hv->hk", S[t - b + 1], do[t]), np.einsum("hkv,hv->hk", D, v[t])
+            rows[t] = norm(q[t], 1) * norm(dq, 1) + norm(k[t], 1) * norm(dk, 1)
+            D *= a[t]
+            dg[t], states[t] = (S[t - b] * D).sum((-1, -2)), norm(S[t - b], 2) * norm(D, 2)
+    return (dg.sum(0) if g.ndim == 1 else dg), rows, states
