@@ -920,7 +920,8 @@ __global__ __launch_bounds__(256) void k_linear_group_sum(LinearJobs jobs) {
 // n tokens, sums from the end and E = <S, D> at the end, dg_t = E + sum_{s >= t} (q_s.dq_s - k_s.dk_s), and at the first
 // token that has to be <S, D> at the start: what it misses is spread evenly over the tokens, which leaves a
 // third of the roundings. At a document's start S is h0 or 0; at its end D is 0, or with dht S is not at hand, and
-// the sum runs from the start alone.
+// the sum runs from the start alone. Where the factor e^g itself is 0 in FP32 (g below the logarithm of half its smallest
+// number) so is dg_t = e^g <S, D>: written as 0, where the sums leave their roundings.
 __global__ __launch_bounds__(256) void k_linear_dg(LinearDgArgs d) {
   const LinearArgs& a = d.a;
   __shared__ double tmp[4], carry[4];
@@ -969,8 +970,9 @@ __global__ __launch_bounds__(256) void k_linear_dg(LinearDgArgs d) {
       before += w < wave ? carry[w] : 0.0;
       turn += carry[w];
     }
-    const double v = from_end ? f + before + p + spread * (j + 1) : f - before - (p - own);
+    double v = from_end ? f + before + p + spread * (j + 1) : f - before - (p - own);
     if (j < n) {
+      if (log_decay(a, h, s.t0 + t, s.t1) < -104.f) v = 0.0;
       if (a.gs) d.dg[(int64_t)(s.t0 + t) * a.HV + h] = (float)v;
       all += v;
     }
