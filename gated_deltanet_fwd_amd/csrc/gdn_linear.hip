@@ -393,7 +393,7 @@ __device__ __forceinline__ void add_to_state(f32x4 (&W)[D / 16][CT], const typen
 extern __shared__ __attribute__((aligned(1024))) char linear_lds[];
 
 // ------------------------------------------------------------------------------------------------
-// What each segment adds to a state, and its decay. The last segment of a document (the first, in reverse)
+// What each segment adds to a state, and the logarithm of its decay. The last segment of a document (the first, in reverse)
 // is left out: no other starts from it. w c goes in as EXACT terms: the states are results in FP32, and
 // everything after them is made from them. Bound by its matrix instructions and by the splitting between them: both
 // directions of 32,768 tokens, 48 heads, 128 wide, 271 GFLOP in 290 us. Two workgroups a CU: one alone leaves it
@@ -462,7 +462,7 @@ __device__ __forceinline__ void segment_state(const LinearArgs& a, int block) {
   if (wave == 0) {
 #pragma unroll
     for (int by = 32; by > 0; by >>= 1) sum += __shfl_xor(sum, by);
-    if (lane == 0) a.decay[(int64_t)slot * a.HV + h] = __builtin_amdgcn_exp2f((float)(sum * 1.4426950408889634));
+    if (lane == 0) a.decay[(int64_t)slot * a.HV + h] = (float)(sum * 1.4426950408889634);
   }
 }
 
@@ -483,6 +483,17 @@ __device__ __forceinline__ double block_sum(double x, double* tmp) { // over 256
   if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = x;
   __syncthreads();
   return (tmp[0] + tmp[1]) + (tmp[2] + tmp[3]);
+}
+
+// W 2^x. Log decays may be positive as long as their sums over a chunk stay in FP32's range; those over a segment need not,
+// and a state of zeros stays one through it.
+__device__ __forceinline__ f32x4 faded(const f32x4& W, float x) {
+  if (!(x > 127.f)) return W * __builtin_amdgcn_exp2f(x);
+  const float whole = __builtin_floorf(__builtin_fminf(x, 1000.f)), part = __builtin_amdgcn_exp2f(__builtin_fminf(x, 1000.f) - whole);
+  f32x4 r;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) r[e] = __builtin_amdgcn_ldexpf(W[e] * part, (int)whole);
+  return r;
 }
 
 // The states that segments start from, in place of what they add: forward from `init` (h0) at the first segment,
@@ -527,7 +538,7 @@ __global__ __launch_bounds__(256) void k_linear_scan(LinearArgs a, const float* 
           if (threadIdx.x == 0) worth[((int64_t)slot(i + j) * a.HV + h) * PARTS + blockIdx.x] = x;
         }
       }
-      W = W * dec[j] + add[j];
+      W = faded(W, dec[j]) + add[j];
     }
   }
 }
