@@ -285,7 +285,8 @@ __device__ __forceinline__ float log_decay(const LinearArgs& a, int h, int t, in
 // 64 rows of an operand from memory to a tile: wave w loads rows 16 w .. of it, through a buffer that ends with
 // the segment, so that rows behind it arrive as zeros. The loads are written in assembly, without output
 // registers: the compiler, which cannot tell one tile from another, would wait for them before every read of any
-// tile. They are waited for by wait_loads before the barrier that hands the tile over.
+// tile. They are waited for by wait_loads before the barrier that hands the tile over. m0 (where in LDS a wave's lanes write) is
+// an operand, so that the compiler sets it and knows until when it is needed; the s_nop stands between the two.
 template <typename T, int D>
 struct Feed {
   typedef Tile<T, D> S;
@@ -308,7 +309,7 @@ struct Feed {
 #pragma unroll
     for (int i = 0; i < S::PIECES; ++i, row += step, to += 1024) {
       const int off = (unit ^ (S::f(i * S::TOGETHER) << 4)) + lane + row;
-      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" : : "s"(to), "v"(off), "s"(from) : "m0", "memory");
+      asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" : : "{m0}"(to), "v"(off), "s"(from) : "memory");
     }
   }
 };
