@@ -249,7 +249,7 @@ struct LinearArgs {
   const float* init; // [N, HV, d, d] states that documents start from (NULL: 0), forward h0, in reverse dht
   float* fin;        // [N, HV, d, d] states that they end with, or NULL
   float* states;     // [slots, HV, d, d] states that segments start from
-  float* decay;      // [slots, HV] log2 of a state's factor over a segment
+  float* decay;      // [slots, HV] factor of a state over a segment
   void* out;         // y: [T, HV, d], or with `part` the sums over groups [T, H, d]
   void* part;        // [T, HV, d] y before those sums, f32 or (for bf16) multiples of `unit` in f16; NULL: y goes to out
   float* unit;       // [T, HV, 4]

@@ -394,7 +394,7 @@ __device__ __forceinline__ void add_to_state(f32x4 (&W)[D / 16][CT], const typen
 extern __shared__ __attribute__((aligned(1024))) char linear_lds[];
 
 // ------------------------------------------------------------------------------------------------
-// What each segment adds to a state, and the logarithm of its decay. The last segment of a document (the first, in reverse)
+// What each segment adds to a state, and its decay. The last segment of a document (the first, in reverse)
 // is left out: no other starts from it. w c goes in as EXACT terms: the states are results in FP32, and
 // everything after them is made from them. Bound by its matrix instructions and by the splitting between them: both
 // directions of 32,768 tokens, 48 heads, 128 wide, 271 GFLOP in 290 us. Two workgroups a CU: one alone leaves it
@@ -463,7 +463,10 @@ __device__ __forceinline__ void segment_state(const LinearArgs& a, int block) {
   if (wave == 0) {
 #pragma unroll
     for (int by = 32; by > 0; by >>= 1) sum += __shfl_xor(sum, by);
-    if (lane == 0) a.decay[(int64_t)slot * a.HV + h] = (float)(sum * 1.4426950408889634);
+    // Rising log decays whose sums over a chunk are in FP32's range may leave it over a segment: a state of zeros stays one (a
+    // test for zeros in the scan, or exponents apart from factors, cost it 1.4 us of 15.5 at 20,001 tokens and 8 heads)
+    const float factor = __builtin_amdgcn_exp2f((float)(sum * 1.4426950408889634));
+    if (lane == 0) a.decay[(int64_t)slot * a.HV + h] = factor > 0x1.fffffep127f ? 0x1.fffffep127f : factor;
   }
 }
 
@@ -484,17 +487,6 @@ __device__ __forceinline__ double block_sum(double x, double* tmp) { // over 256
   if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = x;
   __syncthreads();
   return (tmp[0] + tmp[1]) + (tmp[2] + tmp[3]);
-}
-
-// W 2^x. Log decays may be positive as long as their sums over a chunk stay in FP32's range; those over a segment need not,
-// and a state of zeros stays one through it.
-__device__ __forceinline__ f32x4 faded(const f32x4& W, float x) {
-  if (!(x > 127.f)) return W * __builtin_amdgcn_exp2f(x);
-  const float whole = __builtin_floorf(__builtin_fminf(x, 1000.f)), part = __builtin_amdgcn_exp2f(__builtin_fminf(x, 1000.f) - whole);
-  f32x4 r;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) r[e] = __builtin_amdgcn_ldexpf(W[e] * part, (int)whole);
-  return r;
 }
 
 // The states that segments start from, in place of what they add: forward from `init` (h0) at the first segment,
@@ -539,7 +531,7 @@ __global__ __launch_bounds__(256) void k_linear_scan(LinearArgs a, const float* 
           if (threadIdx.x == 0) worth[((int64_t)slot(i + j) * a.HV + h) * PARTS + blockIdx.x] = x;
         }
       }
-      W = faded(W, dec[j]) + add[j];
+      W = W * dec[j] + add[j];
     }
   }
 }
@@ -973,6 +965,7 @@ __global__ __launch_bounds__(256) void k_linear_dg(LinearDgArgs d) {
   for (int c = 0; c < n; c += 256) { // from the border inwards
     const int j = c + (int)threadIdx.x, t = from_end ? n - 1 - j : j;
     const double own = j < n ? (double)qd[t] - (double)kd[t] : 0.0;
+    const float g = j < n ? log_decay(a, h, s.t0 + t, s.t1) : 0.f;
     const double p = wave_sums(own);
     if (lane == 63) carry[wave] = p;
     __syncthreads();
@@ -984,7 +977,7 @@ __global__ __launch_bounds__(256) void k_linear_dg(LinearDgArgs d) {
     }
     double v = from_end ? f + before + p + spread * (j + 1) : f - before - (p - own);
     if (j < n) {
-      if (log_decay(a, h, s.t0 + t, s.t1) < -104.f) v = 0.0;
+      if (g < -104.f) v = 0.0;
       if (a.gs) d.dg[(int64_t)(s.t0 + t) * a.HV + h] = (float)v;
       all += v;
     }

@@ -411,8 +411,9 @@ int gdn_conv_step(const gdn_conv_step_problem* p, const void* x, const float* we
  *
  * A document goes in chunks of 64 tokens, and what is not finite in a token reaches, through zeros of
  * masked products, all tokens of its chunk (forward also earlier ones), then what depends on the state;
- * other documents never. A log decay of minus infinity drops the state (as any under -10000). Log
- * decays may be positive while their sums over a chunk stay in FP32's range.
+ * other documents never. A log decay of minus infinity drops the state (as any under -10000), and dg is 0 there (as
+ * at any under -104). Log decays may be positive while their sums over a chunk, and over the tokens that a
+ * state other than zero passes, stay in FP32's range.
  *
  * The launch is planned from the host's lengths; the device's cu_seqlens may hold others (a graph that is
  * replayed with other lengths, or a shorter batch: T and N stay), as long as it rises from 0 or more to
