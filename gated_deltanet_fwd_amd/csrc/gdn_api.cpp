@@ -1571,6 +1571,14 @@ int linear_call(LinearCall* c, const LinearLayout& L, const gdn_linear_problem* 
   return GDN_OK;
 }
 
+// A document's last segment writes a state while its first may still read the one at the other end.
+int check_states_apart(const gdn_linear_problem* p, const float* out, const char* name, const float* in, const char* other) {
+  if (!out || !in) return GDN_OK;
+  const uintptr_t a = (uintptr_t)out, b = (uintptr_t)in, bytes = (uintptr_t)p->n_seqs * p->h_v * p->d * p->d * 4;
+  if (a < b + bytes && b < a + bytes) return fail(GDN_EINVAL, "%s must not overlap %s", name, other);
+  return GDN_OK;
+}
+
 int check_linear_workspace(const LinearLayout& L, const void* workspace, size_t bytes) {
   CHECK(check_ptr(workspace, "workspace"));
   if (bytes < L.total) return fail(GDN_EWORKSPACE, "workspace has %zu bytes, needs %zu", bytes, L.total);
@@ -1605,6 +1613,7 @@ int gdn_linear_fwd(const gdn_linear_problem* p, const void* q, const void* k, co
   if (ht) CHECK(check_ptr(ht, "ht"));
   CHECK(check_tok(o, "o", p->n_tokens));
   CHECK(check_linear_workspace(L, workspace, workspace_bytes));
+  CHECK(check_states_apart(p, ht, "ht", h0, "h0"));
   char* w = (char*)workspace;
   gdn::LinearArgs a = c.base;
   a.a = c.q;
@@ -1648,6 +1657,8 @@ int gdn_linear_bwd(const gdn_linear_problem* p, const void* q, const void* k, co
   CHECK(check_tok(dk, "dk", T));
   CHECK(check_tok(dv, "dv", T));
   CHECK(check_linear_workspace(L, workspace, workspace_bytes));
+  CHECK(check_states_apart(p, dh0, "dh0", h0, "h0"));
+  CHECK(check_states_apart(p, dh0, "dh0", dht, "dht"));
   char* w = (char*)workspace;
   const int dt = p->dtype;
   const gdn::LinearSide d_out = {dO, (int64_t)p->h_v * p->d, 0};
