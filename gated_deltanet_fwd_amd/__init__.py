@@ -790,14 +790,15 @@ def gdn_linear_workspace_bytes(p: LinearProblem, op: int) -> int:
 
 def gdn_linear_fwd(p: LinearProblem, q, k, v, g, cu_seqlens, h0=None, o=None, ht=None, workspace=None, stream=None):
     """Linear attention with decays over packed documents: returns (o, ht or None). q, k and v may be parts
-    of one row (a token's heads contiguous)."""
+    of one row (a token's heads contiguous). What a short call allocates (up to 1 MiB, its workspace included) is one
+    storage, which lives as long as any of it; give the buffers where that matters."""
     return _call("linear_fwd", v, stream, p.at, q, k, v, g, cu_seqlens, h0, o, ht, workspace)
 
 
 def gdn_linear_bwd(p: LinearProblem, q, k, v, g, cu_seqlens, dO, h0=None, dht=None, want_dg: bool = True, grads=None,
                    workspace=None, stream=None) -> Dict[str, torch.Tensor]:
     """Its backward, from the forward's inputs: returns dict dq, dk, dv, dg (None unless wanted), dh0 (None
-    without h0). `grads` may name any of the buffers."""
+    without h0). `grads` may name any of the buffers. Allocations as in gdn_linear_fwd."""
     b = grads or {}
     dq, dk, dv, dg, dh0 = _call("linear_bwd", v, stream, p.at, q, k, v, g, cu_seqlens, h0, dO, dht, bool(want_dg),
                                 b.get("dq"), b.get("dk"), b.get("dv"), b.get("dg"), b.get("dh0"), workspace)
@@ -861,7 +862,7 @@ def gdn_rms_norm_bwd(p: RmsNormProblem, x, dy, weight=None, d_residual=None, gra
                      stream=None) -> Dict[str, torch.Tensor]:
     """Its backward (out "io") at the normalised rows x (with a residual: the forward's residual_out), with the
     gradient of residual_out in d_residual: returns dict dx (of x and residual alike), dweight (None without
-    weight). `grads` may name the buffers."""
+    weight). `grads` may name the buffers. Allocations as in gdn_linear_fwd."""
     b = grads or {}
     dx, dw = _call("norm_bwd", x, stream, p.at, x, dy, weight, d_residual, b.get("dx"), b.get("dweight"), workspace)
     return dict(dx=dx, dweight=dw)
@@ -891,7 +892,8 @@ def gdn_step_maps(p: StepMapsProblem, lengths, contexts, block_table, free_list,
     """What a serving step reads, on the GPU (see gdn.h): returns dict cu_seqlens, positions, token_slots, granted,
     slot_in, slot_out, slot_tok, contexts, free_count. block_table [n_seqs, max_blocks] takes the new blocks in place.
     contexts and free_count move on in place unless contexts_out and free_count_out are given; `outs` may name the
-    other buffers. Outputs of a short call share one storage, as those of gdn_conv_step."""
+    other buffers. Outputs of up to 64 MiB together (4 million tokens) share one storage, which lives as long as any
+    of them: copy what is to be kept beyond the step."""
     b = outs or {}
     r = _call("step_maps", lengths, stream, p.at, lengths, contexts, block_table, free_list, free_count,
               *[b.get(n) for n in STEP_MAPS], contexts if contexts_out is None else contexts_out,

@@ -115,8 +115,9 @@ Tensor empty(at::IntArrayRef shape, at::ScalarType type, const at::Device& dev) 
 
 // A call's tensors that the caller did not give. An allocation and its release take 0.8 us of the
 // host; a decoding step with three outputs took 5.9 us, and 3.3 with the outputs given. So those of a
-// short call are parts of one allocation. One part keeps all of it alive: up to SHARED bytes, which
-// is nothing beside what the allocator rounds up.
+// short call are parts of one allocation, a workspace that the caller did not give among them. One part keeps
+// all of it alive: up to SHARED bytes, which is nothing beside what the allocator rounds up, or up to what the call
+// names instead (step_maps: more, since a step's maps are used and dropped together).
 class Buffers {
  public:
   explicit Buffers(const at::Device& dev, int64_t shared = SHARED) : dev_(dev), shared_(shared) {}

@@ -549,16 +549,19 @@ __global__ __launch_bounds__(256) void k_linear_scan(LinearArgs a, const float* 
 // were, after the first barrier. So each load has at least half a chunk to arrive, and two workgroups share a CU.
 //
 // P and W's operand are rounded once, to the io type: their products are summed in FP32 and the result is
-// rounded to that type itself. With DOTS (the decays' gradient, an FP32 result that is a difference of
+// rounded to that type itself. So o and dv are off by 2.3e-3 where their own rounding alone leaves 1.7e-3; two terms for both
+// would leave that, at 537 us for the forward of the tokens below instead of 470, 1930 for the backward instead of 1870, 91 for
+// 20,001 tokens of 8 heads instead of 80 (f32 rows have none of these roundings). With DOTS (the decays' gradient, an FP32 result that is a difference of
 // sums) both go in as EXACT terms instead. w c goes into W as EXACT terms where W is a result (DOTS, or the state that a
 // document ends with), and as 2 where it is not: that leaves 2^-17 of each term, nothing beside W's own rounding
 // (32,768 tokens, 48 heads, 128 wide, whole forward: one document 490 us, as 3 terms 504; four 495 and 500).
 //
-// Bound by the chain of a chunk's phases: some 130 matrix, 650 vector and 130 LDS instructions a wave in the forward, each
-// kind 4000 to 5000 cycles of a CU with two workgroups, which two waves a SIMD overlap in part: 10,000 cycles. A third
-// fewer matrix instructions in W's sum (above) gain 0 to 3%, a tenth fewer vector instructions 1.5% (the state's decay kept
-// apart from W, which lost bits of ht and dg). The same 32,768 tokens: forward 209 GFLOP of matrix instructions in 330 us,
-// the backward's three 957 GFLOP in 1420 us, at the 1.7 GHz to which the card's power limit brings the clock.
+// Bound by the chain of a chunk's phases: some 130 matrix, 650 vector and 130 LDS instructions a wave in the forward, which two
+// waves a SIMD overlap in small part. Of a SIMD's cycles in the backward's walks matrix instructions take 0.32 and vector
+// instructions, 4 cycles each, up to 0.48 more (0.25 and 0.31 in the forward's, whose last workgroups leave CUs idle), at
+// the 2.1 GHz that the card keeps through them. A third fewer matrix instructions in W's sum (above) gain 0 to 3%, a tenth fewer
+// vector instructions 1.5% (the state's decay kept apart from W, which lost bits of ht and dg). The same 32,768
+// tokens: forward 209 GFLOP of matrix instructions in 340 us, the backward's three 957 GFLOP in 1365 us.
 template <typename T, int D>
 struct WalkLds {
   static constexpr int P = 4 * Tile<T, D>::BYTES, P_TILE = 256;      // P: 10 tiles of 256 values

@@ -403,17 +403,17 @@ int gdn_conv_step(const gdn_conv_step_problem* p, const void* x, const float* we
  * S_0 = h0[n,h] (or 0) and ht[n,h] = S_last as in gdn_fwd. The log decays g are one for each token and
  * head (GDN_DECAY_TOKEN, [T, HV]) or one for each head (GDN_DECAY_HEAD, [HV]). Layouts as at the top of
  * this file (g may start at any of its values); q, k and v may be parts of one row (their strides in the
- * problem). o, ht and the gradients are contiguous and no buffers of the inputs (ht over h0, and dh0 over h0 or dht, are
- * refused). States, decays and sums are FP32
- * (the sums of the log decays 64-bit); for bf16 the decayed products of a chunk and the state that they meet are
- * rounded once to bf16 for o, dv and, without dg, dq and dk, which are rounded to it themselves; of a group's
- * value heads each head's dq and dk are rounded to 11 bits before their sum. ht, dh0 and dg keep FP32's
- * accuracy. All sums have a fixed order: the same call gives the same bits.
+ * problem). o, ht and the gradients are contiguous and no buffers of the inputs (ht over h0, and dh0 over h0 or
+ * dht, are refused). States, decays and sums are FP32 (the sums of the log decays 64-bit); for bf16 the decayed
+ * products of a chunk and the state that they meet are rounded once to bf16 for o, dv and, without dg, dq and dk,
+ * which are rounded to it themselves (2.3e-3 instead of 1.7e-3 off); of a group's value heads each head's dq and dk
+ * are rounded to 11 bits before their sum. ht, dh0 and dg keep FP32's accuracy. With f32 rows nothing is rounded
+ * to fewer bits. All sums have a fixed order: the same call gives the same bits.
  *
  * A document goes in chunks of 64 tokens, and what is not finite in a token reaches, through zeros of
  * masked products, all tokens of its chunk (forward also earlier ones), then what depends on the state;
- * other documents never. A log decay of minus infinity drops the state (as any under -10000), and dg is 0 there (as
- * at any under -104). Log decays may be positive while their sums over a chunk, and over the tokens that a
+ * other documents never. A log decay of minus infinity drops the state (as any under -10000), and dg is 0 there
+ * (as at any under -104). Log decays may be positive while their sums over a chunk, and over the tokens that a
  * state other than zero passes, stay in FP32's range.
  *
  * The launch is planned from the host's lengths; the device's cu_seqlens may hold others (a graph that is
