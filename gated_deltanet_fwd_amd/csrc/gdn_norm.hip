@@ -4,7 +4,7 @@
 //   y = w x' / sqrt(mean(x'^2) + eps),   residual_out = x'
 //   dn = w dy, n = x' / sqrt(..):   dx = (dn - n mean(n dn)) / sqrt(..) + d_residual,   dw = sum over rows of dy n
 //
-// It costs moving the rows once: 32,768 rows of 2048 bf16 values with residual to 8 bits, 472 MB in 84.5 us (5.6 TB/s),
+// It costs moving the rows once: 32,768 rows of 2048 bf16 values with residual to 8 bits, 472 MB in 85 us (5.6 TB/s),
 // backward 537 MB in 104 us (5.2 TB/s; the sum of dw's parts 4.5 of them). LANES lanes take a row, 8 neighbouring
 // values a lane and pass, and keep it in registers between the sum and its use.
 #include <algorithm>
