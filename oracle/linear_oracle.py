@@ -90,7 +90,8 @@ def dg_by_states(cu, q, k, v, g, do, h0=None, dht=None, scale=1.0):
     (T, HV, d), group = v.shape, v.shape[1] // q.shape[1]
     a, head = np.exp(_log_decays(g, T, HV))[..., None, None], np.arange(HV) // group
     q, k = q[:, head], k[:, head]
-    norm = lambda x, n: np.sqrt((x * x).sum(tuple(range(-n, 0))))  # noqa: E731
+    dot = lambda x, y: np.einsum("hi,hi->h", x.reshape(HV, -1), y.reshape(HV, -1))  # noqa: E731 (no BLAS, no temporaries)
+    norm = lambda x: np.sqrt(dot(x, x))  # noqa: E731
     dg, rows, states = np.zeros((T, HV)), np.zeros((T, HV)), np.zeros((T, HV))
     for n in range(len(cu) - 1):
         b, e = cu[n], cu[n + 1]
@@ -103,7 +104,7 @@ def dg_by_states(cu, q, k, v, g, do, h0=None, dht=None, scale=1.0):
         for t in range(e - 1, b - 1, -1):
             D += scale * q[t][:, :, None] * do[t][:, None, :]
             dq, dk = scale * np.einsum("hkv,hv->hk", S[t - b + 1], do[t]), np.einsum("hkv,hv->hk", D, v[t])
-            rows[t] = norm(q[t], 1) * norm(dq, 1) + norm(k[t], 1) * norm(dk, 1)
+            rows[t] = norm(q[t]) * norm(dq) + norm(k[t]) * norm(dk)
             D *= a[t]
-            dg[t], states[t] = (S[t - b] * D).sum((-1, -2)), norm(S[t - b], 2) * norm(D, 2)
+            dg[t], states[t] = dot(S[t - b], D), norm(S[t - b]) * norm(D)
     return (dg.sum(0) if g.ndim == 1 else dg), rows, states
